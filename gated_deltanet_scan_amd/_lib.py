@@ -20,6 +20,10 @@ GDN_FLAG_GATES_ARE_LOGITS = 0x1
 GDN_FLAG_NO_KEY_NORM = 0x2
 GDN_FLAG_REVERSE = 0x4
 GDN_NUM_KERNELS = 9
+GDN_ROTARY_MAX_AXES = 4
+GDN_FLAG_ROTARY_HALVES = 0x1
+GDN_FLAG_ROTARY_INVERSE = 0x2
+GDN_FLAG_ROTARY_POS_F32 = 0x4
 
 STATUS = {0: "GDN_OK", 1: "GDN_ERR_INVALID_ARG", 2: "GDN_ERR_UNSUPPORTED", 3: "GDN_ERR_ALIGNMENT",
           4: "GDN_ERR_ALIAS", 5: "GDN_ERR_WORKSPACE", 6: "GDN_ERR_LAUNCH", 7: "GDN_ERR_NO_DEVICE"}
@@ -29,6 +33,18 @@ class GdnDesc(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("H", ctypes.c_int32), ("F", ctypes.c_int32),
                 ("N", ctypes.c_int32), ("Dk", ctypes.c_int32), ("Dv", ctypes.c_int32),
                 ("io_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32), ("eps", ctypes.c_float)]
+
+
+class GdnNormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("C", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
+                ("w_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class GdnRotaryDesc(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("pos_rows", ctypes.c_int64), ("Hq", ctypes.c_int32),
+                ("Hk", ctypes.c_int32), ("D", ctypes.c_int32), ("n_axes", ctypes.c_int32),
+                ("axis_dim", ctypes.c_int32 * GDN_ROTARY_MAX_AXES), ("io_dtype", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("theta", ctypes.c_double)]
 
 
 class GdnError(RuntimeError):
@@ -93,6 +109,15 @@ def load():
     lib.gdn_frame_scan_fwd_static.restype = ctypes.c_int
     lib.gdn_static_scratch_bytes.argtypes = []
     lib.gdn_static_scratch_bytes.restype = sz
+    np_, rp = ctypes.POINTER(GdnNormDesc), ctypes.POINTER(GdnRotaryDesc)
+    lib.gdn_layer_norm_fwd.argtypes = [np_, vp, vp, vp, vp, fp, fp, vp]
+    lib.gdn_layer_norm_fwd.restype = ctypes.c_int
+    lib.gdn_layer_norm_workspace_size.argtypes = [np_]
+    lib.gdn_layer_norm_workspace_size.restype = sz
+    lib.gdn_layer_norm_bwd.argtypes = [np_, vp, vp, vp, fp, fp, vp, vp, vp, vp, sz, vp]
+    lib.gdn_layer_norm_bwd.restype = ctypes.c_int
+    lib.gdn_rotary.argtypes = [rp, vp, vp, vp, vp, vp, vp]
+    lib.gdn_rotary.restype = ctypes.c_int
     lib.gdn_status_string.argtypes = [ctypes.c_int]
     lib.gdn_status_string.restype = ctypes.c_char_p
     lib.gdn_version.argtypes = []

@@ -490,3 +490,188 @@ def block_out_proj(o, w_out, *, y=None, workspace=None, stream=None):
     if st != 0:
         raise GdnError(st, "gdn_block_out_proj")
     return y
+
+
+def _io(dtype: torch.dtype, what: str) -> int:
+    if dtype == torch.bfloat16:
+        return _lib.GDN_BF16
+    if dtype == torch.float32:
+        return _lib.GDN_F32
+    raise TypeError("%s must be bfloat16 or float32 (got %s)" % (what, dtype))
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError("%s must be on %s (got %s)" % (name, device, t.device))
+
+
+def _workspace(workspace, n: int, device):
+    """The caller's workspace, or one of n bytes from the current stream's allocator."""
+    if workspace is not None or n == 0:
+        return workspace
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _ws_bytes(workspace) -> ctypes.c_size_t:
+    return ctypes.c_size_t(0 if workspace is None else workspace.numel())
+
+
+def _norm_desc(x, weight, bias, eps):
+    C = x.shape[-1] if x.dim() else 0
+    rows = x.numel() // C if C else 0
+    w_dtype = next((t.dtype for t in (weight, bias) if t is not None), torch.float32)
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _check(t, name, w_dtype, (C,))
+    return _lib.GdnNormDesc(rows, C, _io(x.dtype, "x"), _io(w_dtype, "weight"), float(eps))
+
+
+def layer_norm_fwd(x, weight=None, bias=None, *, eps: float = 1e-6, y=None, mean=None, rstd=None,
+                   return_stats: bool = True, stream=None):
+    """Layer norm over the last axis: y = (x - mean) * rstd * weight + bias.
+
+    x: [..., C] bf16 or fp32; weight, bias: [C] in x's dtype or fp32 (both the
+    same), or None.  Returns (y, mean, rstd): y like x, mean and rstd [...]
+    fp32, which layer_norm_bwd reads (None with return_stats=False unless
+    passed in).
+    """
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    _check(x, "x", x.dtype, x.shape)
+    desc = _norm_desc(x, weight, bias, eps)
+    stats = tuple(x.shape[:-1])
+    if y is not None:
+        _check(y, "y", x.dtype, x.shape)
+    if mean is not None:
+        _check(mean, "mean", torch.float32, stats)
+    if rstd is not None:
+        _check(rstd, "rstd", torch.float32, stats)
+    _same_device(x.device, weight=weight, bias=bias, y=y, mean=mean, rstd=rstd)
+    stream = _launch_stream(stream, x.device)
+    with torch.cuda.stream(stream):   # allocations belong to the launch stream
+        if y is None:
+            y = torch.empty_like(x)
+        if mean is None and return_stats:
+            mean = torch.empty(stats, dtype=torch.float32, device=x.device)
+        if rstd is None and return_stats:
+            rstd = torch.empty(stats, dtype=torch.float32, device=x.device)
+        st = _lib.load().gdn_layer_norm_fwd(ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias), _ptr(y),
+                                            _ptr(mean), _ptr(rstd), ctypes.c_void_p(stream.cuda_stream))
+    if st != 0:
+        raise GdnError(st, "gdn_layer_norm_fwd")
+    return y, mean, rstd
+
+
+def layer_norm_bwd(dy, x, mean, rstd, weight=None, bias=None, *, dx=None, dweight=None, dbias=None,
+                   workspace=None, stream=None):
+    """Gradients of layer_norm_fwd.
+
+    dy: the loss gradient of y, like x; mean, rstd: the forward call's; weight
+    and bias as given to it (bias only says that its gradient is wanted).
+    Returns (dx, dweight, dbias): dx like x, the others in the weight's dtype,
+    None where the parameter is None.
+    """
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    _check(x, "x", x.dtype, x.shape)
+    _check(dy, "dy", x.dtype, x.shape)
+    desc = _norm_desc(x, weight, bias, 1.0)   # eps acts through rstd
+    stats = tuple(x.shape[:-1])
+    _check(mean, "mean", torch.float32, stats)
+    _check(rstd, "rstd", torch.float32, stats)
+    if dx is not None:
+        _check(dx, "dx", x.dtype, x.shape)
+    for name, t, p in (("dweight", dweight, weight), ("dbias", dbias, bias)):
+        if t is not None:
+            if p is None:
+                raise ValueError("%s needs its parameter" % name)
+            _check(t, name, p.dtype, p.shape)
+    _check_workspace(workspace, x.device)
+    _same_device(x.device, dy=dy, mean=mean, rstd=rstd, weight=weight, bias=bias, dx=dx, dweight=dweight, dbias=dbias)
+    lib = _lib.load()
+    stream = _launch_stream(stream, x.device)
+    with torch.cuda.stream(stream):   # allocations belong to the launch stream
+        if dx is None:
+            dx = torch.empty_like(x)
+        if dweight is None and weight is not None:
+            dweight = torch.empty_like(weight)
+        if dbias is None and bias is not None:
+            dbias = torch.empty_like(bias)
+        if weight is not None or bias is not None:
+            workspace = _workspace(workspace, int(lib.gdn_layer_norm_workspace_size(ctypes.byref(desc))), x.device)
+        st = lib.gdn_layer_norm_bwd(ctypes.byref(desc), _ptr(dy), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd),
+                                    _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(workspace), _ws_bytes(workspace),
+                                    ctypes.c_void_p(stream.cuda_stream))
+    if st != 0:
+        raise GdnError(st, "gdn_layer_norm_bwd")
+    return dx, dweight, dbias
+
+
+def video_positions(F: int, Hg: int, Wg: int, *, frame_offset: int = 0, device="cuda") -> torch.Tensor:
+    """Positions of a video clip's tokens for rotary(): int32 [F, Hg*Wg, 3]
+    with (frame_offset + frame, row, column) of each token."""
+    axes = [torch.arange(n, dtype=torch.int32, device=device) for n in (F, Hg, Wg)]
+    axes[0] += frame_offset
+    return torch.stack(torch.meshgrid(*axes, indexing="ij"), dim=-1).reshape(F, Hg * Wg, 3).contiguous()
+
+
+def rotary(q, k, pos, *, axes, theta: float = 10000.0, halves: bool = False, inverse: bool = False, q_out=None,
+           k_out=None, stream=None):
+    """Rotary positions over several axes, for queries and keys in one launch.
+
+    q: [..., Hq, D] and k: [..., Hk, D], bf16 or fp32, the same leading (token)
+    shape; k (or q) may be None.  pos: int32 or float32 [..., A], its leading
+    shape the last of q's token axes (a batch shares its positions).  axes: A
+    even numbers, the features each axis turns; features past their sum pass
+    through.  inverse=True turns back (also the gradient).  q_out and k_out may
+    be q and k.  Returns (q_out, k_out).
+    """
+    x = q if q is not None else k
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("q or k must be a torch.Tensor")
+    if x.dim() < 2:
+        raise ValueError("q and k must be [..., H, D]")
+    lead, D = tuple(x.shape[:-2]), x.shape[-1]
+    heads = {}
+    for name, t, out in (("q", q, q_out), ("k", k, k_out)):
+        if t is None:
+            if out is not None:
+                raise ValueError("%s_out without %s" % (name, name))
+            heads[name] = 0
+            continue
+        if t.dim() != x.dim():
+            raise ValueError("q and k must have the same token axes")
+        _check(t, name, x.dtype, lead + (t.shape[-2], D))
+        heads[name] = t.shape[-2]
+        if out is not None:
+            _check(out, name + "_out", t.dtype, t.shape)
+    if not isinstance(pos, torch.Tensor) or pos.dtype not in (torch.int32, torch.float32):
+        raise TypeError("pos must be an int32 or float32 tensor")
+    axes = [int(d) for d in axes]
+    if not 1 <= len(axes) <= _lib.GDN_ROTARY_MAX_AXES:
+        raise ValueError("1 to %d axes are supported (got %d)" % (_lib.GDN_ROTARY_MAX_AXES, len(axes)))
+    n = pos.dim() - 1
+    if n < 0 or n > len(lead):
+        raise ValueError("pos must be [..., %d] over q's last token axes" % len(axes))
+    _check(pos, "pos", pos.dtype, lead[len(lead) - n:] + (len(axes),))
+    _same_device(x.device, q=q, k=k, pos=pos, q_out=q_out, k_out=k_out)
+    tokens = 1
+    for s in lead:
+        tokens *= s
+    flags = ((_lib.GDN_FLAG_ROTARY_HALVES if halves else 0) | (_lib.GDN_FLAG_ROTARY_INVERSE if inverse else 0) |
+             (_lib.GDN_FLAG_ROTARY_POS_F32 if pos.dtype == torch.float32 else 0))
+    dims = (ctypes.c_int32 * _lib.GDN_ROTARY_MAX_AXES)(*axes)
+    desc = _lib.GdnRotaryDesc(tokens, pos.numel() // len(axes), heads["q"], heads["k"], D, len(axes), dims,
+                              _io(x.dtype, "q and k"), flags, float(theta))
+    stream = _launch_stream(stream, x.device)
+    with torch.cuda.stream(stream):   # allocations belong to the launch stream
+        if q is not None and q_out is None:
+            q_out = torch.empty_like(q)
+        if k is not None and k_out is None:
+            k_out = torch.empty_like(k)
+        st = _lib.load().gdn_rotary(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(pos), _ptr(q_out), _ptr(k_out),
+                                    ctypes.c_void_p(stream.cuda_stream))
+    if st != 0:
+        raise GdnError(st, "gdn_rotary")
+    return q_out, k_out

@@ -1,4 +1,5 @@
-"""torch.autograd binding of the frame scan (argument marshalling only).
+"""torch.autograd bindings of the frame scan and of the operators around it
+(argument marshalling only).
 
 ``frame_scan(q, k, v, beta, alpha, S0=None, ...)`` returns (o, S_final) as a
 differentiable function of every tensor input: the forward pass is
@@ -48,3 +49,46 @@ def frame_scan(q, k, v, beta, alpha, S0=None, *, gates_are_logits: bool = False,
     """Differentiable whole-clip scan: (o, S_final) with gradients to q, k, v,
     beta, alpha and S0 (layouts as for api.frame_scan_fwd)."""
     return _FrameScan.apply(q, k, v, beta, alpha, S0, gates_are_logits, eps, normalize_keys, reverse, recompute)
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps):
+        y, mean, rstd = api.layer_norm_fwd(x, weight, bias, eps=eps)
+        ctx.save_for_backward(x, mean, rstd, weight, bias)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, mean, rstd, weight, bias = ctx.saved_tensors
+        dx, dweight, dbias = api.layer_norm_bwd(dy.contiguous(), x, mean, rstd, weight, bias)
+        return dx, dweight, dbias, None
+
+
+def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-6):
+    """Differentiable layer norm over the last axis (layouts as for
+    api.layer_norm_fwd); keeps each row's mean and rstd for the backward pass."""
+    return _LayerNorm.apply(x, weight, bias, eps)
+
+
+class _Rotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, pos, axes, theta, halves, inverse):
+        ctx.save_for_backward(pos)
+        ctx.kw = dict(axes=axes, theta=theta, halves=halves, inverse=not inverse)
+        return api.rotary(q, k, pos, axes=axes, theta=theta, halves=halves, inverse=inverse)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        pos, = ctx.saved_tensors
+        dq = None if dq is None else dq.contiguous()
+        dk = None if dk is None else dk.contiguous()
+        if dq is not None or dk is not None:
+            dq, dk = api.rotary(dq, dk, pos, **ctx.kw)
+        return dq, dk, None, None, None, None, None
+
+
+def rotary(q, k, pos, *, axes, theta: float = 10000.0, halves: bool = False, inverse: bool = False):
+    """Differentiable rotary positions (layouts as for api.rotary); the gradient
+    is the rotation turned back."""
+    return _Rotary.apply(q, k, pos, tuple(axes), theta, halves, inverse)

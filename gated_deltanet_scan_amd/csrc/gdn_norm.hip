@@ -1,0 +1,549 @@
+// Layer norm, forward and backward: the C ABI of gdn_layer_norm_fwd /
+// gdn_layer_norm_bwd (declared in include/gdn.h).
+//
+//     mu = <x>,  r = (<(x - mu)^2> + eps)^(-1/2),  h = (x - mu) r,  y = h w + b
+//     g = dy w,  dx = r (g - <g> - h <g h>),  dw = sum_rows dy h,  db = sum_rows dy
+//
+// Both passes are bound by memory: the forward reads x and writes y, the
+// backward reads x and dy and writes dx.  A row stays in registers between its
+// statistics and its result, so nothing is read twice; the variance is a second
+// sum over the registers, about the mean (no cancellation of <x^2> - mu^2).
+// One wave holds a row of up to 4096 elements, so rows of the usual widths need
+// no barrier at all; four waves share a row of up to 16384, and wider rows are
+// read again from memory (norm_wide_*).
+#include "gdn_ops.hpp"
+
+#include <algorithm>
+
+namespace {
+
+using namespace gdnops;
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kMaxPartials = 1024;   // workgroups of the backward pass (partial sums of dw and db)
+
+struct NormArgs {
+    const void* x;
+    const void* dy;
+    const void* w;
+    const void* b;
+    void* y;                         // y or dx
+    float* mean;
+    float* rstd;
+    float* part;                     // [groups][2][C] partial sums of dw and db
+    int64_t rows;
+    int C;
+    float eps, inv_c;
+};
+
+// Sum over the WPR waves of a row.  With WPR = 1 the wave's own sum; with four
+// the waves add through LDS (two buffers, so one barrier a sum is enough).
+template <int WPR>
+__device__ __forceinline__ float row_sum(float x, float (*red)[kWaves], int& phase) {
+    x = wave_sum(x);
+    if constexpr (WPR > 1) {
+        if ((threadIdx.x & 63) == 0) red[phase][threadIdx.x >> 6] = x;
+        __syncthreads();
+        x = (red[phase][0] + red[phase][1]) + (red[phase][2] + red[phase][3]);
+        phase ^= 1;
+    }
+    return x;
+}
+
+template <int WPR>
+__device__ __forceinline__ void row_sum2(float& x, float& y, float (*red)[2 * kWaves], int& phase) {
+    x = wave_sum(x);
+    y = wave_sum(y);
+    if constexpr (WPR > 1) {
+        if ((threadIdx.x & 63) == 0) {
+            red[phase][threadIdx.x >> 6] = x;
+            red[phase][kWaves + (threadIdx.x >> 6)] = y;
+        }
+        __syncthreads();
+        x = (red[phase][0] + red[phase][1]) + (red[phase][2] + red[phase][3]);
+        y = (red[phase][4] + red[phase][5]) + (red[phase][6] + red[phase][7]);
+        phase ^= 1;
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void load_chunk(Vec8<T>& v, const T* row, int c, int C) {
+    if (c + 8 <= C)
+        v.load(row + c);
+    else if (c < C)
+        v.load_tail(row + c, C - c);
+    else
+        v.zero();
+}
+template <typename T>
+__device__ __forceinline__ void store_chunk(const Vec8<T>& v, T* row, int c, int C) {
+    if (c + 8 <= C)
+        v.store(row + c);
+    else if (c < C)
+        v.store_tail(row + c, C - c);
+}
+
+// Rows of up to 512 * NV * WPR elements; lane t of a row holds the chunks of
+// eight at 8 (t + 64 WPR i), i < NV.  Workgroups walk the rows with the
+// weights in registers and the next row's loads in flight.
+template <typename T, typename W, int NV, int WPR>
+__global__ __launch_bounds__(kThreads) void norm_fwd_kernel(const NormArgs a) {
+    __shared__ float red[2][kWaves], red2[2][2 * kWaves];
+    constexpr int RPB = kWaves / WPR;                    // rows per workgroup and step
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int t = WPR == 1 ? (tid & 63) : tid;
+    const int C = a.C;
+    int phase = 0, phase2 = 0;
+    Vec8<W> w[NV], b[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = 8 * (t + 64 * WPR * i);
+        if (a.w) load_chunk(w[i], static_cast<const W*>(a.w), c, C);
+        if (a.b) load_chunk(b[i], static_cast<const W*>(a.b), c, C);
+    }
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    int64_t row = (int64_t)blockIdx.x * RPB + (WPR == 1 ? wave : 0);
+    Vec8<T> nxt[NV];
+    if (row < a.rows) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            load_chunk(nxt[i], static_cast<const T*>(a.x) + row * C, 8 * (t + 64 * WPR * i), C);
+    }
+    for (; row < a.rows; row += step) {
+        Vec8<T> x[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) x[i] = nxt[i];
+        if (row + step < a.rows) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                load_chunk(nxt[i], static_cast<const T*>(a.x) + (row + step) * C, 8 * (t + 64 * WPR * i), C);
+        }
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s += x[i].get(j);            // zeros past C
+        float mu = row_sum<WPR>(s, red, phase) / (float)C;   // divided: rounded once, everywhere the same
+        // spread about the rounded mean, and what that mean is off by: its
+        // correction makes rows of a large mean exact to their own rounding
+        float q = 0.f, e = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float d = 8 * (t + 64 * WPR * i) + j < C ? x[i].get(j) - mu : 0.f;
+                q += d * d;
+                e += d;
+            }
+        row_sum2<WPR>(q, e, red2, phase2);
+        e /= (float)C;
+        mu += e;
+        const float r = 1.0f / sqrtf(fmaxf(q * a.inv_c - e * e, 0.f) + a.eps);
+        T* yr = static_cast<T*>(a.y) + row * C;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float h = (x[i].get(j) - mu) * r;
+                f[j] = h * (a.w ? w[i].get(j) : 1.f) + (a.b ? b[i].get(j) : 0.f);
+            }
+            Vec8<T> y;
+            y.set(f);
+            store_chunk(y, yr, 8 * (t + 64 * WPR * i), C);
+        }
+        if (t == 0) {
+            if (a.mean) a.mean[row] = mu;
+            if (a.rstd) a.rstd[row] = r;
+        }
+    }
+}
+
+// The same layout for the backward pass.  Every lane adds dy h and dy of its
+// columns over the workgroup's rows in fp32 registers; at the end the
+// workgroup adds its waves' sums in order through LDS and writes one row of
+// partial sums, which norm_colsum_kernel adds up (no atomics).
+template <typename T, typename W, int NV, int WPR>
+__global__ __launch_bounds__(kThreads) void norm_bwd_kernel(const NormArgs a) {
+    __shared__ float red[2][2 * kWaves];
+    __shared__ float cols[WPR == 1 ? kWaves * 64 * 8 : 1];
+    constexpr int RPB = kWaves / WPR;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int t = WPR == 1 ? (tid & 63) : tid;
+    const int C = a.C;
+    int phase = 0;
+    Vec8<W> w[NV];
+    float dw[NV][8], db[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (a.w) load_chunk(w[i], static_cast<const W*>(a.w), 8 * (t + 64 * WPR * i), C);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[i][j] = db[i][j] = 0.f;
+    }
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    int64_t row = (int64_t)blockIdx.x * RPB + (WPR == 1 ? wave : 0);
+    Vec8<T> nx[NV], ny[NV];
+    float nmu = 0.f, nr = 0.f;
+    auto fetch = [&](int64_t rw) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            load_chunk(nx[i], static_cast<const T*>(a.x) + rw * C, 8 * (t + 64 * WPR * i), C);
+            load_chunk(ny[i], static_cast<const T*>(a.dy) + rw * C, 8 * (t + 64 * WPR * i), C);
+        }
+        nmu = a.mean[rw];
+        nr = a.rstd[rw];
+    };
+    if (row < a.rows) fetch(row);
+    for (; row < a.rows; row += step) {
+        Vec8<T> x[NV], dy[NV];
+        const float mu = nmu, r = nr;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            x[i] = nx[i];
+            dy[i] = ny[i];
+        }
+        if (row + step < a.rows) fetch(row + step);
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float d = dy[i].get(j), h = (x[i].get(j) - mu) * r;   // d is zero past C
+                const float g = a.w ? d * w[i].get(j) : d;
+                s1 += g;
+                s2 += g * h;
+                dw[i][j] += d * h;
+                db[i][j] += d;
+            }
+        row_sum2<WPR>(s1, s2, red, phase);
+        s1 *= a.inv_c;
+        s2 *= a.inv_c;
+        T* dxr = static_cast<T*>(a.y) + row * C;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float d = dy[i].get(j), h = (x[i].get(j) - mu) * r;
+                const float g = a.w ? d * w[i].get(j) : d;
+                f[j] = r * ((g - s1) - h * s2);
+            }
+            Vec8<T> v;
+            v.set(f);
+            store_chunk(v, dxr, 8 * (t + 64 * WPR * i), C);
+        }
+    }
+    if (!a.part) return;
+    float* pw = a.part + (size_t)blockIdx.x * 2 * C;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float* v = k ? db[i] : dw[i];
+            if constexpr (WPR == 1) {
+                // the four waves hold the same columns: add them in order
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) cols[(wave * 8 + j) * 64 + t] = v[j];
+                __syncthreads();
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int n = tid + 256 * e, j = n >> 6, l = n & 63;     // column 8 (l + 64 i) + j
+                    const int c = 8 * (l + 64 * i) + j;
+                    const float s = (cols[j * 64 + l] + cols[(8 + j) * 64 + l]) +
+                                    (cols[(16 + j) * 64 + l] + cols[(24 + j) * 64 + l]);
+                    if (c < C) pw[(size_t)k * C + c] = s;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int c = 8 * (t + 64 * WPR * i) + j;
+                    if (c < C) pw[(size_t)k * C + c] = v[j];
+                }
+            }
+        }
+}
+
+// Rows wider than a workgroup's registers: one workgroup a row, which reads it
+// three times (statistics, spread, result; the later reads hit the L2).
+template <typename T, typename W>
+__global__ __launch_bounds__(kThreads) void norm_wide_fwd_kernel(const NormArgs a) {
+    __shared__ float red[2][kWaves], red2[2][2 * kWaves];
+    int phase = 0, phase2 = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const T* x = static_cast<const T*>(a.x) + row * a.C;
+        T* y = static_cast<T*>(a.y) + row * a.C;
+        float s = 0.f, q = 0.f, e = 0.f;
+        for (int c = threadIdx.x; c < a.C; c += kThreads) s += to_f<T>(x[c]);
+        float mu = row_sum<4>(s, red, phase) / (float)a.C;
+        for (int c = threadIdx.x; c < a.C; c += kThreads) {
+            const float d = to_f<T>(x[c]) - mu;
+            q += d * d;
+            e += d;
+        }
+        row_sum2<4>(q, e, red2, phase2);
+        e /= (float)a.C;
+        mu += e;
+        const float r = 1.0f / sqrtf(fmaxf(q * a.inv_c - e * e, 0.f) + a.eps);
+        for (int c = threadIdx.x; c < a.C; c += kThreads) {
+            const float h = (to_f<T>(x[c]) - mu) * r;
+            const float w = a.w ? to_f<W>(static_cast<const W*>(a.w)[c]) : 1.f;
+            const float b = a.b ? to_f<W>(static_cast<const W*>(a.b)[c]) : 0.f;
+            y[c] = from_f<T>(h * w + b);
+        }
+        if (threadIdx.x == 0) {
+            if (a.mean) a.mean[row] = mu;
+            if (a.rstd) a.rstd[row] = r;
+        }
+    }
+}
+template <typename T, typename W>
+__global__ __launch_bounds__(kThreads) void norm_wide_dx_kernel(const NormArgs a) {
+    __shared__ float red[2][2 * kWaves];
+    int phase = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const T* x = static_cast<const T*>(a.x) + row * a.C;
+        const T* dy = static_cast<const T*>(a.dy) + row * a.C;
+        T* dx = static_cast<T*>(a.y) + row * a.C;
+        const float mu = a.mean[row], r = a.rstd[row];
+        float s1 = 0.f, s2 = 0.f;
+        auto at = [&](int c, float& h) {
+            h = (to_f<T>(x[c]) - mu) * r;
+            return to_f<T>(dy[c]) * (a.w ? to_f<W>(static_cast<const W*>(a.w)[c]) : 1.f);
+        };
+        for (int c = threadIdx.x; c < a.C; c += kThreads) {
+            float h;
+            const float g = at(c, h);
+            s1 += g;
+            s2 += g * h;
+        }
+        row_sum2<4>(s1, s2, red, phase);
+        s1 *= a.inv_c;
+        s2 *= a.inv_c;
+        for (int c = threadIdx.x; c < a.C; c += kThreads) {
+            float h;
+            const float g = at(c, h);
+            dx[c] = from_f<T>(r * ((g - s1) - h * s2));
+        }
+    }
+}
+// dw and db of wide rows: one thread a column, workgroup y takes every
+// gridDim.y-th row.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void norm_wide_dw_kernel(const NormArgs a) {
+    const int c = blockIdx.x * kThreads + threadIdx.x;
+    if (c >= a.C) return;
+    float dw = 0.f, db = 0.f;
+    for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
+        const float d = to_f<T>(static_cast<const T*>(a.dy)[row * a.C + c]);
+        dw += d * ((to_f<T>(static_cast<const T*>(a.x)[row * a.C + c]) - a.mean[row]) * a.rstd[row]);
+        db += d;
+    }
+    float* pw = a.part + (size_t)blockIdx.y * 2 * a.C;
+    pw[c] = dw;
+    pw[a.C + c] = db;
+}
+
+// dw[c] = sum over the groups' partial rows, 64 columns a workgroup; the four
+// waves take every fourth row and add up through LDS in order.
+template <typename W>
+__global__ __launch_bounds__(kThreads) void norm_colsum_kernel(const float* __restrict__ part, int groups, int C,
+                                                               W* __restrict__ dw, W* __restrict__ db) {
+    __shared__ float red[kWaves][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int n = blockIdx.x * 64 + lane;                // columns of [2][C]
+    float s = 0.f;
+    if (n < 2 * C) {
+        int p = wave;
+        float u0 = 0.f, u1 = 0.f, u2 = 0.f, u3 = 0.f;
+        for (; p + 12 < groups; p += 16) {
+            u0 += part[(size_t)p * 2 * C + n];
+            u1 += part[(size_t)(p + 4) * 2 * C + n];
+            u2 += part[(size_t)(p + 8) * 2 * C + n];
+            u3 += part[(size_t)(p + 12) * 2 * C + n];
+        }
+        for (; p < groups; p += 4) u0 += part[(size_t)p * 2 * C + n];
+        s = (u0 + u1) + (u2 + u3);
+    }
+    red[wave][lane] = s;
+    __syncthreads();
+    if (wave == 0 && n < 2 * C) {
+        s = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+        if (n < C) {
+            if (dw) dw[n] = from_f<W>(s);
+        } else if (db) {
+            db[n - C] = from_f<W>(s);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- launch
+gdn_status check_norm(const gdn_norm_desc* d) {
+    if (!d || d->rows < 0 || d->C < 1) return GDN_ERR_INVALID_ARG;
+    if (!(d->eps > 0.0f) || !(d->eps < 1e30f)) return GDN_ERR_INVALID_ARG;
+    if (d->io_dtype != GDN_BF16 && d->io_dtype != GDN_F32) return GDN_ERR_INVALID_ARG;
+    if (d->w_dtype != GDN_F32 && d->w_dtype != d->io_dtype) return GDN_ERR_INVALID_ARG;
+    if (d->C > (1 << 20)) return GDN_ERR_UNSUPPORTED;
+    return GDN_OK;
+}
+int elem(int dt) { return dt == GDN_BF16 ? 2 : 4; }
+
+// Waves a row and chunks a lane: the smallest that hold the row.
+bool shape_of(int C, int* nv, int* wpr) {
+    for (int w = 1; w <= 4; w *= 4)
+        for (int v = 1; v <= 8; v *= 2)
+            if (C <= 512 * v * w) {
+                *nv = v;
+                *wpr = w;
+                return true;
+            }
+    return false;
+}
+// Workgroups of the backward pass: enough to fill the card (four a compute
+// unit), and no more than leaves each wave a few rows, since every workgroup
+// writes a row of partial sums that is read back (64 MiB of them at most, or 16
+// rows).
+int bwd_groups(const gdn_norm_desc* d) {
+    int nv = 0, wpr = 4;
+    shape_of(d->C, &nv, &wpr);
+    const int64_t rpb = kWaves / wpr;
+    const int64_t g = (d->rows + 4 * rpb - 1) / (4 * rpb);
+    const int64_t most = std::min<int64_t>(kMaxPartials, std::max<int64_t>(16, ((int64_t)64 << 20) / (8 * (int64_t)d->C)));
+    return (int)std::min(std::max<int64_t>(g, 1), most);
+}
+
+template <typename T, typename W>
+gdn_status launch_fwd(const NormArgs& a, int cus, hipStream_t s) {
+    int nv, wpr;
+    if (!shape_of(a.C, &nv, &wpr)) {
+        const int64_t grid = std::min<int64_t>(a.rows, (int64_t)cus * 8);
+        hipLaunchKernelGGL((norm_wide_fwd_kernel<T, W>), dim3((unsigned)grid), dim3(kThreads), 0, s, a);
+        return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+    }
+    const int rpb = kWaves / wpr;
+    const dim3 grid((unsigned)std::min<int64_t>((a.rows + rpb - 1) / rpb, (int64_t)cus * 4));
+#define GDN_NORM(NV, WPR) hipLaunchKernelGGL((norm_fwd_kernel<T, W, NV, WPR>), grid, dim3(kThreads), 0, s, a)
+    if (wpr == 1) {
+        if (nv == 1) GDN_NORM(1, 1);
+        if (nv == 2) GDN_NORM(2, 1);
+        if (nv == 4) GDN_NORM(4, 1);
+        if (nv == 8) GDN_NORM(8, 1);
+    } else {
+        if (nv == 4) GDN_NORM(4, 4);
+        if (nv == 8) GDN_NORM(8, 4);
+    }
+#undef GDN_NORM
+    return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
+template <typename T, typename W>
+gdn_status launch_bwd(const NormArgs& a, int groups, void* dw, void* db, int cus, hipStream_t s) {
+    int nv, wpr;
+    if (a.rows > 0) {
+        if (!shape_of(a.C, &nv, &wpr)) {
+            const int64_t grid = std::min<int64_t>(a.rows, (int64_t)cus * 8);
+            hipLaunchKernelGGL((norm_wide_dx_kernel<T, W>), dim3((unsigned)grid), dim3(kThreads), 0, s, a);
+            if (a.part)
+                hipLaunchKernelGGL(norm_wide_dw_kernel<T>, dim3((a.C + kThreads - 1) / kThreads, groups),
+                                   dim3(kThreads), 0, s, a);
+        } else {
+            const dim3 grid(groups);
+#define GDN_NORM(NV, WPR) hipLaunchKernelGGL((norm_bwd_kernel<T, W, NV, WPR>), grid, dim3(kThreads), 0, s, a)
+            if (wpr == 1) {
+                if (nv == 1) GDN_NORM(1, 1);
+                if (nv == 2) GDN_NORM(2, 1);
+                if (nv == 4) GDN_NORM(4, 1);
+                if (nv == 8) GDN_NORM(8, 1);
+            } else {
+                if (nv == 4) GDN_NORM(4, 4);
+                if (nv == 8) GDN_NORM(8, 4);
+            }
+#undef GDN_NORM
+        }
+        if (hipGetLastError() != hipSuccess) return GDN_ERR_LAUNCH;
+    }
+    if (dw || db) {
+        hipLaunchKernelGGL(norm_colsum_kernel<W>, dim3((2 * a.C + 63) / 64), dim3(kThreads), 0, s, a.part,
+                           a.rows > 0 ? groups : 0, a.C, static_cast<W*>(dw), static_cast<W*>(db));
+        if (hipGetLastError() != hipSuccess) return GDN_ERR_LAUNCH;
+    }
+    return GDN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+gdn_status gdn_layer_norm_fwd(const gdn_norm_desc* d, const void* x, const void* weight, const void* bias, void* y,
+                              float* mean, float* rstd, void* stream) {
+    gdn_status st = check_norm(d);
+    if (st != GDN_OK) return st;
+    if (d->rows == 0) return GDN_OK;
+    if (!x || !y) return GDN_ERR_INVALID_ARG;
+    const int e = elem(d->io_dtype), we = elem(d->w_dtype);
+    if (!aligned(x, e) || !aligned(y, e) || !aligned(weight, we) || !aligned(bias, we) || !aligned(mean, 4) ||
+        !aligned(rstd, 4))
+        return GDN_ERR_ALIGNMENT;
+    const size_t nb = (size_t)d->rows * d->C * e, wb = (size_t)d->C * we, sb = (size_t)d->rows * 4;
+    const Range ins[] = {rng(x, nb), rng(weight, wb), rng(bias, wb)};
+    const Range outs[] = {rng(y, nb), rng(mean, sb), rng(rstd, sb)};
+    for (int i = 0; i < 3; ++i) {
+        for (const Range& r : ins)
+            if (overlap(outs[i], r)) return GDN_ERR_ALIAS;
+        for (int j = i + 1; j < 3; ++j)
+            if (overlap(outs[i], outs[j])) return GDN_ERR_ALIAS;
+    }
+    int cus;
+    if ((st = check_device(&cus)) != GDN_OK) return st;
+    NormArgs a = {};
+    a.x = x, a.w = weight, a.b = bias, a.y = y, a.mean = mean, a.rstd = rstd;
+    a.rows = d->rows, a.C = d->C, a.eps = d->eps, a.inv_c = 1.0f / (float)d->C;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if (d->io_dtype == GDN_F32) return launch_fwd<float, float>(a, cus, s);
+    return d->w_dtype == GDN_F32 ? launch_fwd<uint16_t, float>(a, cus, s) : launch_fwd<uint16_t, uint16_t>(a, cus, s);
+}
+
+size_t gdn_layer_norm_workspace_size(const gdn_norm_desc* d) {
+    if (check_norm(d) != GDN_OK || d->rows == 0) return 0;
+    return round256((size_t)bwd_groups(d) * 2 * d->C * sizeof(float));
+}
+
+gdn_status gdn_layer_norm_bwd(const gdn_norm_desc* d, const void* dy, const void* x, const void* weight,
+                              const float* mean, const float* rstd, void* dx, void* dweight, void* dbias,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+    gdn_status st = check_norm(d);
+    if (st != GDN_OK) return st;
+    const bool sums = dweight || dbias;
+    if (d->rows > 0 && (!dy || !x || !mean || !rstd || !dx)) return GDN_ERR_INVALID_ARG;
+    const int e = elem(d->io_dtype), we = elem(d->w_dtype);
+    if (!aligned(dy, e) || !aligned(x, e) || !aligned(dx, e) || !aligned(weight, we) || !aligned(dweight, we) ||
+        !aligned(dbias, we) || !aligned(mean, 4) || !aligned(rstd, 4))
+        return GDN_ERR_ALIGNMENT;
+    const size_t need = sums ? gdn_layer_norm_workspace_size(d) : 0;
+    if (need && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
+    if (need && !aligned(workspace, 256)) return GDN_ERR_ALIGNMENT;
+    const size_t nb = (size_t)d->rows * d->C * e, wb = (size_t)d->C * we, sb = (size_t)d->rows * 4;
+    const Range ins[] = {rng(dy, nb), rng(x, nb), rng(weight, wb), rng(mean, sb), rng(rstd, sb)};
+    const Range outs[] = {rng(dx, nb), rng(dweight, wb), rng(dbias, wb), rng(need ? workspace : nullptr, need)};
+    for (int i = 0; i < 4; ++i) {
+        for (const Range& r : ins)
+            if (overlap(outs[i], r)) return GDN_ERR_ALIAS;
+        for (int j = i + 1; j < 4; ++j)
+            if (overlap(outs[i], outs[j])) return GDN_ERR_ALIAS;
+    }
+    if (d->rows == 0 && !sums) return GDN_OK;
+    int cus;
+    if ((st = check_device(&cus)) != GDN_OK) return st;
+    NormArgs a = {};
+    a.x = x, a.dy = dy, a.w = weight, a.y = dx, a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd);
+    a.part = need ? static_cast<float*>(workspace) : nullptr;
+    a.rows = d->rows, a.C = d->C, a.eps = d->eps, a.inv_c = 1.0f / (float)d->C;
+    const int groups = d->rows > 0 ? bwd_groups(d) : 0;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if (d->io_dtype == GDN_F32) return launch_bwd<float, float>(a, groups, dweight, dbias, cus, s);
+    return d->w_dtype == GDN_F32 ? launch_bwd<uint16_t, float>(a, groups, dweight, dbias, cus, s)
+                                 : launch_bwd<uint16_t, uint16_t>(a, groups, dweight, dbias, cus, s);
+}
+
+}  // extern "C"

@@ -350,6 +350,81 @@ gdn_status gdn_block_out_proj(const gdn_desc* d, int32_t C,
                               void* workspace, size_t workspace_bytes,
                               void* stream);
 
+/* ----------------------------------------------------------------- layer norm
+ * The norm in front of a block's projections (gdn_block_in_proj), forward and
+ * backward, for serving and training.  For every row x of C values
+ *     mean = <x>,  rstd = (<(x - mean)^2> + eps)^(-1/2)
+ *     h = (x - mean) rstd,     y = h weight + bias
+ * x, y [rows][C] in io_dtype (GDN_BF16 or GDN_F32); weight and bias [C] in
+ * w_dtype (the io dtype or GDN_F32), either may be NULL (1 and 0: the norm of a
+ * block that modulates its activations itself); mean and rstd [rows] float32,
+ * written where not NULL.  Sums are float32; outputs round once.
+ *
+ * gdn_layer_norm_bwd takes dy = dL/dy, the forward's x and weight and the mean
+ * and rstd it wrote, and writes
+ *     dx = rstd (g - <g> - h <g h>),   g = dy weight            io dtype
+ *     dweight = sum over rows of dy h,  dbias = sum of dy        w dtype
+ * dweight and dbias may be NULL (not computed); both NULL needs no workspace.
+ * rows == 0 gives dweight = dbias = 0.  The sums over rows add fp32 partial
+ * sums in a fixed order, so results are bitwise reproducible.
+ *
+ * rows >= 0, 1 <= C <= 2^20, eps finite and > 0.  Rows are contiguous; pointers
+ * need only their element's alignment (workspace: 256 bytes).  Outputs are
+ * disjoint from the inputs, from each other and from the workspace. */
+typedef struct gdn_norm_desc {
+    int64_t rows;               /* tokens                                */
+    int32_t C;                  /* width                                 */
+    int32_t io_dtype, w_dtype;  /* gdn_dtype of x, y, dy, dx; of weight, bias and their gradients */
+    float eps;
+} gdn_norm_desc;
+
+gdn_status gdn_layer_norm_fwd(const gdn_norm_desc* d, const void* x, const void* weight, const void* bias,
+                              void* y, float* mean, float* rstd, void* stream);
+size_t gdn_layer_norm_workspace_size(const gdn_norm_desc* d);
+gdn_status gdn_layer_norm_bwd(const gdn_norm_desc* d, const void* dy, const void* x, const void* weight,
+                              const float* mean, const float* rstd,
+                              void* dx, void* dweight, void* dbias,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* ----------------------------------------------------------- rotary positions
+ * Rotary positions over several axes (time, height and width of a video token)
+ * for queries and keys, between gdn_block_in_proj and the scan or the
+ * attention.  Of each head's D features the first R = sum of axis_dim are
+ * rotated in R/2 pairs, the rest pass through unchanged.  The pairs are dealt
+ * to the axes in order, axis_dim[a]/2 each; the i-th pair of axis a turns by
+ *     angle = pos[token][a] * theta^(-2i / axis_dim[a])
+ *     (x, y) -> (x cos - y sin, x sin + y cos).
+ * Pair j holds features (2j, 2j+1), or with GDN_FLAG_ROTARY_HALVES features
+ * (j, j + R/2).  GDN_FLAG_ROTARY_INVERSE turns back, which is also the
+ * gradient: dq = the inverse rotation of dq_out.
+ *
+ * q, q_out [tokens][Hq][D] and k, k_out [tokens][Hk][D] in io_dtype (GDN_BF16
+ * or GDN_F32); Hq or Hk may be 0 (its pointers are then unused).  pos
+ * [pos_rows][n_axes], int32 or (GDN_FLAG_ROTARY_POS_F32) float32; token t takes
+ * row t % pos_rows, so that a batch shares its positions.  Angles are formed
+ * and reduced to one turn in 64 bits, the rotation is float32, outputs round
+ * once.  q_out may be q and k_out may be k; any other overlap of an output is
+ * refused.
+ *
+ * 1 to 4 axes of even dimension >= 0 with 0 < R <= D, theta finite and > 0
+ * (GDN_ERR_INVALID_ARG); D a multiple of 8, at most 256 (GDN_ERR_UNSUPPORTED).
+ * q, k and outputs are 16-byte aligned, pos 4-byte. */
+#define GDN_ROTARY_MAX_AXES 4
+#define GDN_FLAG_ROTARY_HALVES 0x1u
+#define GDN_FLAG_ROTARY_INVERSE 0x2u
+#define GDN_FLAG_ROTARY_POS_F32 0x4u
+typedef struct gdn_rotary_desc {
+    int64_t tokens, pos_rows;
+    int32_t Hq, Hk, D;
+    int32_t n_axes, axis_dim[GDN_ROTARY_MAX_AXES];
+    int32_t io_dtype;
+    uint32_t flags;             /* GDN_FLAG_ROTARY_* */
+    double theta;
+} gdn_rotary_desc;
+
+gdn_status gdn_rotary(const gdn_rotary_desc* d, const void* q, const void* k, const void* pos,
+                      void* q_out, void* k_out, void* stream);
+
 /* Human-readable name of a status code (static storage). */
 const char* gdn_status_string(gdn_status s);
 

@@ -1,0 +1,128 @@
+"""The C ABI of the operators around the scan, on the host: bad calls are
+rejected with the documented status before any launch.  The fake addresses are
+never dereferenced.
+"""
+import ctypes
+import os
+
+import pytest
+import torch
+
+from gated_deltanet_scan_amd import _lib, api
+
+OK, INVALID, UNSUPPORTED, ALIGN, ALIAS, WORKSPACE = 0, 1, 2, 3, 4, 5
+BF16, F32 = _lib.GDN_BF16, _lib.GDN_F32
+BASE = 0x7f0000000000
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(_lib.LIB_PATH):
+        from gated_deltanet_scan_amd import build
+        build.build()
+    return _lib.load()
+
+
+def addresses(names):
+    return {n: BASE + i * (1 << 36) for i, n in enumerate(names)}
+
+
+# ------------------------------------------------------------------ layer norm
+def norm(rows=4, C=64, io=BF16, w=BF16, eps=1e-6):
+    return _lib.GdnNormDesc(rows, C, io, w, eps)
+
+
+NF = ["x", "w", "b", "y", "mean", "rstd"]
+NB = ["dy", "x", "w", "mean", "rstd", "dx", "dw", "db", "ws"]
+
+
+def norm_fwd(lib, d, **over):
+    p = dict(addresses(NF), **over)
+    return lib.gdn_layer_norm_fwd(None if d is None else ctypes.byref(d), *[p[n] for n in NF], None)
+
+
+def norm_bwd(lib, d, ws_bytes=1 << 35, **over):
+    p = dict(addresses(NB), **over)
+    return lib.gdn_layer_norm_bwd(None if d is None else ctypes.byref(d), *[p[n] for n in NB], ws_bytes, None)
+
+
+@pytest.mark.parametrize("d,expect", [
+    (None, INVALID), (norm(rows=-1), INVALID), (norm(C=0), INVALID), (norm(eps=0.0), INVALID),
+    (norm(eps=float("nan")), INVALID), (norm(eps=float("inf")), INVALID), (norm(io=_lib.GDN_FP8_E4M3), INVALID),
+    (norm(io=F32, w=BF16), INVALID), (norm(C=(1 << 20) + 1), UNSUPPORTED),
+])
+def test_norm_descriptor(lib, d, expect):
+    assert norm_fwd(lib, d) == expect and norm_bwd(lib, d) == expect
+
+
+def test_norm_pointers(lib):
+    d, a, b = norm(), addresses(NF), addresses(NB)
+    assert norm_fwd(lib, d, x=None) == INVALID and norm_fwd(lib, d, y=None) == INVALID
+    for n in ("dy", "x", "mean", "rstd", "dx"):
+        assert norm_bwd(lib, d, **{n: None}) == INVALID, n
+    assert norm_fwd(lib, d, x=a["x"] + 1) == ALIGN and norm_fwd(lib, d, mean=a["mean"] + 2) == ALIGN
+    assert norm_fwd(lib, norm(w=F32), w=a["w"] + 2) == ALIGN
+    assert norm_bwd(lib, d, dw=b["dw"] + 1) == ALIGN and norm_bwd(lib, d, ws=b["ws"] + 16) == ALIGN
+    assert norm_fwd(lib, d, y=a["x"]) == ALIAS and norm_fwd(lib, d, rstd=a["mean"] + 12) == ALIAS
+    assert norm_bwd(lib, d, dx=b["dy"]) == ALIAS and norm_bwd(lib, d, dw=b["ws"] + 256) == ALIAS
+    need = lib.gdn_layer_norm_workspace_size(ctypes.byref(d))
+    assert need == 2 * 64 * 4                                     # one row of partial sums for a few rows
+    assert norm_bwd(lib, d, ws_bytes=need - 1) == WORKSPACE and norm_bwd(lib, d, ws=None) == WORKSPACE
+    assert lib.gdn_layer_norm_workspace_size(ctypes.byref(norm(rows=0))) == 0
+    assert norm_fwd(lib, norm(rows=0), x=None, y=None) == OK
+    assert norm_bwd(lib, norm(rows=0), **{n: None for n in NB}) == OK
+
+
+# ------------------------------------------------------------------ rotary
+def rot(tokens=6, pos_rows=6, Hq=2, Hk=2, D=64, axes=(16, 24, 24), io=BF16, flags=0, theta=1e4, n=None):
+    dims = (ctypes.c_int32 * 4)(*axes[:4])
+    return _lib.GdnRotaryDesc(tokens, pos_rows, Hq, Hk, D, len(axes) if n is None else n, dims, io, flags, theta)
+
+
+RN = ["q", "k", "pos", "qo", "ko"]
+
+
+def rotary(lib, d, **over):
+    p = dict(addresses(RN), **over)
+    return lib.gdn_rotary(None if d is None else ctypes.byref(d), *[p[n] for n in RN], None)
+
+
+@pytest.mark.parametrize("d,expect", [
+    (None, INVALID), (rot(tokens=-1), INVALID), (rot(pos_rows=0), INVALID), (rot(Hq=-1), INVALID), (rot(D=0), INVALID),
+    (rot(n=0), INVALID), (rot(n=5), INVALID), (rot(axes=(15, 17)), INVALID), (rot(axes=(32, 34)), INVALID),
+    (rot(axes=(-2, 8)), INVALID), (rot(axes=(0,)), INVALID), (rot(io=9), INVALID), (rot(flags=8), INVALID),
+    (rot(theta=0.0), INVALID), (rot(theta=float("nan")), INVALID), (rot(D=68), UNSUPPORTED), (rot(D=264), UNSUPPORTED),
+    (rot(Hq=65537), UNSUPPORTED),
+])
+def test_rotary_descriptor(lib, d, expect):
+    assert rotary(lib, d) == expect
+
+
+def test_rotary_pointers(lib):
+    a = addresses(RN)
+    for n in RN:
+        assert rotary(lib, rot(), **{n: None}) == INVALID, n
+    for n in ("q", "k", "qo", "ko"):
+        assert rotary(lib, rot(), **{n: a[n] + 8}) == ALIGN, n
+    assert rotary(lib, rot(), pos=a["pos"] + 2) == ALIGN
+    assert rotary(lib, rot(), qo=a["q"] + 16) == ALIAS            # in place exactly, or apart
+    assert rotary(lib, rot(), qo=a["k"]) == ALIAS and rotary(lib, rot(), ko=a["qo"]) == ALIAS
+    assert rotary(lib, rot(), ko=a["pos"]) == ALIAS
+    assert rotary(lib, rot(tokens=0), **{n: None for n in RN}) == OK
+    assert rotary(lib, rot(Hq=0, Hk=0), **{n: None for n in RN}) == OK
+
+
+# ------------------------------------------------------------------ the torch side
+def test_torch_refusals():
+    x = torch.zeros(4, 64)
+    with pytest.raises(ValueError, match="device tensor"):
+        api.layer_norm_fwd(x)
+    with pytest.raises(ValueError, match="device tensor"):
+        api.layer_norm_bwd(x, x, x[:, 0], x[:, 0])
+    with pytest.raises(TypeError):
+        api.layer_norm_fwd([1.0])
+    q = torch.zeros(4, 2, 64)
+    with pytest.raises(ValueError, match="device tensor"):
+        api.rotary(q, q, torch.zeros(4, 1, dtype=torch.int32), axes=(64,))
+    with pytest.raises(TypeError):
+        api.rotary(None, None, torch.zeros(4, 1, dtype=torch.int32), axes=(64,))
