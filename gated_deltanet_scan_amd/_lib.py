@@ -24,6 +24,7 @@ GDN_ROTARY_MAX_AXES = 4
 GDN_FLAG_ROTARY_HALVES = 0x1
 GDN_FLAG_ROTARY_INVERSE = 0x2
 GDN_FLAG_ROTARY_POS_F32 = 0x4
+GDN_FLAG_ATTN_CAUSAL = 0x1
 
 STATUS = {0: "GDN_OK", 1: "GDN_ERR_INVALID_ARG", 2: "GDN_ERR_UNSUPPORTED", 3: "GDN_ERR_ALIGNMENT",
           4: "GDN_ERR_ALIAS", 5: "GDN_ERR_WORKSPACE", 6: "GDN_ERR_LAUNCH", 7: "GDN_ERR_NO_DEVICE"}
@@ -45,6 +46,14 @@ class GdnRotaryDesc(ctypes.Structure):
                 ("Hk", ctypes.c_int32), ("D", ctypes.c_int32), ("n_axes", ctypes.c_int32),
                 ("axis_dim", ctypes.c_int32 * GDN_ROTARY_MAX_AXES), ("io_dtype", ctypes.c_int32),
                 ("flags", ctypes.c_uint32), ("theta", ctypes.c_double)]
+
+
+class GdnAttnDesc(ctypes.Structure):
+    _fields_ = [("total_q", ctypes.c_int64), ("total_k", ctypes.c_int64), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("k_room", ctypes.c_int64), ("n_seq", ctypes.c_int32),
+                ("Hq", ctypes.c_int32), ("Hk", ctypes.c_int32), ("D", ctypes.c_int32), ("max_q", ctypes.c_int32),
+                ("max_k", ctypes.c_int32), ("causal_block", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("scale", ctypes.c_float)]
 
 
 class GdnError(RuntimeError):
@@ -118,6 +127,15 @@ def load():
     lib.gdn_layer_norm_bwd.restype = ctypes.c_int
     lib.gdn_rotary.argtypes = [rp, vp, vp, vp, vp, vp, vp]
     lib.gdn_rotary.restype = ctypes.c_int
+    ap = ctypes.POINTER(GdnAttnDesc)
+    lib.gdn_attn_workspace_size.argtypes = [ap]
+    lib.gdn_attn_workspace_size.restype = sz
+    lib.gdn_attn_workspace_size_bwd.argtypes = [ap]
+    lib.gdn_attn_workspace_size_bwd.restype = sz
+    lib.gdn_attn_fwd.argtypes = [ap, vp, vp, vp, vp, vp, vp, vp, fp, vp, sz, vp]
+    lib.gdn_attn_fwd.restype = ctypes.c_int
+    lib.gdn_attn_bwd.argtypes = [ap, vp, vp, vp, vp, fp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.gdn_attn_bwd.restype = ctypes.c_int
     lib.gdn_status_string.argtypes = [ctypes.c_int]
     lib.gdn_status_string.restype = ctypes.c_char_p
     lib.gdn_version.argtypes = []

@@ -675,3 +675,153 @@ def rotary(q, k, pos, *, axes, theta: float = 10000.0, halves: bool = False, inv
     if st != 0:
         raise GdnError(st, "gdn_rotary")
     return q_out, k_out
+
+
+def _token_strides(t, name, dtype):
+    """(token stride, tokens between sequences or 0 for packed) of t [..., H, D]:
+    heads packed, a sequence's tokens evenly apart."""
+    if t.device.type != "cuda":
+        raise ValueError("%s must be a device tensor (got %s)" % (name, t.device))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s (got %s)" % (name, dtype, t.dtype))
+    H, D = t.shape[-2:]
+    if t.is_contiguous() or t.numel() == 0:
+        return H * D, 0
+    ok = (D == 1 or t.stride(-1) == 1) and (H == 1 or t.stride(-2) == D)
+    axes = [i for i in range(t.dim() - 2) if t.shape[i] > 1]
+    batch = bool(axes) and t.dim() > 3 and axes[0] == 0
+    inner = axes[1:] if batch else axes
+    ld = t.stride(inner[-1]) if inner else H * D
+    ok = ok and ld >= H * D
+    step = ld
+    for i in reversed(inner):                 # the token axes continue one step
+        ok = ok and t.stride(i) == step
+        step *= t.shape[i]
+    room = 0
+    if batch and t.stride(0) != step:
+        if not inner:                         # one token a sequence: any step between them will do
+            ld = t.stride(0)
+        else:
+            room = t.stride(0) // ld
+            ok = ok and t.stride(0) % ld == 0 and t.stride(0) > step
+    if not ok:
+        raise ValueError("%s must have packed heads and evenly spaced tokens" % name)
+    return ld, room
+
+
+def _attn_args(q, k, v, causal, causal_block, scale, cu_q, cu_k, max_q, max_k):
+    """Checks shared by attention_fwd and attention_bwd: (desc, cu_q, cu_k)."""
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a torch.Tensor" % name)
+    if q.dim() not in (3, 4, 5) or k.dim() != q.dim() or v.shape != k.shape:
+        raise ValueError("q, k and v must be [T, H, D], [B, L, H, D] or [B, F, N, H, D], k and v alike (got %s, %s, %s)"
+                         % (tuple(q.shape), tuple(k.shape), tuple(v.shape)))
+    Hq, D = q.shape[-2:]
+    Hk = k.shape[-2]
+    if k.shape[-1] != D:
+        raise ValueError("q and k must have the same head size")
+    tq, tk = q.shape[:-2].numel(), k.shape[:-2].numel()
+    _io(q.dtype, "q, k and v")
+    (ldq, rq), (ldk, rk), (ldv, rv) = [_token_strides(t, n, q.dtype)
+                                       for t, n in ((q, "q"), (k, "k"), (v, "v"))]
+    if rq:
+        raise ValueError("q must have packed heads and evenly spaced tokens")
+    if rk != rv:
+        raise ValueError("the sequences of k and v must lie equally far apart")
+    if causal_block is None:
+        causal_block = q.shape[2] if q.dim() == 5 else 1
+    if q.dim() == 3:
+        if cu_q is None:
+            raise ValueError("packed q [T, H, D] needs cu_q")
+        cu_k = cu_q if cu_k is None else cu_k
+        n_seq = cu_q.numel() - 1
+        for name, t in (("cu_q", cu_q), ("cu_k", cu_k)):
+            _check(t, name, torch.int32, (n_seq + 1,))
+        if n_seq < 0:
+            raise ValueError("cu_q must hold n_seq + 1 offsets")
+        max_q = tq if max_q is None else int(max_q)
+        max_k = tk if max_k is None else int(max_k)
+    else:
+        if cu_q is not None or cu_k is not None or max_q is not None or max_k is not None:
+            raise ValueError("cu_q, cu_k, max_q and max_k belong to packed q [T, H, D]")
+        n_seq = q.shape[0]
+        if k.shape[0] != n_seq:
+            raise ValueError("q and k must have the same batch size")
+        max_q, max_k = (tq // n_seq, tk // n_seq) if n_seq else (0, 0)
+    _same_device(q.device, k=k, v=v, cu_q=cu_q, cu_k=cu_k)
+    desc = _lib.GdnAttnDesc(tq, tk, ldq, ldk, ldv, rk, n_seq, Hq, Hk, D, max_q, max_k, int(causal_block),
+                            _io(q.dtype, "q"), _lib.GDN_FLAG_ATTN_CAUSAL if causal else 0,
+                            float(D ** -0.5 if scale is None else scale))
+    return desc, cu_q, cu_k
+
+
+def attention_fwd(q, k, v, *, causal: bool = False, causal_block: Optional[int] = None, scale=None, cu_q=None,
+                  cu_k=None, max_q=None, max_k=None, k_len=None, o=None, lse=None, return_lse: bool = True,
+                  workspace=None, stream=None):
+    """Softmax attention with grouped heads.
+
+    q: [B, L, Hq, D], k and v: [B, Lk, Hk, D] (or [B, F, N, H, D] frames, or
+    packed [T, H, D] with cu_q), bf16 or fp32, Hq a multiple of Hk, D in {16,
+    32, 64, 128}; heads packed, tokens evenly apart (a slice of a fused
+    projection, or the first tokens k[:, :n] of a cache's slots, will do).  causal=True: the queries are the last positions of
+    their sequence and see the keys up to the end of their own block of
+    causal_block positions (default: a frame's N tokens for [B, F, N, H, D],
+    else 1).  cu_q, cu_k (default cu_q): int32 [n_seq + 1] offsets of packed
+    sequences, max_q and max_k bounds of their lengths (default: all tokens;
+    the tighter, the fewer empty workgroups).  k_len: int32 [n_seq], keys in use
+    of each sequence's (a cache with room).  Returns (o like q, lse [..., Hq]
+    fp32 or None); tokens of no sequence are left unset.
+    """
+    desc, cu_q, cu_k = _attn_args(q, k, v, causal, causal_block, scale, cu_q, cu_k, max_q, max_k)
+    if k_len is not None:
+        _check(k_len, "k_len", torch.int32, (desc.n_seq,))
+    if o is not None:
+        _check(o, "o", q.dtype, q.shape)
+    if lse is not None:
+        _check(lse, "lse", torch.float32, q.shape[:-1])
+    _check_workspace(workspace, q.device)
+    _same_device(q.device, k_len=k_len, o=o, lse=lse)
+    lib = _lib.load()
+    stream = _launch_stream(stream, q.device)
+    with torch.cuda.stream(stream):   # allocations belong to the launch stream
+        if o is None:
+            o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if lse is None and return_lse:
+            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+        workspace = _workspace(workspace, int(lib.gdn_attn_workspace_size(ctypes.byref(desc))), q.device)
+        st = lib.gdn_attn_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k), _ptr(k_len),
+                              _ptr(o), _ptr(lse), _ptr(workspace), _ws_bytes(workspace),
+                              ctypes.c_void_p(stream.cuda_stream))
+    if st != 0:
+        raise GdnError(st, "gdn_attn_fwd")
+    return o, lse
+
+
+def attention_bwd(q, k, v, o, lse, dO, *, causal: bool = False, causal_block: Optional[int] = None, scale=None,
+                  cu_q=None, cu_k=None, max_q=None, max_k=None, dq=None, dk=None, dv=None, workspace=None,
+                  stream=None):
+    """Gradients of attention_fwd (without k_len): (dq, dk, dv) in the inputs'
+    dtype, contiguous.  o and lse are the forward call's, dO the loss gradient
+    of o; the rest as given to it.  Tokens of no sequence are left unset."""
+    desc, cu_q, cu_k = _attn_args(q, k, v, causal, causal_block, scale, cu_q, cu_k, max_q, max_k)
+    _check(o, "o", q.dtype, q.shape)
+    _check(lse, "lse", torch.float32, q.shape[:-1])
+    _check(dO, "dO", q.dtype, q.shape)
+    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        if t is not None:
+            _check(t, name, like.dtype, like.shape)
+    _check_workspace(workspace, q.device)
+    _same_device(q.device, o=o, lse=lse, dO=dO, dq=dq, dk=dk, dv=dv)
+    lib = _lib.load()
+    stream = _launch_stream(stream, q.device)
+    with torch.cuda.stream(stream):   # allocations belong to the launch stream
+        dq, dk, dv = [t if t is not None else torch.empty(like.shape, dtype=like.dtype, device=like.device)
+                      for t, like in ((dq, q), (dk, k), (dv, v))]
+        workspace = _workspace(workspace, int(lib.gdn_attn_workspace_size_bwd(ctypes.byref(desc))), q.device)
+        st = lib.gdn_attn_bwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dO), _ptr(cu_q),
+                              _ptr(cu_k), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), _ws_bytes(workspace),
+                              ctypes.c_void_p(stream.cuda_stream))
+    if st != 0:
+        raise GdnError(st, "gdn_attn_bwd")
+    return dq, dk, dv

@@ -92,3 +92,31 @@ def rotary(q, k, pos, *, axes, theta: float = 10000.0, halves: bool = False, inv
     """Differentiable rotary positions (layouts as for api.rotary); the gradient
     is the rotation turned back."""
     return _Rotary.apply(q, k, pos, tuple(axes), theta, halves, inverse)
+
+
+class _Attention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, causal, causal_block, scale, cu_q, cu_k, max_q, max_k):
+        kw = dict(causal=causal, causal_block=causal_block, scale=scale, max_q=max_q, max_k=max_k)
+        # tokens of no sequence: zeros, so that they add nothing further on
+        o = None if cu_q is None else torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+        o, lse = api.attention_fwd(q, k, v, cu_q=cu_q, cu_k=cu_k, o=o, **kw)
+        ctx.kw = kw
+        ctx.save_for_backward(q, k, v, o, lse, cu_q, cu_k)
+        return o
+
+    @staticmethod
+    def backward(ctx, dO):
+        q, k, v, o, lse, cu_q, cu_k = ctx.saved_tensors
+        outs = [None] * 3 if cu_q is None else [torch.zeros(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v)]
+        dq, dk, dv = api.attention_bwd(q, k, v, o, lse, dO.contiguous(), cu_q=cu_q, cu_k=cu_k, dq=outs[0], dk=outs[1],
+                                       dv=outs[2], **ctx.kw)
+        return dq, dk, dv, None, None, None, None, None, None, None
+
+
+def attention(q, k, v, *, causal: bool = False, causal_block=None, scale=None, cu_q=None, cu_k=None, max_q=None,
+              max_k=None):
+    """Differentiable softmax attention (layouts as for api.attention_fwd); keeps
+    o and the logarithm of each row's sum for the backward pass.  Tokens of no
+    packed sequence give zeros, in the output and in the gradients."""
+    return _Attention.apply(q, k, v, causal, causal_block, scale, cu_q, cu_k, max_q, max_k)

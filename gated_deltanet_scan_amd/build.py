@@ -12,7 +12,8 @@ ROOT = os.path.dirname(PKG)
 SRCS = [os.path.join(PKG, "csrc", "gdn_api.hip"),    # scan kernels and their C ABI
         os.path.join(PKG, "csrc", "gdn_block.hip"),  # block projections (hipBLASLt GEMMs)
         os.path.join(PKG, "csrc", "gdn_norm.hip"),   # layer norm
-        os.path.join(PKG, "csrc", "gdn_rotary.hip")] # rotary positions
+        os.path.join(PKG, "csrc", "gdn_rotary.hip"), # rotary positions
+        os.path.join(PKG, "csrc", "gdn_attn.hip")]   # softmax attention
 LIBS = ["-L/opt/rocm/lib", "-lhipblaslt", "-Wl,-rpath,/opt/rocm/lib"]
 SO = os.path.join(PKG, "libgdn.so")
 

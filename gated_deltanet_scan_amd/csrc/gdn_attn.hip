@@ -1,0 +1,575 @@
+// Softmax attention, forward and backward: the C ABI of gdn_attn_fwd /
+// gdn_attn_bwd (declared in include/gdn.h), and the kernels in fp32 matrix
+// instructions.
+//
+//     S = scale q k^T,  P = softmax over the visible keys,  o = P v
+//     dP = d_o v^T,  dS = P (dP - <d_o, o>)
+//     dq = scale dS k,  dk = scale dS^T q,  dv = P^T d_o
+//
+// The forward pass keeps a running maximum and sum per row, so P never leaves
+// the registers; the backward pass forms P again from the saved logarithm of
+// the sum.  dq and (dk, dv) are two kernels, each summing in its own registers
+// in a fixed order (no atomics; S and dP are formed twice).
+//
+// v_mfma_f32_16x16x4_f32: lane l = 16 g + r holds operand A[row r][k = g] and
+// B[k = g][column r]; the result sits in lane l as rows 4g..4g+3 of column r.
+// Scores are formed transposed (keys as rows, the wave's 16 query rows as
+// columns), so the four values that a lane holds are the B operands of the
+// next product, key 4g + i for its i-th: P needs no trip through LDS.
+// The feature axis is contracted in the order 16 s + 4 g + j, which lets a
+// lane read four features at once.
+#include "gdn_attn.hpp"
+
+#include <algorithm>
+
+namespace {
+
+using namespace gdnattn;
+
+constexpr int kThreads = 256;
+constexpr int kRows = 64;     // query rows (or keys, in the dk/dv kernel) per workgroup: 16 a wave
+constexpr int kTile = 32;     // keys (or rows) staged in LDS at a time
+
+__device__ __forceinline__ f32x4 mma(float a, float b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 load4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+__device__ __forceinline__ f32x4 load4(const uint16_t* p) {
+    const u32x2 r = *reinterpret_cast<const u32x2*>(p);
+    return f32x4{__uint_as_float(r[0] << 16), __uint_as_float(r[0] & 0xffff0000u), __uint_as_float(r[1] << 16),
+                 __uint_as_float(r[1] & 0xffff0000u)};
+}
+__device__ __forceinline__ void store4(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
+__device__ __forceinline__ void store4(uint16_t* p, f32x4 v) {
+    *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+}
+// Over the four lanes that hold one column.
+__device__ __forceinline__ float col_max(float x) {
+    x = fmaxf(x, __shfl_xor(x, 16));
+    return fmaxf(x, __shfl_xor(x, 32));
+}
+__device__ __forceinline__ float col_sum(float x) {
+    x += __shfl_xor(x, 16);
+    return x + __shfl_xor(x, 32);
+}
+
+// Row r of the packed row axis of kv head hk: its global (token, head) row.
+__device__ __forceinline__ int64_t packed_row(const AttnArgs& a, const Seq& z, int hk, int r) {
+    return (z.q0 + r / a.G) * a.Hq + hk * a.G + r % a.G;
+}
+template <typename T>
+__device__ __forceinline__ const T* q_row(const AttnArgs& a, const Seq& z, int hk, int r) {
+    return static_cast<const T*>(a.q) + (z.q0 + r / a.G) * a.ldq + (int64_t)(hk * a.G + r % a.G) * a.D;
+}
+
+// The lane's share of one row, features 16 s + 4 g .. + 3 for every s.
+template <typename T, int D>
+__device__ __forceinline__ void row_frag(f32x4 (&f)[D / 16], const T* row, bool valid, int g) {
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) f[s] = valid ? load4(row + 16 * s + 4 * g) : f32x4{0.f, 0.f, 0.f, 0.f};
+}
+
+// Rows [n0, n0 + kTile) of a key tensor into LDS as fp32, zeros from hi on.
+template <typename T, int D>
+__device__ __forceinline__ void stage(float (*t)[D + 4], const T* base, int64_t ld, int n0, int hi) {
+    for (int c = threadIdx.x; c < kTile * D / 4; c += kThreads) {
+        const int n = c / (D / 4), e = c % (D / 4) * 4;
+        store4(&t[n][e], n0 + n < hi ? load4(base + (int64_t)(n0 + n) * ld + e) : f32x4{0.f, 0.f, 0.f, 0.f});
+    }
+}
+
+// (sequence, kv head, tile, split) of a workgroup; the tile runs fastest, from
+// the last (the longest under a causal mask) to the first.
+struct Place {
+    int s, hk, tile, split;
+};
+__device__ __forceinline__ Place place(const AttnArgs& a) {
+    unsigned b = blockIdx.x;
+    Place p;
+    p.tile = a.tiles - 1 - (int)(b % a.tiles);
+    b /= a.tiles;
+    p.split = (int)(b % a.splits);
+    b /= a.splits;
+    p.hk = (int)(b % a.Hk);
+    p.s = (int)(b / a.Hk);
+    return p;
+}
+
+template <typename T, int D>
+__global__ __launch_bounds__(kThreads) void attn_fwd_f32_kernel(const AttnArgs a) {
+    __shared__ float kt[kTile][D + 4], vt[kTile][D + 4];
+    const Place p = place(a);
+    const Seq z = sequence(a, p.s);
+    const int rows = z.lq * a.G, r0 = p.tile * kRows;
+    if (r0 >= rows) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
+    const int row = r0 + 16 * wave + c;
+    const bool valid = row < rows;
+    const int n = valid ? visible(a, z, row / a.G) : 0;
+    const int upto = visible(a, z, (min(r0 + kRows, rows) - 1) / a.G);
+    int lo, hi;
+    split_range(upto, kTile, a.splits, p.split, lo, hi);
+    f32x4 q[D / 16], acc[D / 16];
+    row_frag<T, D>(q, valid ? q_row<T>(a, z, p.hk, row) : nullptr, valid, g);
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) acc[s] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const T* kb = static_cast<const T*>(a.k) + z.k0 * a.ldk + (int64_t)p.hk * D;
+    const T* vb = static_cast<const T*>(a.v) + z.k0 * a.ldv + (int64_t)p.hk * D;
+    const float c2 = a.scale * kLog2e;
+    float m = -INFINITY, l = 0.f;
+    for (int n0 = lo; n0 < hi; n0 += kTile) {
+        __syncthreads();
+        stage<T, D>(kt, kb, a.ldk, n0, hi);
+        stage<T, D>(vt, vb, a.ldv, n0, hi);
+        __syncthreads();
+        f32x4 s[2];
+        float mt = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            s[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int e = 0; e < D / 16; ++e) {
+                const f32x4 kf = load4(&kt[16 * t + c][16 * e + 4 * g]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[t] = mma(kf[j], q[e][j], s[t]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (n0 + 16 * t + 4 * g + i >= n) s[t][i] = -INFINITY;
+                mt = fmaxf(mt, s[t][i]);
+            }
+        }
+        mt = fmaxf(m, col_max(mt) * c2);
+        const float ms = mt == -INFINITY ? 0.f : mt;      // nothing visible so far
+        const float al = exp2_f(m - ms);
+        m = mt;
+        float sum = 0.f;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s[t][i] = exp2_f(__builtin_fmaf(s[t][i], c2, -ms));
+                sum += s[t][i];
+            }
+        l = l * al + sum;                                 // this lane's keys; joined at the end
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e) acc[e] *= al;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < D / 16; ++e) acc[e] = mma(vt[16 * t + 4 * g + i][16 * e + c], s[t][i], acc[e]);
+    }
+    l = col_sum(l);
+    if (!valid) return;
+    const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
+    const float ls = l == 0.f ? -INFINITY : (m + log2_f(l)) * kLn2;
+    const int64_t gr = packed_row(a, z, p.hk, row);
+    if (a.splits > 1) {
+        const int64_t pr = (int64_t)p.split * a.total_q * a.Hq + gr;
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e) store4(a.part_o + pr * D + 16 * e + 4 * g, acc[e] * inv);
+        if (g == 0) a.part_lse[pr] = ls;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < D / 16; ++e) store4(static_cast<T*>(a.out) + gr * D + 16 * e + 4 * g, acc[e] * inv);
+    if (g == 0 && a.lse) a.lse[gr] = ls;
+}
+
+// o = sum over the splits of exp(lse_s - lse) o_s.  A quarter-wave a row; the
+// rows are the sequences' own, so what lies behind the last one is left alone.
+template <typename T, int D>
+__global__ __launch_bounds__(kThreads) void attn_join_kernel(const AttnArgs a) {
+    const int per = kThreads / 16;
+    const int tiles = (a.max_q * a.Hq + per - 1) / per;
+    const int s = (int)(blockIdx.x / (unsigned)tiles);
+    int64_t q0;
+    int lq;
+    seq_range(a.cu_q, s, a.total_q, a.max_q, q0, lq);
+    const int64_t r = (int64_t)(blockIdx.x % (unsigned)tiles) * per + (threadIdx.x >> 4);
+    if (r >= (int64_t)lq * a.Hq) return;
+    const int64_t gr = q0 * a.Hq + r, all = a.total_q * a.Hq;
+    float m = -INFINITY;
+    for (int i = 0; i < a.splits; ++i) m = fmaxf(m, a.part_lse[i * all + gr]);
+    const float ms = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    f32x4 acc[(D + 63) / 64];
+    const int c = 4 * (threadIdx.x & 15);
+#pragma unroll
+    for (int e = 0; e < (D + 63) / 64; ++e) acc[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < a.splits; ++i) {
+        const float pl = a.part_lse[i * all + gr];
+        if (pl == -INFINITY) continue;                    // a split that saw nothing wrote zeros
+        const float w = exp2_f((pl - ms) * kLog2e);
+        l += w;
+#pragma unroll
+        for (int e = 0; e < (D + 63) / 64; ++e)
+            if (64 * e + c < D) acc[e] += w * load4(a.part_o + (i * all + gr) * D + 64 * e + c);
+    }
+    const float inv = l > 0.f ? 1.0f / l : l;
+#pragma unroll
+    for (int e = 0; e < (D + 63) / 64; ++e)
+        if (64 * e + c < D) store4(static_cast<T*>(a.out) + gr * D + 64 * e + c, acc[e] * inv);
+    if (c == 0 && a.lse) a.lse[gr] = l == 0.f ? -INFINITY : ms + log2_f(l) * kLn2;
+}
+
+// dq, and <d_o, o> for the dk/dv kernel: query rows as columns, as in the
+// forward kernel.
+template <typename T, int D>
+__global__ __launch_bounds__(kThreads) void attn_dq_f32_kernel(const AttnArgs a) {
+    __shared__ float kt[kTile][D + 4], vt[kTile][D + 4];
+    const Place p = place(a);
+    const Seq z = sequence(a, p.s);
+    const int rows = z.lq * a.G, r0 = p.tile * kRows;
+    if (r0 >= rows) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
+    const int row = r0 + 16 * wave + c;
+    const bool valid = row < rows;
+    const int n = valid ? visible(a, z, row / a.G) : 0;
+    const int upto = visible(a, z, (min(r0 + kRows, rows) - 1) / a.G);
+    const int64_t gr = packed_row(a, z, p.hk, valid ? row : r0);
+    f32x4 q[D / 16], dout[D / 16], acc[D / 16];
+    row_frag<T, D>(q, valid ? q_row<T>(a, z, p.hk, row) : nullptr, valid, g);
+    row_frag<T, D>(dout, static_cast<const T*>(a.d_o) + gr * D, valid, g);
+    float delta = 0.f;
+    {
+        f32x4 o[D / 16];
+        row_frag<T, D>(o, static_cast<const T*>(a.o) + gr * D, valid, g);
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) delta += dout[e][j] * o[e][j];
+    }
+    delta = col_sum(delta);
+    if (valid && g == 0) a.delta[gr] = delta;
+    const float c2 = a.scale * kLog2e;
+    float ls = valid ? a.lse[gr] * kLog2e : -INFINITY;
+    const int nn = ls == -INFINITY ? 0 : n;
+    if (ls == -INFINITY) ls = 0.f;
+#pragma unroll
+    for (int e = 0; e < D / 16; ++e) acc[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const T* kb = static_cast<const T*>(a.k) + z.k0 * a.ldk + (int64_t)p.hk * D;
+    const T* vb = static_cast<const T*>(a.v) + z.k0 * a.ldv + (int64_t)p.hk * D;
+    for (int n0 = 0; n0 < upto; n0 += kTile) {
+        __syncthreads();
+        stage<T, D>(kt, kb, a.ldk, n0, upto);
+        stage<T, D>(vt, vb, a.ldv, n0, upto);
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f}, dp = s;
+#pragma unroll
+            for (int e = 0; e < D / 16; ++e) {
+                const f32x4 kf = load4(&kt[16 * t + c][16 * e + 4 * g]), vf = load4(&vt[16 * t + c][16 * e + 4 * g]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s = mma(kf[j], q[e][j], s);
+                    dp = mma(vf[j], dout[e][j], dp);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float pr = exp2_f(__builtin_fmaf(s[i], c2, -ls));
+                const float ds = n0 + 16 * t + 4 * g + i < nn ? pr * (dp[i] - delta) : 0.f;
+#pragma unroll
+                for (int e = 0; e < D / 16; ++e) acc[e] = mma(kt[16 * t + 4 * g + i][16 * e + c], ds, acc[e]);
+            }
+        }
+    }
+    if (!valid) return;
+#pragma unroll
+    for (int e = 0; e < D / 16; ++e) store4(static_cast<T*>(a.dq) + gr * D + 16 * e + 4 * g, acc[e] * a.scale);
+}
+
+// dk and dv: a wave's 16 keys as columns, the packed query rows staged in LDS.
+template <typename T, int D>
+__global__ __launch_bounds__(kThreads) void attn_dkv_f32_kernel(const AttnArgs a) {
+    __shared__ float qt[kTile][D + 4], dt[kTile][D + 4];
+    __shared__ float ls[kTile], dl[kTile];
+    __shared__ int nv[kTile];
+    const Place p = place(a);
+    const Seq z = sequence(a, p.s);
+    const int k0 = p.tile * kRows;
+    if (k0 >= z.lk) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
+    const int key = k0 + 16 * wave + c;
+    const bool valid = key < z.lk;
+    f32x4 kf[D / 16], vf[D / 16], ak[D / 16], av[D / 16];
+    row_frag<T, D>(kf, static_cast<const T*>(a.k) + (z.k0 + key) * a.ldk + (int64_t)p.hk * D, valid, g);
+    row_frag<T, D>(vf, static_cast<const T*>(a.v) + (z.k0 + key) * a.ldv + (int64_t)p.hk * D, valid, g);
+#pragma unroll
+    for (int e = 0; e < D / 16; ++e) ak[e] = av[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const float c2 = a.scale * kLog2e;
+    const int rows = z.lq * a.G;
+    for (int r0 = first_query(a, z, k0) * a.G; r0 < rows; r0 += kTile) {
+        __syncthreads();
+        for (int x = threadIdx.x; x < kTile * D / 4; x += kThreads) {
+            const int n = x / (D / 4), e = x % (D / 4) * 4;
+            f32x4 qv = f32x4{0.f, 0.f, 0.f, 0.f}, dv = qv;
+            if (r0 + n < rows) {
+                qv = load4(q_row<T>(a, z, p.hk, r0 + n) + e);
+                dv = load4(static_cast<const T*>(a.d_o) + packed_row(a, z, p.hk, r0 + n) * D + e);
+            }
+            store4(&qt[n][e], qv);
+            store4(&dt[n][e], dv);
+        }
+        if (threadIdx.x < kTile) {
+            const int r = r0 + threadIdx.x;
+            float l = -INFINITY, d = 0.f;
+            int n = 0;
+            if (r < rows) {
+                const int64_t gr = packed_row(a, z, p.hk, r);
+                l = a.lse[gr] * kLog2e;
+                d = a.delta[gr];
+                n = visible(a, z, r / a.G);
+            }
+            ls[threadIdx.x] = l == -INFINITY ? 0.f : l;
+            dl[threadIdx.x] = d;
+            nv[threadIdx.x] = l == -INFINITY ? 0 : n;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f}, dp = s;
+#pragma unroll
+            for (int e = 0; e < D / 16; ++e) {
+                const f32x4 qf = load4(&qt[16 * t + c][16 * e + 4 * g]), df = load4(&dt[16 * t + c][16 * e + 4 * g]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s = mma(qf[j], kf[e][j], s);
+                    dp = mma(df[j], vf[e][j], dp);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 16 * t + 4 * g + i;
+                const float pr = key < nv[r] ? exp2_f(__builtin_fmaf(s[i], c2, -ls[r])) : 0.f;
+                const float ds = key < nv[r] ? pr * (dp[i] - dl[r]) : 0.f;
+#pragma unroll
+                for (int e = 0; e < D / 16; ++e) {
+                    av[e] = mma(dt[r][16 * e + c], pr, av[e]);
+                    ak[e] = mma(qt[r][16 * e + c], ds, ak[e]);
+                }
+            }
+        }
+    }
+    if (!valid) return;
+    const int64_t kr = ((z.ko + key) * a.Hk + p.hk) * D;
+#pragma unroll
+    for (int e = 0; e < D / 16; ++e) {
+        store4(static_cast<T*>(a.dk) + kr + 16 * e + 4 * g, ak[e] * a.scale);
+        store4(static_cast<T*>(a.dv) + kr + 16 * e + 4 * g, av[e]);
+    }
+}
+
+// ---------------------------------------------------------------- launch
+gdn_status check_attn(const gdn_attn_desc* d) {
+    if (!d) return GDN_ERR_INVALID_ARG;
+    if (d->n_seq < 0 || d->Hq < 1 || d->Hk < 1 || d->D < 1 || d->total_q < 0 || d->total_k < 0 || d->max_q < 0 ||
+        d->max_k < 0)
+        return GDN_ERR_INVALID_ARG;
+    if (d->Hq % d->Hk) return GDN_ERR_INVALID_ARG;
+    if (d->io_dtype != GDN_BF16 && d->io_dtype != GDN_F32) return GDN_ERR_INVALID_ARG;
+    if (d->flags & ~(uint32_t)GDN_FLAG_ATTN_CAUSAL) return GDN_ERR_INVALID_ARG;
+    if ((d->flags & GDN_FLAG_ATTN_CAUSAL) && d->causal_block < 1) return GDN_ERR_INVALID_ARG;
+    if (!(d->scale > 0.0f) || !(d->scale < 1e30f)) return GDN_ERR_INVALID_ARG;
+    if (d->k_room && d->k_room < d->max_k) return GDN_ERR_INVALID_ARG;
+    const int64_t rq = (int64_t)d->Hq * d->D, rk = (int64_t)d->Hk * d->D;
+    if ((d->q_stride && d->q_stride < rq) || (d->k_stride && d->k_stride < rk) || (d->v_stride && d->v_stride < rk))
+        return GDN_ERR_INVALID_ARG;
+    if (d->D != 16 && d->D != 32 && d->D != 64 && d->D != 128) return GDN_ERR_UNSUPPORTED;
+    if (rq > (1 << 20) || d->q_stride > (1 << 20) || d->k_stride > (1 << 20) || d->v_stride > (1 << 20))
+        return GDN_ERR_UNSUPPORTED;
+    // row numbers within a sequence are 32-bit, with room for a tile
+    if (d->total_q > INT32_MAX || d->total_k > INT32_MAX || (int64_t)d->max_q * d->Hq > (1 << 30) ||
+        d->max_k > (1 << 30) || d->k_room > INT32_MAX)
+        return GDN_ERR_UNSUPPORTED;
+    return GDN_OK;
+}
+
+bool fast(const gdn_attn_desc* d) { return d->io_dtype == GDN_BF16 && d->D >= 32; }
+
+int fwd_rows(const gdn_attn_desc* d) {
+    return kRows;
+}
+
+// Splits of the key axis: where the row tiles alone would leave compute units
+// idle, enough for about two workgroups on each of the 256, but no less than
+// 256 keys a split (a split's partial result is written and read in fp32).
+int fwd_splits(const gdn_attn_desc* d) {
+    const int64_t rows = (int64_t)d->max_q * (d->Hq / d->Hk);
+    const int64_t units = (int64_t)d->n_seq * d->Hk * std::max<int64_t>(1, (rows + fwd_rows(d) - 1) / fwd_rows(d));
+    if (units >= 256) return 1;
+    const int64_t most = std::max<int64_t>(1, d->max_k / 256);
+    return (int)std::min<int64_t>(std::min<int64_t>(most, (512 + units - 1) / std::max<int64_t>(units, 1)), 128);
+}
+
+AttnArgs fill(const gdn_attn_desc* d) {
+    AttnArgs a = {};
+    a.total_q = d->total_q, a.total_k = d->total_k;
+    a.n_seq = d->n_seq, a.Hq = d->Hq, a.Hk = d->Hk, a.G = d->Hq / d->Hk, a.D = d->D;
+    a.ldq = d->q_stride ? d->q_stride : (int64_t)d->Hq * d->D;
+    a.ldk = d->k_stride ? d->k_stride : (int64_t)d->Hk * d->D;
+    a.ldv = d->v_stride ? d->v_stride : (int64_t)d->Hk * d->D;
+    a.max_q = d->max_q, a.max_k = d->max_k;
+    a.k_room = d->k_room ? d->k_room : d->max_k;
+    a.causal = (d->flags & GDN_FLAG_ATTN_CAUSAL) ? 1 : 0;
+    a.block = a.causal ? d->causal_block : 1;
+    a.scale = d->scale;
+    a.splits = 1;
+    return a;
+}
+
+// Bytes from the first to the last element of a [rows][ld] tensor whose rows
+// hold w elements.
+size_t span(int64_t rows, int64_t ld, int64_t w, size_t e) { return rows > 0 ? ((size_t)(rows - 1) * ld + w) * e : 0; }
+
+// Key tokens from the first sequence's first to the last one's last.
+int64_t key_rows(const gdn_attn_desc* d, bool packed) {
+    if (packed || !d->k_room || d->n_seq < 1) return d->total_k;
+    return (d->n_seq - 1) * d->k_room + d->max_k;
+}
+
+bool grid_of(int64_t n, unsigned* g) {
+    if (n > INT32_MAX) return false;
+    *g = (unsigned)n;
+    return true;
+}
+
+template <typename T, int D>
+gdn_status run_fwd(AttnArgs a, hipStream_t s) {
+    unsigned grid;
+    a.tiles = (int)(((int64_t)a.max_q * a.G + kRows - 1) / kRows);
+    if (!grid_of((int64_t)a.tiles * a.splits * a.Hk * a.n_seq, &grid)) return GDN_ERR_UNSUPPORTED;
+    hipLaunchKernelGGL((attn_fwd_f32_kernel<T, D>), dim3(grid), dim3(kThreads), 0, s, a);
+    return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+template <typename T, int D>
+gdn_status run_join(const AttnArgs& a, hipStream_t s) {
+    unsigned grid;
+    if (!grid_of(((int64_t)a.max_q * a.Hq + 15) / 16 * a.n_seq, &grid)) return GDN_ERR_UNSUPPORTED;
+    hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3(grid), dim3(kThreads), 0, s, a);
+    return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+template <typename T, int D>
+gdn_status run_bwd(AttnArgs a, hipStream_t s) {
+    unsigned grid;
+    a.tiles = (int)(((int64_t)a.max_q * a.G + kRows - 1) / kRows);
+    if (!grid_of((int64_t)a.tiles * a.Hk * a.n_seq, &grid)) return GDN_ERR_UNSUPPORTED;
+    if (grid) hipLaunchKernelGGL((attn_dq_f32_kernel<T, D>), dim3(grid), dim3(kThreads), 0, s, a);
+    a.tiles = (a.max_k + kRows - 1) / kRows;
+    if (!grid_of((int64_t)a.tiles * a.Hk * a.n_seq, &grid)) return GDN_ERR_UNSUPPORTED;
+    if (grid) hipLaunchKernelGGL((attn_dkv_f32_kernel<T, D>), dim3(grid), dim3(kThreads), 0, s, a);
+    return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
+#define GDN_BY_D(FN, T, ...)                                              \
+    (a.D == 16 ? FN<T, 16>(__VA_ARGS__) : a.D == 32 ? FN<T, 32>(__VA_ARGS__) \
+     : a.D == 64 ? FN<T, 64>(__VA_ARGS__) : FN<T, 128>(__VA_ARGS__))
+
+}  // namespace
+
+extern "C" {
+
+size_t gdn_attn_workspace_size(const gdn_attn_desc* d) {
+    if (check_attn(d) != GDN_OK || d->n_seq == 0 || d->total_q == 0 || d->max_q == 0) return 0;
+    const int64_t n = fwd_splits(d);
+    if (n < 2) return 0;
+    return round256((size_t)n * d->total_q * d->Hq * d->D * 4) + round256((size_t)n * d->total_q * d->Hq * 4);
+}
+
+gdn_status gdn_attn_fwd(const gdn_attn_desc* d, const void* q, const void* k, const void* v, const int32_t* cu_q,
+                        const int32_t* cu_k, const int32_t* k_len, void* o, float* lse, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+    gdn_status st = check_attn(d);
+    if (st != GDN_OK) return st;
+    if (!cu_q && (int64_t)d->n_seq * d->max_q != d->total_q) return GDN_ERR_INVALID_ARG;
+    if (!cu_k && (int64_t)d->n_seq * d->max_k != d->total_k) return GDN_ERR_INVALID_ARG;
+    if (d->n_seq == 0 || d->total_q == 0 || d->max_q == 0) return GDN_OK;
+    if (!q || !o || (d->total_k > 0 && (!k || !v))) return GDN_ERR_INVALID_ARG;
+    AttnArgs a = fill(d);
+    const size_t e = d->io_dtype == GDN_F32 ? 4 : 2;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
+        !aligned(cu_q, 4) || !aligned(cu_k, 4) || !aligned(k_len, 4))
+        return GDN_ERR_ALIGNMENT;
+    if (a.ldq * e % 16 || a.ldk * e % 16 || a.ldv * e % 16) return GDN_ERR_ALIGNMENT;
+    const size_t need = gdn_attn_workspace_size(d);
+    if (need && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
+    if (need && !aligned(workspace, 256)) return GDN_ERR_ALIGNMENT;
+    const int64_t wq = (int64_t)d->Hq * d->D, wk = (int64_t)d->Hk * d->D;
+    const Range ins[] = {rng(q, span(d->total_q, a.ldq, wq, e)), rng(k, span(key_rows(d, cu_k), a.ldk, wk, e)),
+                         rng(v, span(key_rows(d, cu_k), a.ldv, wk, e)), rng(cu_q, (size_t)(d->n_seq + 1) * 4),
+                         rng(cu_k, (size_t)(d->n_seq + 1) * 4), rng(k_len, (size_t)d->n_seq * 4)};
+    const Range outs[] = {rng(o, (size_t)d->total_q * wq * e), rng(lse, (size_t)d->total_q * d->Hq * 4),
+                          rng(need ? workspace : nullptr, need)};
+    for (int i = 0; i < 3; ++i) {
+        for (const Range& r : ins)
+            if (overlap(outs[i], r)) return GDN_ERR_ALIAS;
+        for (int j = i + 1; j < 3; ++j)
+            if (overlap(outs[i], outs[j])) return GDN_ERR_ALIAS;
+    }
+    int cus;
+    if ((st = check_device(&cus)) != GDN_OK) return st;
+    a.q = q, a.k = k, a.v = v, a.out = o, a.lse = lse, a.cu_q = cu_q, a.cu_k = cu_k, a.k_len = k_len;
+    a.splits = fwd_splits(d);
+    if (a.splits > 1) {
+        a.part_o = static_cast<float*>(workspace);
+        a.part_lse = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
+                                              round256((size_t)a.splits * d->total_q * d->Hq * d->D * 4));
+    }
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    const bool f32 = d->io_dtype == GDN_F32;
+    st = f32 ? GDN_BY_D(run_fwd, float, a, s) : GDN_BY_D(run_fwd, uint16_t, a, s);
+    if (st != GDN_OK || a.splits == 1) return st;
+    return f32 ? GDN_BY_D(run_join, float, a, s) : GDN_BY_D(run_join, uint16_t, a, s);
+}
+
+size_t gdn_attn_workspace_size_bwd(const gdn_attn_desc* d) {
+    if (check_attn(d) != GDN_OK || d->n_seq == 0) return 0;
+    return round256((size_t)d->total_q * d->Hq * 4);
+}
+
+gdn_status gdn_attn_bwd(const gdn_attn_desc* d, const void* q, const void* k, const void* v, const void* o,
+                        const float* lse, const void* dO, const int32_t* cu_q, const int32_t* cu_k, void* dq, void* dk,
+                        void* dv, void* workspace, size_t workspace_bytes, void* stream) {
+    gdn_status st = check_attn(d);
+    if (st != GDN_OK) return st;
+    if (!cu_q && (int64_t)d->n_seq * d->max_q != d->total_q) return GDN_ERR_INVALID_ARG;
+    if (!cu_k && (int64_t)d->n_seq * d->max_k != d->total_k) return GDN_ERR_INVALID_ARG;
+    if (d->n_seq == 0 || (d->total_q == 0 && d->total_k == 0)) return GDN_OK;
+    if (d->total_q > 0 && (!q || !o || !lse || !dO || !dq)) return GDN_ERR_INVALID_ARG;
+    if (d->total_k > 0 && (!k || !v || !dk || !dv)) return GDN_ERR_INVALID_ARG;
+    AttnArgs a = fill(d);
+    const size_t e = d->io_dtype == GDN_F32 ? 4 : 2;
+    for (const void* p : {q, k, v, o, dO, (const void*)dq, (const void*)dk, (const void*)dv})
+        if (!aligned(p, 16)) return GDN_ERR_ALIGNMENT;
+    if (!aligned(lse, 4) || !aligned(cu_q, 4) || !aligned(cu_k, 4)) return GDN_ERR_ALIGNMENT;
+    if (a.ldq * e % 16 || a.ldk * e % 16 || a.ldv * e % 16) return GDN_ERR_ALIGNMENT;
+    const size_t need = gdn_attn_workspace_size_bwd(d);
+    if (need && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return GDN_ERR_ALIGNMENT;
+    const int64_t wq = (int64_t)d->Hq * d->D, wk = (int64_t)d->Hk * d->D;
+    const size_t qb = (size_t)d->total_q * wq * e, kb = (size_t)d->total_k * wk * e;
+    const Range ins[] = {rng(q, span(d->total_q, a.ldq, wq, e)), rng(k, span(key_rows(d, cu_k), a.ldk, wk, e)),
+                         rng(v, span(key_rows(d, cu_k), a.ldv, wk, e)), rng(o, qb), rng(dO, qb),
+                         rng(lse, (size_t)d->total_q * d->Hq * 4), rng(cu_q, (size_t)(d->n_seq + 1) * 4),
+                         rng(cu_k, (size_t)(d->n_seq + 1) * 4)};
+    const Range outs[] = {rng(dq, qb), rng(dk, kb), rng(dv, kb), rng(need ? workspace : nullptr, need)};
+    for (int i = 0; i < 4; ++i) {
+        for (const Range& r : ins)
+            if (overlap(outs[i], r)) return GDN_ERR_ALIAS;
+        for (int j = i + 1; j < 4; ++j)
+            if (overlap(outs[i], outs[j])) return GDN_ERR_ALIAS;
+    }
+    int cus;
+    if ((st = check_device(&cus)) != GDN_OK) return st;
+    a.q = q, a.k = k, a.v = v, a.o = o, a.lse = const_cast<float*>(lse), a.d_o = dO;
+    a.dq = dq, a.dk = dk, a.dv = dv, a.cu_q = cu_q, a.cu_k = cu_k;
+    a.delta = static_cast<float*>(workspace);
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    return d->io_dtype == GDN_F32 ? GDN_BY_D(run_bwd, float, a, s) : GDN_BY_D(run_bwd, uint16_t, a, s);
+}
+
+}  // extern "C"

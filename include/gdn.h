@@ -425,6 +425,75 @@ typedef struct gdn_rotary_desc {
 gdn_status gdn_rotary(const gdn_rotary_desc* d, const void* q, const void* k, const void* pos,
                       void* q_out, void* k_out, void* stream);
 
+/* ------------------------------------------------------------------ attention
+ * Softmax attention, the exact-recall mixer of a hybrid backbone beside the
+ * scan: whole prompts, packed sequences of different lengths, a key cache filled
+ * in part, grouped heads, forward and backward.  For sequence s, query head h
+ * (key/value head h / (Hq/Hk)) and query i
+ *     o_i = sum_j p_ij v_j,   p_ij = softmax over the visible j of scale q_i . k_j
+ *     lse_i = log sum_j exp(scale q_i . k_j)
+ * Without GDN_FLAG_ATTN_CAUSAL every key of the sequence is visible.  With it the
+ * queries are the last lq positions of the sequence (position p = i + lk - lq)
+ * and key j is visible if it lies in p's block of causal_block positions or
+ * before it: floor(j / causal_block) <= floor(p / causal_block).  causal_block 1
+ * is the token-causal mask; N tokens a frame make it frame-causal, the order in
+ * which the scan consumes frames.  A query that sees nothing (p < 0, or no
+ * keys) gives o = 0 and lse = -infinity, and takes no part in the gradients.
+ *
+ * Layouts: q, o [total_q][Hq][D] and k, v [total_k][Hk][D] in io_dtype (GDN_BF16
+ * or GDN_F32), lse [total_q][Hq] float32.  q, k and v may have a token stride
+ * (q_stride, k_stride, v_stride in elements, 0 = packed; a slice of a fused
+ * projection), o and the gradients are packed.  Sequence s holds query tokens
+ * cu_q[s] .. cu_q[s+1]-1 and key tokens cu_k[s] .. cu_k[s+1]-1 (int32 device
+ * arrays of n_seq + 1 offsets); with k_len (int32 [n_seq], NULL: all) only the
+ * first k_len[s] of them: a cache with room to grow.  cu_q == NULL means
+ * sequences of max_q tokens each (total_q = n_seq max_q), and so for cu_k, where
+ * the sequences of k and v may lie k_room >= max_k tokens apart (the first max_k
+ * tokens of each slot of a cache; dk and dv are packed).
+ * max_q and max_k bound the lengths: a longer sequence is cut to them.  The
+ * arrays are read on the device; offsets outside the tensors are clamped.
+ * Tokens of no sequence are neither read nor written, in any output, and key
+ * values that no query of a sequence may see, past k_len included, are not used,
+ * whatever they hold.  (Within a sequence a non-finite value may reach any of
+ * its rows, as it does in a masked matrix product.)
+ *
+ * gdn_attn_bwd takes the forward call's q, k, v, o and lse and dO = dL/do, and
+ * writes dq, dk and dv (sums over the query heads that share a key head
+ * included); k_len is not supported there.  Products are float32 sums (bf16
+ * inputs: bf16 products, the probabilities and dS rounded to bf16 between them),
+ * the softmax's statistics float32; results are bitwise reproducible.
+ *
+ * Hq a multiple of Hk, scale finite and > 0, causal_block >= 1
+ * (GDN_ERR_INVALID_ARG); D in {16, 32, 64, 128}, Hq D and the strides at most
+ * 2^20, tokens below 2^31, max_q Hq and max_k at most 2^30 (GDN_ERR_UNSUPPORTED).  Tensors and token
+ * strides are multiples of 16 bytes, workspace 256 (its size depends on the
+ * descriptor alone); outputs are disjoint from the inputs, from each other and
+ * from the workspace. */
+#define GDN_FLAG_ATTN_CAUSAL 0x1u
+typedef struct gdn_attn_desc {
+    int64_t total_q, total_k;              /* query and key tokens               */
+    int64_t q_stride, k_stride, v_stride;  /* elements between tokens, 0: packed */
+    int64_t k_room;                        /* cu_k NULL: tokens from one sequence's first
+                                              key to the next one's, 0: max_k  */
+    int32_t n_seq, Hq, Hk, D;
+    int32_t max_q, max_k;                  /* bounds of the sequences' lengths   */
+    int32_t causal_block;                  /* positions a block (causal)         */
+    int32_t io_dtype;
+    uint32_t flags;                        /* GDN_FLAG_ATTN_*                    */
+    float scale;
+} gdn_attn_desc;
+
+size_t gdn_attn_workspace_size(const gdn_attn_desc* d);
+gdn_status gdn_attn_fwd(const gdn_attn_desc* d, const void* q, const void* k, const void* v,
+                        const int32_t* cu_q, const int32_t* cu_k, const int32_t* k_len,
+                        void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+size_t gdn_attn_workspace_size_bwd(const gdn_attn_desc* d);
+gdn_status gdn_attn_bwd(const gdn_attn_desc* d, const void* q, const void* k, const void* v,
+                        const void* o, const float* lse, const void* dO,
+                        const int32_t* cu_q, const int32_t* cu_k,
+                        void* dq, void* dk, void* dv,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
 /* Human-readable name of a status code (static storage). */
 const char* gdn_status_string(gdn_status s);
 

@@ -126,3 +126,93 @@ def test_torch_refusals():
         api.rotary(q, q, torch.zeros(4, 1, dtype=torch.int32), axes=(64,))
     with pytest.raises(TypeError):
         api.rotary(None, None, torch.zeros(4, 1, dtype=torch.int32), axes=(64,))
+
+
+# ------------------------------------------------------------------ attention
+def attn(tq=8, tk=8, qs=0, ks=0, vs=0, room=0, n=2, Hq=4, Hk=2, D=64, mq=4, mk=4, block=1, io=BF16, flags=0, scale=0.1):
+    return _lib.GdnAttnDesc(tq, tk, qs, ks, vs, room, n, Hq, Hk, D, mq, mk, block, io, flags, scale)
+
+
+AF = ["q", "k", "v", "cu_q", "cu_k", "k_len", "o", "lse", "ws"]
+AB = ["q", "k", "v", "o", "lse", "dO", "cu_q", "cu_k", "dq", "dk", "dv", "ws"]
+
+
+def attn_fwd(lib, d, ws_bytes=1 << 35, **over):
+    p = dict(addresses(AF), cu_q=None, cu_k=None, k_len=None)
+    p.update(over)
+    return lib.gdn_attn_fwd(None if d is None else ctypes.byref(d), *[p[n] for n in AF], ws_bytes, None)
+
+
+def attn_bwd(lib, d, ws_bytes=1 << 35, **over):
+    p = dict(addresses(AB), cu_q=None, cu_k=None)
+    p.update(over)
+    return lib.gdn_attn_bwd(None if d is None else ctypes.byref(d), *[p[n] for n in AB], ws_bytes, None)
+
+
+@pytest.mark.parametrize("d,expect", [
+    (None, INVALID), (attn(n=-1), INVALID), (attn(Hq=0), INVALID), (attn(Hk=3), INVALID), (attn(D=0), INVALID),
+    (attn(tq=-1), INVALID), (attn(mk=-1), INVALID), (attn(io=2), INVALID), (attn(flags=2), INVALID),
+    (attn(flags=1, block=0), INVALID), (attn(scale=0.0), INVALID), (attn(scale=-1.0), INVALID),
+    (attn(scale=float("nan")), INVALID), (attn(qs=248), INVALID), (attn(ks=120), INVALID), (attn(room=3), INVALID),
+    (attn(tq=9), INVALID), (attn(mk=5), INVALID),              # uniform sequences must fill the tensors
+    (attn(D=48), UNSUPPORTED), (attn(D=256), UNSUPPORTED), (attn(Hq=1 << 15, Hk=1 << 15), UNSUPPORTED),
+    (attn(ks=(1 << 20) + 8), UNSUPPORTED), (attn(tq=1 << 32, mq=1 << 31 - 1, n=2), UNSUPPORTED),
+])
+def test_attn_descriptor(lib, d, expect):
+    assert attn_fwd(lib, d) == expect and attn_bwd(lib, d) == expect
+
+
+def test_attn_pointers(lib):
+    d, a, b = attn(), addresses(AF), addresses(AB)
+    for n in ("q", "k", "v", "o"):
+        assert attn_fwd(lib, d, **{n: None}) == INVALID, n
+        assert attn_fwd(lib, d, **{n: a[n] + 8}) == ALIGN, n
+    for n in ("q", "k", "v", "o", "lse", "dO", "dq", "dk", "dv"):
+        assert attn_bwd(lib, d, **{n: None}) == INVALID, n
+    for n in ("q", "k", "v", "o", "dO", "dq", "dk", "dv"):
+        assert attn_bwd(lib, d, **{n: b[n] + 8}) == ALIGN, n
+    assert attn_fwd(lib, d, lse=a["lse"] + 2) == ALIGN and attn_fwd(lib, d, k_len=a["k_len"] + 1) == ALIGN
+    assert attn_fwd(lib, attn(qs=260)) == ALIGN                     # 520 bytes: not a multiple of 16
+    assert attn_bwd(lib, d, cu_q=b["cu_q"] + 2, cu_k=b["cu_k"]) == ALIGN
+    assert attn_fwd(lib, d, o=a["q"]) == ALIAS and attn_fwd(lib, d, lse=a["o"] + 64) == ALIAS
+    assert attn_fwd(lib, attn(ks=256), o=a["k"] + 7 * 512) == ALIAS  # inside the strided view's last row
+    assert attn_fwd(lib, attn(room=100), o=a["v"] + 103 * 256) == ALIAS
+    assert attn_fwd(lib, d, cu_q=a["o"]) == ALIAS
+    assert attn_bwd(lib, d, dk=b["dv"]) == ALIAS and attn_bwd(lib, d, dq=b["dO"]) == ALIAS
+    need = lib.gdn_attn_workspace_size_bwd(ctypes.byref(d))
+    assert need == 256                                              # a float per query row
+    assert attn_bwd(lib, d, ws_bytes=need - 1) == WORKSPACE and attn_bwd(lib, d, ws=None) == WORKSPACE
+    assert attn_bwd(lib, d, dv=b["ws"]) == ALIAS and attn_bwd(lib, d, ws=b["ws"] + 16) == ALIGN
+
+
+def test_attn_split_workspace(lib):
+    # few queries against a long cache: fp32 partial outputs and one logarithm a row and split
+    d = attn(tq=2, mq=1, tk=2 * 32768, mk=32768)
+    need = lib.gdn_attn_workspace_size(ctypes.byref(d))
+    rows = 2 * 4
+    n = need // (rows * (64 + 1) * 4)
+    assert n >= 8 and need == (n * rows * 64 * 4 + 255) // 256 * 256 + (n * rows * 4 + 255) // 256 * 256
+    assert attn_fwd(lib, d, ws_bytes=need - 1) == WORKSPACE and attn_fwd(lib, d, ws=None) == WORKSPACE
+    a = addresses(AF)
+    assert attn_fwd(lib, d, ws=a["ws"] + 64) == ALIGN and attn_fwd(lib, d, lse=a["ws"] + 256) == ALIAS
+    assert lib.gdn_attn_workspace_size(ctypes.byref(attn())) == 0
+    assert lib.gdn_attn_workspace_size(None) == 0 and lib.gdn_attn_workspace_size_bwd(None) == 0
+
+
+def test_attn_nothing_to_do(lib):
+    none = {n: None for n in AF}
+    assert attn_fwd(lib, attn(n=0, tq=0, tk=0), **none) == OK
+    assert attn_fwd(lib, attn(tq=0, mq=0), **none) == OK
+    assert attn_bwd(lib, attn(n=0, tq=0, tk=0), **{n: None for n in AB}) == OK
+
+
+def test_attn_torch_refusals():
+    q = torch.zeros(2, 5, 4, 64)
+    with pytest.raises(ValueError, match="device tensor"):
+        api.attention_fwd(q, q, q)
+    with pytest.raises(ValueError, match="must be"):
+        api.attention_fwd(q, q[0], q[0])
+    with pytest.raises(ValueError, match="head size"):
+        api.attention_fwd(q, q[..., :32], q[..., :32])
+    with pytest.raises(TypeError):
+        api.attention_fwd(q.half(), q.half(), q.half())
