@@ -13,7 +13,8 @@ SRCS = [os.path.join(PKG, "csrc", "gdn_api.hip"),    # scan kernels and their C 
         os.path.join(PKG, "csrc", "gdn_block.hip"),  # block projections (hipBLASLt GEMMs)
         os.path.join(PKG, "csrc", "gdn_norm.hip"),   # layer norm
         os.path.join(PKG, "csrc", "gdn_rotary.hip"), # rotary positions
-        os.path.join(PKG, "csrc", "gdn_attn.hip")]   # softmax attention
+        os.path.join(PKG, "csrc", "gdn_attn.hip"),   # softmax attention: entry points, fp32 kernels
+        os.path.join(PKG, "csrc", "gdn_attn_bf16.hip")]   # its bf16 kernels
 LIBS = ["-L/opt/rocm/lib", "-lhipblaslt", "-Wl,-rpath,/opt/rocm/lib"]
 SO = os.path.join(PKG, "libgdn.so")
 

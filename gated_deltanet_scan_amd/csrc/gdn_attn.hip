@@ -392,7 +392,7 @@ gdn_status check_attn(const gdn_attn_desc* d) {
 bool fast(const gdn_attn_desc* d) { return d->io_dtype == GDN_BF16 && d->D >= 32; }
 
 int fwd_rows(const gdn_attn_desc* d) {
-    return kRows;
+    return fast(d) ? attn_fwd_bf16_rows(d->max_q, d->Hq / d->Hk, d->D) : kRows;
 }
 
 // Splits of the key axis: where the row tiles alone would leave compute units
@@ -521,7 +521,8 @@ gdn_status gdn_attn_fwd(const gdn_attn_desc* d, const void* q, const void* k, co
     }
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const bool f32 = d->io_dtype == GDN_F32;
-    st = f32 ? GDN_BY_D(run_fwd, float, a, s) : GDN_BY_D(run_fwd, uint16_t, a, s);
+    // bf16 heads of 16 features are narrower than the bf16 tiles and take the fp32 kernels
+    st = f32 ? GDN_BY_D(run_fwd, float, a, s) : fast(d) ? attn_fwd_bf16(a, s) : run_fwd<uint16_t, 16>(a, s);
     if (st != GDN_OK || a.splits == 1) return st;
     return f32 ? GDN_BY_D(run_join, float, a, s) : GDN_BY_D(run_join, uint16_t, a, s);
 }
