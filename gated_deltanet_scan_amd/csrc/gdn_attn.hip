@@ -570,7 +570,7 @@ gdn_status gdn_attn_bwd(const gdn_attn_desc* d, const void* q, const void* k, co
     a.dq = dq, a.dk = dk, a.dv = dv, a.cu_q = cu_q, a.cu_k = cu_k;
     a.delta = static_cast<float*>(workspace);
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    return d->io_dtype == GDN_F32 ? GDN_BY_D(run_bwd, float, a, s) : GDN_BY_D(run_bwd, uint16_t, a, s);
+    return d->io_dtype == GDN_F32 ? GDN_BY_D(run_bwd, float, a, s) : fast(d) ? attn_bwd_bf16(a, s) : run_bwd<uint16_t, 16>(a, s);
 }
 
 }  // extern "C"

@@ -40,16 +40,15 @@ __device__ __forceinline__ float half_sum(float x) {
 }
 
 // LDS tiles hold rows of D features in 16-byte chunks whose place within the
-// row is permuted by the row, so that neither read meets bank conflicts.
-// Row-wise fragments (eight lanes read one chunk column of eight rows):
+// row is permuted by the row.  Row-wise fragments read one chunk column of
+// eight consecutive rows at a time, transposed ones 32 bytes of four; the
+// permutation sends both to different banks: the row's lowest two bits move
+// pairs of chunks, the third exchanges the two of a pair (at D = 32 two rows
+// share the 128 bytes of one bank cycle, so one bit less of each).
 template <int D>
-__device__ __forceinline__ uint32_t row_chunk(int row, int c) {
-    return (uint32_t)(row * 2 * D) + (uint32_t)((D >= 64 ? c ^ (row & 7) : c ^ ((row >> 1) & 3)) << 4);
-}
-// Transposed fragments (sixteen lanes read 32 bytes of four rows):
-template <int D>
-__device__ __forceinline__ uint32_t col_chunk(int row, int c) {
-    return (uint32_t)(row * 2 * D) + (uint32_t)((D >= 64 ? c ^ (2 * (row & 3)) : c ^ (row & 2)) << 4);
+__device__ __forceinline__ uint32_t chunk_at(int row, int c) {
+    const int f = D >= 64 ? 2 * (row & 3) + ((row >> 2) & 1) : (row & 2) + ((row >> 2) & 1);
+    return (uint32_t)(row * 2 * D) + (uint32_t)((c ^ f) << 4);
 }
 __device__ __forceinline__ u32x4 read_row(const unsigned char* t, uint32_t off) {
     return *reinterpret_cast<const u32x4*>(t + off);
@@ -66,7 +65,7 @@ __device__ __forceinline__ u32x4 read_col(const unsigned char* t, int db, int s,
     const int row = 16 * s + 4 * (j >> 1) + (q >> 2);
     const int c = 4 * db + 2 * (j & 1) + ((q >> 1) & 1);
     const uint32_t sub = (q & 1) * 8;
-    const u32x2 lo = read_tr(t + col_chunk<D>(row, c) + sub), hi = read_tr(t + col_chunk<D>(row + 8, c) + sub);
+    const u32x2 lo = read_tr(t + chunk_at<D>(row, c) + sub), hi = read_tr(t + chunk_at<D>(row + 8, c) + sub);
     return u32x4{lo[0], lo[1], hi[0], hi[1]};
 }
 
@@ -132,8 +131,8 @@ struct Stage {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const int i = tid + j * NT, row = i / (D / 8), c = i % (D / 8);
-            *reinterpret_cast<u32x4*>(kt + row_chunk<D>(row, c)) = k[j];
-            *reinterpret_cast<u32x4*>(vt + col_chunk<D>(row, c)) = v[j];
+            *reinterpret_cast<u32x4*>(kt + chunk_at<D>(row, c)) = k[j];
+            *reinterpret_cast<u32x4*>(vt + chunk_at<D>(row, c)) = v[j];
         }
     }
 };
@@ -199,7 +198,7 @@ __global__ __launch_bounds__(64 * NW, NW * QB <= 8 && QB == 1 ? 2 : 1) void attn
             for (int e = 0; e < KS; ++e)
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    const u32x4 kf = read_row(kt[buf], row_chunk<D>(32 * t + r, 2 * e + h));
+                    const u32x4 kf = read_row(kt[buf], chunk_at<D>(32 * t + r, 2 * e + h));
 #pragma unroll
                     for (int b = 0; b < QB; ++b) s[t][b] = mma(kf, q[b][e], s[t][b]);
                 }
@@ -297,6 +296,253 @@ __global__ __launch_bounds__(64 * NW, NW * QB <= 8 && QB == 1 ? 2 : 1) void attn
     }
 }
 
+// dq, and <d_o, o> for the dk/dv kernel.  Query rows as columns, as in the
+// forward kernel; the key tile is read both ways (S^T = K Q^T, dQ^T += K^T dS^T).
+template <int D, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void attn_dq_kernel(const AttnArgs a) {
+    constexpr int NT = 64 * NW, BM = 32 * NW, KS = D / 16, DB = D / 32, TB = kKeys * D * 2;
+    __shared__ __attribute__((aligned(16))) unsigned char kt[2][TB], vt[2][TB];
+    const Place p = place(a);
+    const Seq z = sequence(a, p.s);
+    const int rows = z.lq * a.G, r0 = p.tile * BM;
+    if (r0 >= rows) return;
+    const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, r = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int w0 = r0 + 32 * wave, row = w0 + r;
+    const bool valid = row < rows;
+    const int upto = visible(a, z, (min(r0 + BM, rows) - 1) / a.G);
+    const int n_first = w0 < rows ? visible(a, z, w0 / a.G) : 0;
+    const int n_last = w0 < rows ? visible(a, z, (min(w0 + 32, rows) - 1) / a.G) : 0;
+    const int n = valid ? visible(a, z, row / a.G) : 0;
+    const int64_t gr = packed_row(a, z, p.hk, valid ? row : r0);
+    const u32x4 none = {0u, 0u, 0u, 0u};
+    u32x4 q[KS], g[KS];
+    float delta = 0.f;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+        q[s] = g[s] = none;
+        if (valid) {
+            q[s] = *reinterpret_cast<const u32x4*>(q_row(a, z, p.hk, row) + 16 * s + 8 * h);
+            g[s] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.d_o) + gr * D + 16 * s + 8 * h);
+            const u32x4 o = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.o) + gr * D + 16 * s + 8 * h);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                delta += __uint_as_float(g[s][j] << 16) * __uint_as_float(o[j] << 16);
+                delta += __uint_as_float(g[s][j] & 0xffff0000u) * __uint_as_float(o[j] & 0xffff0000u);
+            }
+        }
+    }
+    delta = half_sum(delta);
+    if (valid && h == 0) a.delta[gr] = delta;
+    float ls = valid ? a.lse[gr] * kLog2e : INFINITY;
+    if (ls == -INFINITY) ls = INFINITY;                       // a row that saw nothing: p = 0
+    f32x16 acc[DB];
+#pragma unroll
+    for (int e = 0; e < DB; ++e) acc[e] = zero16();
+    const uint16_t* kb = static_cast<const uint16_t*>(a.k) + z.k0 * a.ldk + (int64_t)p.hk * D;
+    const uint16_t* vb = static_cast<const uint16_t*>(a.v) + z.k0 * a.ldv + (int64_t)p.hk * D;
+    const float c2 = a.scale * kLog2e;
+    Stage<D, NT> st;
+    if (upto > 0) {
+        st.load(kb, vb, a.ldk, a.ldv, 0, upto, tid);
+        st.store(kt[0], vt[0], tid);
+    }
+    __syncthreads();
+    int buf = 0;
+    for (int n0 = 0; n0 < upto; n0 += kKeys, buf ^= 1) {
+        const bool more = n0 + kKeys < upto;
+        if (more) st.load(kb, vb, a.ldk, a.ldv, n0 + kKeys, upto, tid);
+        if (n0 < n_last) {
+            const bool mask = n0 + kKeys > n_first;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+                for (int e = 0; e < KS; ++e) {
+                    s = mma(read_row(kt[buf], chunk_at<D>(32 * t + r, 2 * e + h)), q[e], s);
+                    dp = mma(read_row(vt[buf], chunk_at<D>(32 * t + r, 2 * e + h)), g[e], dp);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[i] = exp2_f(__builtin_fmaf(s[i], c2, -ls)) * (dp[i] - delta);
+                if (mask) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (n0 + 32 * t + 8 * (i >> 2) + 4 * h + (i & 3) >= n) s[i] = 0.f;
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const u32x4 ds = pack8(s, 8 * u);
+#pragma unroll
+                    for (int e = 0; e < DB; ++e) acc[e] = mma(read_col<D>(kt[buf], e, 2 * t + u, lane), ds, acc[e]);
+                }
+            }
+        }
+        if (more) st.store(kt[buf ^ 1], vt[buf ^ 1], tid);
+        __syncthreads();
+    }
+    if (!valid) return;
+#pragma unroll
+    for (int e = 0; e < DB; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.dq) + gr * D + 32 * e + 8 * i + 4 * h) =
+                u32x2{pack_bf16x2(acc[e][4 * i] * a.scale, acc[e][4 * i + 1] * a.scale),
+                      pack_bf16x2(acc[e][4 * i + 2] * a.scale, acc[e][4 * i + 3] * a.scale)};
+}
+
+// Staging of 64 packed query rows: q, d_o, and each row's logarithm and
+// <d_o, o>.  A row's token is found from the tile's first by a multiplication
+// (place within the tile times 2^32 / G, exact for G <= 2^15).
+template <int D, int NT>
+struct RowStage {
+    static constexpr int N = kKeys * D / 8 / NT;
+    u32x4 q[N], g[N];
+    float ls, dl;
+    __device__ __forceinline__ void load(const AttnArgs& a, const Seq& z, int hk, int r0, int rows, uint32_t inv,
+                                         int tid) {
+        const int i0 = r0 / a.G, g0 = r0 - i0 * a.G;
+        const rsrc_t rq = make_rsrc(static_cast<const uint16_t*>(a.q) + (z.q0 + i0) * a.ldq + (int64_t)hk * a.G * D,
+                                    0x7ffffff0u);
+        const rsrc_t rg = make_rsrc(static_cast<const uint16_t*>(a.d_o) +
+                                        ((z.q0 + i0) * a.Hq + (int64_t)hk * a.G) * D, 0x7ffffff0u);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int i = tid + j * NT, rr = i / (D / 8), c = i % (D / 8);
+            const uint32_t x = (uint32_t)(g0 + rr);
+            const uint32_t tok = a.G == 1 ? x : __umulhi(x, inv), gg = x - tok * a.G;
+            const bool in = r0 + rr < rows;                    // rows past the last read as zeros
+            const uint32_t at = gg * (2 * D) + c * 16;
+            q[j] = __builtin_amdgcn_raw_buffer_load_b128(rq, in ? tok * (uint32_t)(a.ldq * 2) + at : 0x80000000u, 0, 0);
+            g[j] = __builtin_amdgcn_raw_buffer_load_b128(rg, in ? tok * (uint32_t)(a.Hq * D * 2) + at : 0x80000000u, 0, 0);
+        }
+        ls = 0.f, dl = 0.f;
+        if (tid < kKeys && r0 + tid < rows) {
+            const int64_t gr = packed_row(a, z, hk, r0 + tid);
+            ls = a.lse[gr] * kLog2e;
+            if (ls == -INFINITY) ls = INFINITY;                // a row that saw nothing: p = 0
+            dl = a.delta[gr];
+        }
+    }
+    __device__ __forceinline__ void store(unsigned char* qt, unsigned char* gt, float* lt, float* dt, int tid) const {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int i = tid + j * NT, rr = i / (D / 8), c = i % (D / 8);
+            *reinterpret_cast<u32x4*>(qt + chunk_at<D>(rr, c)) = q[j];
+            *reinterpret_cast<u32x4*>(gt + chunk_at<D>(rr, c)) = g[j];
+        }
+        if (tid < kKeys) {
+            lt[tid] = ls;
+            dt[tid] = dl;
+        }
+    }
+};
+
+// dk and dv.  A wave's 32 keys as columns, with K and V in registers; the
+// packed query rows of all heads that share them walk through LDS, read both
+// ways (S = Q K^T and dP = dO V^T by rows; dV^T += dO^T P, dK^T += Q^T dS).
+template <int D, int NW>
+__global__ __launch_bounds__(64 * NW, 1) void attn_dkv_kernel(const AttnArgs a) {
+    constexpr int NT = 64 * NW, BN = 32 * NW, KS = D / 16, DB = D / 32, TB = kKeys * D * 2;
+    __shared__ __attribute__((aligned(16))) unsigned char qt[2][TB], gt[2][TB];
+    __shared__ __attribute__((aligned(16))) float lt[2][kKeys], dt[2][kKeys];
+    Place p = place(a);
+    p.tile = a.tiles - 1 - p.tile;                            // the first keys see the most rows
+    const Seq z = sequence(a, p.s);
+    const int k0 = p.tile * BN;
+    if (k0 >= z.lk) return;
+    const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, r = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int w0 = k0 + 32 * wave, key = w0 + r;
+    const bool valid = key < z.lk;
+    const int rows = z.lq * a.G;
+    // rows below w_first see none of the wave's keys, rows from w_all on see them all
+    const int w_first = w0 < z.lk ? first_query(a, z, w0) * a.G : rows;
+    const int w_all = w0 < z.lk ? first_query(a, z, min(w0 + 32, z.lk) - 1) * a.G : rows;
+    const int from = first_query(a, z, min(key, z.lk - 1)) * a.G;
+    const u32x4 none = {0u, 0u, 0u, 0u};
+    u32x4 kf[KS], vf[KS];
+    f32x16 ak[DB], av[DB];
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+        const int64_t kr = z.k0 + (valid ? key : 0);
+        kf[s] = vf[s] = none;
+        if (valid) {
+            kf[s] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.k) + kr * a.ldk +
+                                                    (int64_t)p.hk * D + 16 * s + 8 * h);
+            vf[s] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.v) + kr * a.ldv +
+                                                    (int64_t)p.hk * D + 16 * s + 8 * h);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < DB; ++e) ak[e] = av[e] = zero16();
+    const float c2 = a.scale * kLog2e;
+    const uint32_t inv = a.G == 1 ? 0u : (uint32_t)((0x100000000ull + a.G - 1) / a.G);
+    RowStage<D, NT> st;
+    const int start = min(first_query(a, z, k0) * a.G, rows) / kKeys * kKeys;
+    if (start < rows) {
+        st.load(a, z, p.hk, start, rows, inv, tid);
+        st.store(qt[0], gt[0], lt[0], dt[0], tid);
+    }
+    __syncthreads();
+    int buf = 0;
+    for (int r0 = start; r0 < rows; r0 += kKeys, buf ^= 1) {
+        const bool more = r0 + kKeys < rows;
+        if (more) st.load(a, z, p.hk, r0 + kKeys, rows, inv, tid);
+        if (r0 + kKeys > w_first) {
+            const bool mask = r0 < w_all;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+                for (int e = 0; e < KS; ++e) {
+                    s = mma(read_row(qt[buf], chunk_at<D>(32 * t + r, 2 * e + h)), kf[e], s);
+                    dp = mma(read_row(gt[buf], chunk_at<D>(32 * t + r, 2 * e + h)), vf[e], dp);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const f32x4 l4 = *reinterpret_cast<const f32x4*>(&lt[buf][32 * t + 8 * i + 4 * h]);
+                    const f32x4 d4 = *reinterpret_cast<const f32x4*>(&dt[buf][32 * t + 8 * i + 4 * h]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float pr = exp2_f(__builtin_fmaf(s[4 * i + j], c2, -l4[j]));
+                        dp[4 * i + j] = pr * (dp[4 * i + j] - d4[j]);
+                        s[4 * i + j] = pr;
+                    }
+                }
+                if (mask) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (r0 + 32 * t + 8 * (i >> 2) + 4 * h + (i & 3) < from) s[i] = dp[i] = 0.f;
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const u32x4 pp = pack8(s, 8 * u), ds = pack8(dp, 8 * u);
+#pragma unroll
+                    for (int e = 0; e < DB; ++e) {
+                        av[e] = mma(read_col<D>(gt[buf], e, 2 * t + u, lane), pp, av[e]);
+                        ak[e] = mma(read_col<D>(qt[buf], e, 2 * t + u, lane), ds, ak[e]);
+                    }
+                }
+            }
+        }
+        if (more) st.store(qt[buf ^ 1], gt[buf ^ 1], lt[buf ^ 1], dt[buf ^ 1], tid);
+        __syncthreads();
+    }
+    if (!valid) return;
+    const int64_t at = ((z.ko + key) * a.Hk + p.hk) * D;
+#pragma unroll
+    for (int e = 0; e < DB; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int d = 32 * e + 8 * i + 4 * h;
+            *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.dk) + at + d) =
+                u32x2{pack_bf16x2(ak[e][4 * i] * a.scale, ak[e][4 * i + 1] * a.scale),
+                      pack_bf16x2(ak[e][4 * i + 2] * a.scale, ak[e][4 * i + 3] * a.scale)};
+            *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.dv) + at + d) =
+                u32x2{pack_bf16x2(av[e][4 * i], av[e][4 * i + 1]), pack_bf16x2(av[e][4 * i + 2], av[e][4 * i + 3])};
+        }
+}
+
 bool grid_of(int64_t n, unsigned* g) {
     if (n > INT32_MAX) return false;
     *g = (unsigned)n;
@@ -312,6 +558,18 @@ gdn_status launch_fwd(AttnArgs a, hipStream_t s) {
     return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
+template <int D>
+gdn_status launch_bwd(AttnArgs a, hipStream_t s) {
+    unsigned grid;
+    a.tiles = (int)(((int64_t)a.max_q * a.G + 127) / 128);
+    if (!grid_of((int64_t)a.tiles * a.Hk * a.n_seq, &grid)) return GDN_ERR_UNSUPPORTED;
+    if (grid) hipLaunchKernelGGL((attn_dq_kernel<D, 4>), dim3(grid), dim3(256), 0, s, a);
+    a.tiles = (a.max_k + 127) / 128;
+    if (!grid_of((int64_t)a.tiles * a.Hk * a.n_seq, &grid)) return GDN_ERR_UNSUPPORTED;
+    if (grid) hipLaunchKernelGGL((attn_dkv_kernel<D, 4>), dim3(grid), dim3(256), 0, s, a);
+    return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
 }  // namespace
 
 int attn_fwd_bf16_rows(int max_q, int G, int D) { return 128; }
@@ -320,6 +578,12 @@ gdn_status attn_fwd_bf16(const AttnArgs& a, hipStream_t s) {
     if (a.D == 32) return launch_fwd<32, 1, 4>(a, s);
     if (a.D == 64) return launch_fwd<64, 1, 4>(a, s);
     return launch_fwd<128, 1, 4>(a, s);
+}
+
+gdn_status attn_bwd_bf16(const AttnArgs& a, hipStream_t s) {
+    if (a.D == 32) return launch_bwd<32>(a, s);
+    if (a.D == 64) return launch_bwd<64>(a, s);
+    return launch_bwd<128>(a, s);
 }
 
 }  // namespace gdnattn
