@@ -78,27 +78,11 @@ __device__ __forceinline__ void stage(float (*t)[D + 4], const T* base, int64_t 
     }
 }
 
-// (sequence, kv head, tile, split) of a workgroup; the tile runs fastest, from
-// the last (the longest under a causal mask) to the first.
-struct Place {
-    int s, hk, tile, split;
-};
-__device__ __forceinline__ Place place(const AttnArgs& a) {
-    unsigned b = blockIdx.x;
-    Place p;
-    p.tile = a.tiles - 1 - (int)(b % a.tiles);
-    b /= a.tiles;
-    p.split = (int)(b % a.splits);
-    b /= a.splits;
-    p.hk = (int)(b % a.Hk);
-    p.s = (int)(b / a.Hk);
-    return p;
-}
-
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void attn_fwd_f32_kernel(const AttnArgs a) {
     __shared__ float kt[kTile][D + 4], vt[kTile][D + 4];
-    const Place p = place(a);
+    const Place p = find_place<false>(a, kRows);
+    if (p.s < 0) return;
     const Seq z = sequence(a, p.s);
     const int rows = z.lq * a.G, r0 = p.tile * kRows;
     if (r0 >= rows) return;
@@ -220,7 +204,8 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(const AttnArgs a) {
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void attn_dq_f32_kernel(const AttnArgs a) {
     __shared__ float kt[kTile][D + 4], vt[kTile][D + 4];
-    const Place p = place(a);
+    const Place p = find_place<false>(a, kRows);
+    if (p.s < 0) return;
     const Seq z = sequence(a, p.s);
     const int rows = z.lq * a.G, r0 = p.tile * kRows;
     if (r0 >= rows) return;
@@ -289,7 +274,8 @@ __global__ __launch_bounds__(kThreads) void attn_dkv_f32_kernel(const AttnArgs a
     __shared__ float qt[kTile][D + 4], dt[kTile][D + 4];
     __shared__ float ls[kTile], dl[kTile];
     __shared__ int nv[kTile];
-    const Place p = place(a);
+    const Place p = find_place<true>(a, kRows);
+    if (p.s < 0) return;
     const Seq z = sequence(a, p.s);
     const int k0 = p.tile * kRows;
     if (k0 >= z.lk) return;
@@ -406,6 +392,18 @@ int fwd_splits(const gdn_attn_desc* d) {
     return (int)std::min<int64_t>(std::min<int64_t>(most, (512 + units - 1) / std::max<int64_t>(units, 1)), 128);
 }
 
+// Splits of the query rows in the bf16 dk/dv kernel.  Its workgroups each walk
+// all the rows that see their keys; with few key tiles (grouped heads: few
+// heads with many rows each) that leaves compute units idle and the first
+// tiles' long walks last, so below two workgroups a unit the rows are split for
+// about four.  A split's fp32 sums cost 16 D bytes a key, its products 8 D
+// flops a (row, key): from 1024 rows a split on, the former stay a small part.
+// The sizes do not depend on the lengths on the device, nor on whether the
+// sequences are packed (uniform ones count the same tiles).
+int bwd_splits(const gdn_attn_desc* d) {
+    return fast(d) ? attn_bwd_bf16_splits(d->total_k, d->max_q, d->max_k, d->n_seq, d->Hk, d->Hq / d->Hk) : 1;
+}
+
 AttnArgs fill(const gdn_attn_desc* d) {
     AttnArgs a = {};
     a.total_q = d->total_q, a.total_k = d->total_k;
@@ -418,7 +416,7 @@ AttnArgs fill(const gdn_attn_desc* d) {
     a.causal = (d->flags & GDN_FLAG_ATTN_CAUSAL) ? 1 : 0;
     a.block = a.causal ? d->causal_block : 1;
     a.scale = d->scale;
-    a.splits = 1;
+    a.splits = a.k_splits = 1;
     return a;
 }
 
@@ -441,8 +439,8 @@ bool grid_of(int64_t n, unsigned* g) {
 template <typename T, int D>
 gdn_status run_fwd(AttnArgs a, hipStream_t s) {
     unsigned grid;
-    a.tiles = (int)(((int64_t)a.max_q * a.G + kRows - 1) / kRows);
-    if (!grid_of((int64_t)a.tiles * a.splits * a.Hk * a.n_seq, &grid)) return GDN_ERR_UNSUPPORTED;
+    const int64_t n = places(a.total_q * a.G, (int64_t)a.max_q * a.G, a.n_seq, kRows, a.cu_q, &a.tiles);
+    if (!grid_of(n * a.splits * a.Hk, &grid)) return GDN_ERR_UNSUPPORTED;
     hipLaunchKernelGGL((attn_fwd_f32_kernel<T, D>), dim3(grid), dim3(kThreads), 0, s, a);
     return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
@@ -456,11 +454,11 @@ gdn_status run_join(const AttnArgs& a, hipStream_t s) {
 template <typename T, int D>
 gdn_status run_bwd(AttnArgs a, hipStream_t s) {
     unsigned grid;
-    a.tiles = (int)(((int64_t)a.max_q * a.G + kRows - 1) / kRows);
-    if (!grid_of((int64_t)a.tiles * a.Hk * a.n_seq, &grid)) return GDN_ERR_UNSUPPORTED;
+    int64_t n = places(a.total_q * a.G, (int64_t)a.max_q * a.G, a.n_seq, kRows, a.cu_q, &a.tiles);
+    if (!grid_of(n * a.Hk, &grid)) return GDN_ERR_UNSUPPORTED;
     if (grid) hipLaunchKernelGGL((attn_dq_f32_kernel<T, D>), dim3(grid), dim3(kThreads), 0, s, a);
-    a.tiles = (a.max_k + kRows - 1) / kRows;
-    if (!grid_of((int64_t)a.tiles * a.Hk * a.n_seq, &grid)) return GDN_ERR_UNSUPPORTED;
+    n = places(a.total_k, a.max_k, a.n_seq, kRows, a.cu_k, &a.tiles);
+    if (!grid_of(n * a.Hk, &grid)) return GDN_ERR_UNSUPPORTED;
     if (grid) hipLaunchKernelGGL((attn_dkv_f32_kernel<T, D>), dim3(grid), dim3(kThreads), 0, s, a);
     return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
@@ -529,7 +527,8 @@ gdn_status gdn_attn_fwd(const gdn_attn_desc* d, const void* q, const void* k, co
 
 size_t gdn_attn_workspace_size_bwd(const gdn_attn_desc* d) {
     if (check_attn(d) != GDN_OK || d->n_seq == 0) return 0;
-    return round256((size_t)d->total_q * d->Hq * 4);
+    const size_t n = bwd_splits(d);
+    return round256((size_t)d->total_q * d->Hq * 4) + (n > 1 ? 2 * round256(n * d->total_k * d->Hk * d->D * 4) : 0);
 }
 
 gdn_status gdn_attn_bwd(const gdn_attn_desc* d, const void* q, const void* k, const void* v, const void* o,
@@ -569,6 +568,12 @@ gdn_status gdn_attn_bwd(const gdn_attn_desc* d, const void* q, const void* k, co
     a.q = q, a.k = k, a.v = v, a.o = o, a.lse = const_cast<float*>(lse), a.d_o = dO;
     a.dq = dq, a.dk = dk, a.dv = dv, a.cu_q = cu_q, a.cu_k = cu_k;
     a.delta = static_cast<float*>(workspace);
+    a.k_splits = bwd_splits(d);
+    if (a.k_splits > 1) {
+        unsigned char* w = static_cast<unsigned char*>(workspace) + round256((size_t)d->total_q * d->Hq * 4);
+        a.part_k = reinterpret_cast<float*>(w);
+        a.part_v = reinterpret_cast<float*>(w + round256((size_t)a.k_splits * d->total_k * d->Hk * d->D * 4));
+    }
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     return d->io_dtype == GDN_F32 ? GDN_BY_D(run_bwd, float, a, s) : fast(d) ? attn_bwd_bf16(a, s) : run_bwd<uint16_t, 16>(a, s);
 }

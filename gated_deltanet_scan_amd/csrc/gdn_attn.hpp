@@ -24,12 +24,13 @@ struct AttnArgs {
     float* lse;                          // [total_q][Hq], natural logarithm (forward: may be NULL)
     float* delta;                        // [total_q][Hq] <d_o, o> (backward)
     float *part_o, *part_lse;            // splits > 1: [splits][total_q Hq][D], [splits][total_q Hq]
+    float *part_k, *part_v;              // k_splits > 1: [k_splits][total_k Hk][D] each (backward)
     const int32_t *cu_q, *cu_k, *k_len;
     int64_t total_q, total_k, ldq, ldk, ldv, k_room;
     int n_seq, Hq, Hk, G, D;
     int max_q, max_k;
     int tiles;                           // row (or key) tiles of the longest sequence
-    int splits;
+    int splits, k_splits;                // of the key axis (forward), of the row axis (dk, dv)
     int causal, block;
     float scale;
 };
@@ -47,6 +48,10 @@ __device__ __forceinline__ void seq_range(const int32_t* cu, int s, int64_t tota
         len = most;
     }
 }
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)x), hi = __builtin_amdgcn_readfirstlane((int)(x >> 32));
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
 struct Seq {
     int64_t q0, k0, ko;                  // first query, first key, and its place in dk and dv
     int lq, lk;
@@ -57,6 +62,9 @@ __device__ __forceinline__ Seq sequence(const AttnArgs& a, int s) {
     seq_range(a.cu_k, s, a.total_k, a.max_k, z.ko, z.lk);
     z.k0 = a.cu_k ? z.ko : (int64_t)s * a.k_room;
     if (a.k_len) z.lk = min(z.lk, max(a.k_len[s], 0));
+    // one sequence a workgroup: scalar registers
+    z.q0 = uniform(z.q0), z.k0 = uniform(z.k0), z.ko = uniform(z.ko);
+    z.lq = __builtin_amdgcn_readfirstlane(z.lq), z.lk = __builtin_amdgcn_readfirstlane(z.lk);
     return z;
 }
 // Keys that query i sees.
@@ -79,12 +87,122 @@ __device__ __forceinline__ void split_range(int upto, int tile, int n, int sp, i
     hi = min(lo + per * tile, upto);
 }
 
+// What a workgroup computes: one tile of rows (queries) or of keys of one
+// sequence and key head, one split of it.  s < 0: nothing.
+struct Place {
+    int s, hk, split, tile;
+};
+__device__ __forceinline__ int wave_sum_i(int x) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) x += __shfl_xor(x, d);
+    return __builtin_amdgcn_readfirstlane(x);
+}
+// Tiles of `size` of sequence s, along its packed query rows or its keys.
+template <bool KEYS>
+__device__ __forceinline__ int tiles_of(const AttnArgs& a, int s, int size) {
+    int64_t at;
+    int len;
+    if (KEYS)
+        seq_range(a.cu_k, s, a.total_k, a.max_k, at, len);
+    else
+        seq_range(a.cu_q, s, a.total_q, a.max_q, at, len);
+    return KEYS ? (len + size - 1) / size : (len * a.G + size - 1) / size;
+}
+// The key head runs fastest: workgroups go round the eight XCDs in turn, so
+// with eight key heads or a multiple of eight each XCD's L2 holds the keys of
+// its own heads only.  Then the splits, then the tiles: level by level across
+// the sequences, the longest sequences' last tiles first (under a causal mask
+// tile L of any sequence costs about L, so long work starts early), and only
+// tiles that exist.  (A grid over (level, sequence) with its empty places left
+// in put all the long sequences of one packed batch on four of the XCDs.)
+// Key tiles run the other way, since the first keys are seen by the most rows.
+template <bool KEYS>
+__device__ __forceinline__ Place find_place(const AttnArgs& a, int size) {
+    unsigned b = blockIdx.x;
+    Place p;
+    p.hk = (int)(b % (unsigned)a.Hk);
+    b /= (unsigned)a.Hk;
+    const unsigned splits = KEYS ? a.k_splits : a.splits;
+    p.split = (int)(b % splits);
+    const int w = (int)(b / splits);
+    const int32_t* cu = KEYS ? a.cu_k : a.cu_q;
+    int count, level;                                     // tiles of the sequence, and ours
+    if (!cu || a.tiles == 1) {
+        p.s = w % a.n_seq;
+        count = a.tiles;
+        level = a.tiles - 1 - w / a.n_seq;
+    } else if (a.n_seq <= 64) {
+        const int lane = threadIdx.x & 63;
+        const int t = lane < a.n_seq ? tiles_of<KEYS>(a, lane, size) : 0;
+        // the highest level with more than w tiles at it or above
+        int lo = 0, hi = a.tiles, above = 0;              // count(hi) <= w, `above` of it
+        if (wave_sum_i(t) <= w) {
+            p.s = -1;
+            return p;
+        }
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            const int n = wave_sum_i(max(0, t - mid));
+            if (n > w) {
+                lo = mid;
+            } else {
+                hi = mid;
+                above = n;
+            }
+        }
+        level = lo;
+        const uint64_t at = __ballot(t > level);
+        const int before = __popcll(at & ((1ull << lane) - 1));
+        p.s = __builtin_amdgcn_readfirstlane(
+            __ffsll((unsigned long long)__ballot(t > level && before == w - above)) - 1);
+        count = __builtin_amdgcn_readlane(t, p.s);
+    } else {
+        // many sequences: in their order, which by itself spreads the work
+        const int lane = threadIdx.x & 63;
+        int base = 0;
+        p.s = -1;
+        count = level = 0;
+        for (int s0 = 0; s0 < a.n_seq; s0 += 64) {
+            const int t = s0 + lane < a.n_seq ? tiles_of<KEYS>(a, s0 + lane, size) : 0;
+            int scan = t;
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2) {
+                const int up = __shfl_up(scan, d);
+                if (lane >= d) scan += up;
+            }
+            const int total = __builtin_amdgcn_readlane(scan, 63);
+            if (w < base + total) {
+                const int hit =
+                    __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)__ballot(base + scan > w)) - 1);
+                count = __builtin_amdgcn_readlane(t, hit);
+                level = base + __builtin_amdgcn_readlane(scan, hit) - 1 - w;
+                p.s = s0 + hit;
+                break;
+            }
+            base += total;
+        }
+        if (p.s < 0) return p;
+    }
+    p.s = __builtin_amdgcn_readfirstlane(p.s);
+    p.tile = __builtin_amdgcn_readfirstlane(KEYS ? count - 1 - level : level);
+    return p;
+}
+// Workgroups of one split and key head that find_place hands out: no more than
+// every sequence's share of the tensor, rounded up.
+inline int64_t places(int64_t rows, int64_t most, int n_seq, int size, bool packed, int* tiles) {
+    *tiles = (int)((most + size - 1) / size);
+    const int64_t all = (int64_t)*tiles * n_seq;
+    return packed && *tiles > 1 ? (all < rows / size + n_seq ? all : rows / size + n_seq) : all;
+}
+
 __device__ __forceinline__ float exp2_f(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float log2_f(float x) { return __builtin_amdgcn_logf(x); }
 
 // Kernels in bf16 matrix instructions (gdn_attn_bf16.hip), D in {32, 64, 128}.
 gdn_status attn_fwd_bf16(const AttnArgs& a, hipStream_t s);
 gdn_status attn_bwd_bf16(const AttnArgs& a, hipStream_t s);
+// Splits of the row axis in the dk/dv kernel.
+int attn_bwd_bf16_splits(int64_t total_k, int max_q, int max_k, int n_seq, int Hk, int G);
 // Row tile of the forward kernel that these arguments select.
 int attn_fwd_bf16_rows(int max_q, int G, int D);
 

@@ -19,7 +19,11 @@ namespace {
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 
+// The base must be the same in all lanes and known to be (a descriptor in vector
+// registers turns every load into a loop over its values).
 __device__ __forceinline__ rsrc_t make_rsrc(const void* p, uint32_t bytes) {
+    p = reinterpret_cast<const void*>(uniform((int64_t)p));
+    bytes = (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes);
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
 }
 __device__ __forceinline__ f32x16 mma(u32x4 x, u32x4 y, f32x16 c) {
@@ -50,24 +54,35 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int c) {
     const int f = D >= 64 ? 2 * (row & 3) + ((row >> 2) & 1) : (row & 2) + ((row >> 2) & 1);
     return (uint32_t)(row * 2 * D) + (uint32_t)((c ^ f) << 4);
 }
-__device__ __forceinline__ u32x4 read_row(const unsigned char* t, uint32_t off) {
-    return *reinterpret_cast<const u32x4*>(t + off);
-}
 __device__ __forceinline__ u32x2 read_tr(const unsigned char* p) {
     typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
     return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p));
 }
-// Operand A of a transposed tile: features 32 db + r, rows 16 s + 4 h + 0..3 and
-// 16 s + 8 + 4 h + 0..3.
+// A lane's addresses in a tile.  The permutation acts on the low bits of the
+// chunk alone, so a few registers hold all of them and the rest is constant.
 template <int D>
-__device__ __forceinline__ u32x4 read_col(const unsigned char* t, int db, int s, int lane) {
-    const int j = lane >> 4, q = lane & 15;
-    const int row = 16 * s + 4 * (j >> 1) + (q >> 2);
-    const int c = 4 * db + 2 * (j & 1) + ((q >> 1) & 1);
-    const uint32_t sub = (q & 1) * 8;
-    const u32x2 lo = read_tr(t + chunk_at<D>(row, c) + sub), hi = read_tr(t + chunk_at<D>(row + 8, c) + sub);
-    return u32x4{lo[0], lo[1], hi[0], hi[1]};
-}
+struct Addr {
+    static constexpr int NR = D >= 64 ? 4 : 2, NC = D >= 64 ? 2 : 1;
+    uint32_t row[NR], col[NC];
+    __device__ __forceinline__ void init(int lane) {
+        const int h = lane >> 5, r = lane & 31, j = lane >> 4, q = lane & 15;
+#pragma unroll
+        for (int x = 0; x < NR; ++x) row[x] = chunk_at<D>(r, 2 * x + h);
+#pragma unroll
+        for (int x = 0; x < NC; ++x)
+            col[x] = chunk_at<D>(4 * (j >> 1) + (q >> 2), 4 * x + 2 * (j & 1) + ((q >> 1) & 1)) + (q & 1) * 8;
+    }
+    // rows 32 t + r, features 16 e + 8 h .. + 7
+    __device__ __forceinline__ u32x4 rows(const unsigned char* tile, int t, int e) const {
+        return *reinterpret_cast<const u32x4*>(tile + row[e % NR] + (e / NR) * 128 + t * 64 * D);
+    }
+    // features 32 e + r, rows 16 s + 4 h + 0..3 and 16 s + 8 + 4 h + 0..3
+    __device__ __forceinline__ u32x4 cols(const unsigned char* tile, int e, int s) const {
+        const unsigned char* p = tile + col[e % NC] + (e / NC) * 128 + s * 32 * D;
+        const u32x2 lo = read_tr(p), hi = read_tr(p + 16 * D);
+        return u32x4{lo[0], lo[1], hi[0], hi[1]};
+    }
+};
 
 // Eight values as one bf16 operand.
 __device__ __forceinline__ u32x4 pack8(const f32x16& x, int at) {
@@ -81,25 +96,6 @@ __device__ __forceinline__ int64_t packed_row(const AttnArgs& a, const Seq& z, i
 }
 __device__ __forceinline__ const uint16_t* q_row(const AttnArgs& a, const Seq& z, int hk, int r) {
     return static_cast<const uint16_t*>(a.q) + (z.q0 + r / a.G) * a.ldq + (int64_t)(hk * a.G + r % a.G) * a.D;
-}
-
-// (kv head, sequence, split, tile) of a workgroup, the head fastest: workgroups
-// go round the eight XCDs in turn, so with eight heads or a multiple each
-// XCD's L2 holds the keys of its own heads only.  Tiles run slowest, from the
-// last (under a causal mask the longest) to the first.
-struct Place {
-    int s, hk, tile, split;
-};
-__device__ __forceinline__ Place place(const AttnArgs& a) {
-    unsigned b = blockIdx.x;
-    Place p;
-    p.hk = (int)(b % (unsigned)a.Hk);
-    b /= (unsigned)a.Hk;
-    p.s = (int)(b % (unsigned)a.n_seq);
-    b /= (unsigned)a.n_seq;
-    p.split = (int)(b % (unsigned)a.splits);
-    p.tile = a.tiles - 1 - (int)(b / (unsigned)a.splits);
-    return p;
 }
 
 constexpr int kKeys = 64;       // keys per tile
@@ -143,7 +139,8 @@ template <int D, int QB, int NW>
 __global__ __launch_bounds__(64 * NW, NW * QB <= 8 && QB == 1 ? 2 : 1) void attn_fwd_kernel(const AttnArgs a) {
     constexpr int NT = 64 * NW, BM = 32 * QB * NW, KS = D / 16, DB = D / 32, TB = kKeys * D * 2;
     __shared__ __attribute__((aligned(16))) unsigned char kt[2][TB], vt[2][TB];
-    const Place p = place(a);
+    const Place p = find_place<false>(a, BM);
+    if (p.s < 0) return;
     const Seq z = sequence(a, p.s);
     const int rows = z.lq * a.G, r0 = p.tile * BM;
     if (r0 >= rows) return;
@@ -178,6 +175,8 @@ __global__ __launch_bounds__(64 * NW, NW * QB <= 8 && QB == 1 ? 2 : 1) void attn
     const uint16_t* kb = static_cast<const uint16_t*>(a.k) + z.k0 * a.ldk + (int64_t)p.hk * D;
     const uint16_t* vb = static_cast<const uint16_t*>(a.v) + z.k0 * a.ldv + (int64_t)p.hk * D;
     const float c2 = a.scale * kLog2e;
+    Addr<D> ad;
+    ad.init(lane);
     Stage<D, NT> st;
     if (lo < hi) {
         st.load(kb, vb, a.ldk, a.ldv, lo, hi, tid);
@@ -198,7 +197,7 @@ __global__ __launch_bounds__(64 * NW, NW * QB <= 8 && QB == 1 ? 2 : 1) void attn
             for (int e = 0; e < KS; ++e)
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    const u32x4 kf = read_row(kt[buf], chunk_at<D>(32 * t + r, 2 * e + h));
+                    const u32x4 kf = ad.rows(kt[buf], t, e);
 #pragma unroll
                     for (int b = 0; b < QB; ++b) s[t][b] = mma(kf, q[b][e], s[t][b]);
                 }
@@ -257,7 +256,7 @@ __global__ __launch_bounds__(64 * NW, NW * QB <= 8 && QB == 1 ? 2 : 1) void attn
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
                     for (int e = 0; e < DB; ++e) {
-                        const u32x4 vf = read_col<D>(vt[buf], e, 2 * t + u, lane);
+                        const u32x4 vf = ad.cols(vt[buf], e, 2 * t + u);
 #pragma unroll
                         for (int b = 0; b < QB; ++b) acc[b][e] = mma(vf, pf[t][b][u], acc[b][e]);
                     }
@@ -302,7 +301,8 @@ template <int D, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void attn_dq_kernel(const AttnArgs a) {
     constexpr int NT = 64 * NW, BM = 32 * NW, KS = D / 16, DB = D / 32, TB = kKeys * D * 2;
     __shared__ __attribute__((aligned(16))) unsigned char kt[2][TB], vt[2][TB];
-    const Place p = place(a);
+    const Place p = find_place<false>(a, BM);
+    if (p.s < 0) return;
     const Seq z = sequence(a, p.s);
     const int rows = z.lq * a.G, r0 = p.tile * BM;
     if (r0 >= rows) return;
@@ -342,6 +342,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_dq_kernel(const AttnArgs a) {
     const uint16_t* kb = static_cast<const uint16_t*>(a.k) + z.k0 * a.ldk + (int64_t)p.hk * D;
     const uint16_t* vb = static_cast<const uint16_t*>(a.v) + z.k0 * a.ldv + (int64_t)p.hk * D;
     const float c2 = a.scale * kLog2e;
+    Addr<D> ad;
+    ad.init(lane);
     Stage<D, NT> st;
     if (upto > 0) {
         st.load(kb, vb, a.ldk, a.ldv, 0, upto, tid);
@@ -359,8 +361,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_dq_kernel(const AttnArgs a) {
                 f32x16 s = zero16(), dp = zero16();
 #pragma unroll
                 for (int e = 0; e < KS; ++e) {
-                    s = mma(read_row(kt[buf], chunk_at<D>(32 * t + r, 2 * e + h)), q[e], s);
-                    dp = mma(read_row(vt[buf], chunk_at<D>(32 * t + r, 2 * e + h)), g[e], dp);
+                    s = mma(ad.rows(kt[buf], t, e), q[e], s);
+                    dp = mma(ad.rows(vt[buf], t, e), g[e], dp);
                 }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) s[i] = exp2_f(__builtin_fmaf(s[i], c2, -ls)) * (dp[i] - delta);
@@ -373,7 +375,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_dq_kernel(const AttnArgs a) {
                 for (int u = 0; u < 2; ++u) {
                     const u32x4 ds = pack8(s, 8 * u);
 #pragma unroll
-                    for (int e = 0; e < DB; ++e) acc[e] = mma(read_col<D>(kt[buf], e, 2 * t + u, lane), ds, acc[e]);
+                    for (int e = 0; e < DB; ++e) acc[e] = mma(ad.cols(kt[buf], e, 2 * t + u), ds, acc[e]);
                 }
             }
         }
@@ -390,12 +392,13 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_dq_kernel(const AttnArgs a) {
                       pack_bf16x2(acc[e][4 * i + 2] * a.scale, acc[e][4 * i + 3] * a.scale)};
 }
 
-// Staging of 64 packed query rows: q, d_o, and each row's logarithm and
+// Staging of RT packed query rows: q, d_o, and each row's logarithm and
 // <d_o, o>.  A row's token is found from the tile's first by a multiplication
 // (place within the tile times 2^32 / G, exact for G <= 2^15).
-template <int D, int NT>
+template <int D, int NT, int RT>
 struct RowStage {
-    static constexpr int N = kKeys * D / 8 / NT;
+    static constexpr int N = RT * D / 8 / NT;
+    static_assert(N >= 1 && RT <= NT, "every thread stages something");
     u32x4 q[N], g[N];
     float ls, dl;
     __device__ __forceinline__ void load(const AttnArgs& a, const Seq& z, int hk, int r0, int rows, uint32_t inv,
@@ -416,7 +419,7 @@ struct RowStage {
             g[j] = __builtin_amdgcn_raw_buffer_load_b128(rg, in ? tok * (uint32_t)(a.Hq * D * 2) + at : 0x80000000u, 0, 0);
         }
         ls = 0.f, dl = 0.f;
-        if (tid < kKeys && r0 + tid < rows) {
+        if (tid < RT && r0 + tid < rows) {
             const int64_t gr = packed_row(a, z, hk, r0 + tid);
             ls = a.lse[gr] * kLog2e;
             if (ls == -INFINITY) ls = INFINITY;                // a row that saw nothing: p = 0
@@ -430,7 +433,7 @@ struct RowStage {
             *reinterpret_cast<u32x4*>(qt + chunk_at<D>(rr, c)) = q[j];
             *reinterpret_cast<u32x4*>(gt + chunk_at<D>(rr, c)) = g[j];
         }
-        if (tid < kKeys) {
+        if (tid < RT) {
             lt[tid] = ls;
             dt[tid] = dl;
         }
@@ -440,13 +443,17 @@ struct RowStage {
 // dk and dv.  A wave's 32 keys as columns, with K and V in registers; the
 // packed query rows of all heads that share them walk through LDS, read both
 // ways (S = Q K^T and dP = dO V^T by rows; dV^T += dO^T P, dK^T += Q^T dS).
-template <int D, int NW>
-__global__ __launch_bounds__(64 * NW, 1) void attn_dkv_kernel(const AttnArgs a) {
-    constexpr int NT = 64 * NW, BN = 32 * NW, KS = D / 16, DB = D / 32, TB = kKeys * D * 2;
+// At D = 128 the two accumulators take 128 registers; V then stays in LDS and
+// row tiles are half as long, so that two waves fit a SIMD.
+template <int D, int NW, int RT>
+__global__ __launch_bounds__(64 * NW, 2) void attn_dkv_kernel(const AttnArgs a) {
+    constexpr int NT = 64 * NW, BN = 32 * NW, KS = D / 16, DB = D / 32, TB = RT * D * 2;
     __shared__ __attribute__((aligned(16))) unsigned char qt[2][TB], gt[2][TB];
-    __shared__ __attribute__((aligned(16))) float lt[2][kKeys], dt[2][kKeys];
-    Place p = place(a);
-    p.tile = a.tiles - 1 - p.tile;                            // the first keys see the most rows
+    __shared__ __attribute__((aligned(16))) float lt[2][RT], dt[2][RT];
+    constexpr bool VL = D == 128;
+    __shared__ __attribute__((aligned(16))) unsigned char vl[VL ? BN * D * 2 : 16];
+    const Place p = find_place<true>(a, BN);
+    if (p.s < 0) return;
     const Seq z = sequence(a, p.s);
     const int k0 = p.tile * BN;
     if (k0 >= z.lk) return;
@@ -460,43 +467,56 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_dkv_kernel(const AttnArgs a) 
     const int w_all = w0 < z.lk ? first_query(a, z, min(w0 + 32, z.lk) - 1) * a.G : rows;
     const int from = first_query(a, z, min(key, z.lk - 1)) * a.G;
     const u32x4 none = {0u, 0u, 0u, 0u};
-    u32x4 kf[KS], vf[KS];
+    u32x4 kf[KS], vf[VL ? 1 : KS];
     f32x16 ak[DB], av[DB];
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
         const int64_t kr = z.k0 + (valid ? key : 0);
-        kf[s] = vf[s] = none;
+        u32x4 vv = none;
+        kf[s] = none;
         if (valid) {
             kf[s] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.k) + kr * a.ldk +
                                                     (int64_t)p.hk * D + 16 * s + 8 * h);
-            vf[s] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.v) + kr * a.ldv +
-                                                    (int64_t)p.hk * D + 16 * s + 8 * h);
+            vv = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.v) + kr * a.ldv +
+                                                 (int64_t)p.hk * D + 16 * s + 8 * h);
         }
+        if constexpr (VL)
+            *reinterpret_cast<u32x4*>(vl + chunk_at<D>(32 * wave + r, 2 * s + h)) = vv;   // read by this wave alone
+        else
+            vf[s] = vv;
     }
 #pragma unroll
     for (int e = 0; e < DB; ++e) ak[e] = av[e] = zero16();
     const float c2 = a.scale * kLog2e;
     const uint32_t inv = a.G == 1 ? 0u : (uint32_t)((0x100000000ull + a.G - 1) / a.G);
-    RowStage<D, NT> st;
-    const int start = min(first_query(a, z, k0) * a.G, rows) / kKeys * kKeys;
-    if (start < rows) {
+    Addr<D> ad;
+    ad.init(lane);
+    RowStage<D, NT, RT> st;
+    int start = min(first_query(a, z, k0) * a.G, rows) / RT * RT, end = rows;
+    if (a.k_splits > 1) {
+        int lo, hi;
+        split_range(rows - start, RT, a.k_splits, p.split, lo, hi);
+        end = start + hi;
+        start += lo;
+    }
+    if (start < end) {
         st.load(a, z, p.hk, start, rows, inv, tid);
         st.store(qt[0], gt[0], lt[0], dt[0], tid);
     }
     __syncthreads();
     int buf = 0;
-    for (int r0 = start; r0 < rows; r0 += kKeys, buf ^= 1) {
-        const bool more = r0 + kKeys < rows;
-        if (more) st.load(a, z, p.hk, r0 + kKeys, rows, inv, tid);
-        if (r0 + kKeys > w_first) {
+    for (int r0 = start; r0 < end; r0 += RT, buf ^= 1) {
+        const bool more = r0 + RT < end;
+        if (more) st.load(a, z, p.hk, r0 + RT, rows, inv, tid);
+        if (r0 + RT > w_first) {
             const bool mask = r0 < w_all;
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
+            for (int t = 0; t < RT / 32; ++t) {
                 f32x16 s = zero16(), dp = zero16();
 #pragma unroll
                 for (int e = 0; e < KS; ++e) {
-                    s = mma(read_row(qt[buf], chunk_at<D>(32 * t + r, 2 * e + h)), kf[e], s);
-                    dp = mma(read_row(gt[buf], chunk_at<D>(32 * t + r, 2 * e + h)), vf[e], dp);
+                    s = mma(ad.rows(qt[buf], t, e), kf[e], s);
+                    dp = mma(ad.rows(gt[buf], t, e), VL ? ad.rows(vl + wave * 64 * D, 0, e) : vf[VL ? 0 : e], dp);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -519,8 +539,8 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_dkv_kernel(const AttnArgs a) 
                     const u32x4 pp = pack8(s, 8 * u), ds = pack8(dp, 8 * u);
 #pragma unroll
                     for (int e = 0; e < DB; ++e) {
-                        av[e] = mma(read_col<D>(gt[buf], e, 2 * t + u, lane), pp, av[e]);
-                        ak[e] = mma(read_col<D>(qt[buf], e, 2 * t + u, lane), ds, ak[e]);
+                        av[e] = mma(ad.cols(gt[buf], e, 2 * t + u), pp, av[e]);
+                        ak[e] = mma(ad.cols(qt[buf], e, 2 * t + u), ds, ak[e]);
                     }
                 }
             }
@@ -529,6 +549,20 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_dkv_kernel(const AttnArgs a) 
         __syncthreads();
     }
     if (!valid) return;
+    if (a.k_splits > 1) {
+        const int64_t at = (((int64_t)p.split * a.total_k + z.ko + key) * a.Hk + p.hk) * D;
+#pragma unroll
+        for (int e = 0; e < DB; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int d = 32 * e + 8 * i + 4 * h;
+                *reinterpret_cast<f32x4*>(a.part_k + at + d) =
+                    f32x4{ak[e][4 * i], ak[e][4 * i + 1], ak[e][4 * i + 2], ak[e][4 * i + 3]};
+                *reinterpret_cast<f32x4*>(a.part_v + at + d) =
+                    f32x4{av[e][4 * i], av[e][4 * i + 1], av[e][4 * i + 2], av[e][4 * i + 3]};
+            }
+        return;
+    }
     const int64_t at = ((z.ko + key) * a.Hk + p.hk) * D;
 #pragma unroll
     for (int e = 0; e < DB; ++e)
@@ -552,25 +586,59 @@ bool grid_of(int64_t n, unsigned* g) {
 template <int D, int QB, int NW>
 gdn_status launch_fwd(AttnArgs a, hipStream_t s) {
     unsigned grid;
-    a.tiles = (int)(((int64_t)a.max_q * a.G + 32 * QB * NW - 1) / (32 * QB * NW));
-    if (!grid_of((int64_t)a.tiles * a.splits * a.Hk * a.n_seq, &grid)) return GDN_ERR_UNSUPPORTED;
+    const int64_t n = places(a.total_q * a.G, (int64_t)a.max_q * a.G, a.n_seq, 32 * QB * NW, a.cu_q, &a.tiles);
+    if (!grid_of(n * a.splits * a.Hk, &grid)) return GDN_ERR_UNSUPPORTED;
     hipLaunchKernelGGL((attn_fwd_kernel<D, QB, NW>), dim3(grid), dim3(64 * NW), 0, s, a);
     return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
+// dk and dv from the splits' sums, four features a thread.  The keys are the
+// sequences' own; what lies outside them is left alone.
+template <int D>
+__global__ __launch_bounds__(256) void attn_sum_kernel(const AttnArgs a) {
+    const unsigned per = 256 / (D / 4), groups = ((unsigned)a.max_k * a.Hk + per - 1) / per;
+    const Seq z = sequence(a, (int)(blockIdx.x / groups));
+    const int64_t r = (int64_t)(blockIdx.x % groups) * per + threadIdx.x / (D / 4);
+    if (r >= (int64_t)z.lk * a.Hk) return;
+    const int64_t at = (z.ko * a.Hk + r) * D + threadIdx.x % (D / 4) * 4, all = a.total_k * a.Hk * D;
+    f32x4 k = {0.f, 0.f, 0.f, 0.f}, v = k;
+    for (int i = 0; i < a.k_splits; ++i) {
+        k += *reinterpret_cast<const f32x4*>(a.part_k + i * all + at);
+        v += *reinterpret_cast<const f32x4*>(a.part_v + i * all + at);
+    }
+    k *= a.scale;
+    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.dk) + at) =
+        u32x2{pack_bf16x2(k[0], k[1]), pack_bf16x2(k[2], k[3])};
+    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.dv) + at) =
+        u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
 }
 
 template <int D>
 gdn_status launch_bwd(AttnArgs a, hipStream_t s) {
     unsigned grid;
-    a.tiles = (int)(((int64_t)a.max_q * a.G + 127) / 128);
-    if (!grid_of((int64_t)a.tiles * a.Hk * a.n_seq, &grid)) return GDN_ERR_UNSUPPORTED;
+    int64_t n = places(a.total_q * a.G, (int64_t)a.max_q * a.G, a.n_seq, 128, a.cu_q, &a.tiles);
+    if (!grid_of(n * a.Hk, &grid)) return GDN_ERR_UNSUPPORTED;
     if (grid) hipLaunchKernelGGL((attn_dq_kernel<D, 4>), dim3(grid), dim3(256), 0, s, a);
-    a.tiles = (a.max_k + 127) / 128;
-    if (!grid_of((int64_t)a.tiles * a.Hk * a.n_seq, &grid)) return GDN_ERR_UNSUPPORTED;
-    if (grid) hipLaunchKernelGGL((attn_dkv_kernel<D, 4>), dim3(grid), dim3(256), 0, s, a);
+    n = places(a.total_k, a.max_k, a.n_seq, 128, a.cu_k, &a.tiles);
+    if (!grid_of(n * a.Hk * a.k_splits, &grid)) return GDN_ERR_UNSUPPORTED;
+    if (grid) hipLaunchKernelGGL((attn_dkv_kernel<D, 4, (D == 128 ? 32 : 64)>), dim3(grid), dim3(256), 0, s, a);
+    if (grid && a.k_splits > 1) {
+        const int64_t per = 256 / (D / 4);
+        if (!grid_of(((int64_t)a.max_k * a.Hk + per - 1) / per * a.n_seq, &grid)) return GDN_ERR_UNSUPPORTED;
+        hipLaunchKernelGGL(attn_sum_kernel<D>, dim3(grid), dim3(256), 0, s, a);
+    }
     return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
 }  // namespace
+
+int attn_bwd_bf16_splits(int64_t total_k, int max_q, int max_k, int n_seq, int Hk, int G) {
+    int tiles;
+    const int64_t items = places(total_k, max_k, n_seq, 128, true, &tiles) * Hk;
+    const int64_t most = (int64_t)max_q * G / 1024;
+    if (items < 1 || items >= 512 || most < 2) return 1;
+    return (int)std::min<int64_t>(std::min<int64_t>((1024 + items - 1) / items, most), 64);
+}
 
 int attn_fwd_bf16_rows(int max_q, int G, int D) { return 128; }
 
