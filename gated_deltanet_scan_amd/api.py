@@ -6,6 +6,7 @@ raw device pointers plus torch's current HIP stream across the ABI.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Optional, Tuple
 
@@ -16,7 +17,7 @@ from ._lib import GdnDesc, GdnError
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _check(t: torch.Tensor, name: str, dtype, shape):
@@ -506,6 +507,22 @@ def _same_device(device, **tensors):
             raise ValueError("%s must be on %s (got %s)" % (name, device, t.device))
 
 
+_HERE = contextlib.nullcontext()
+# the current stream's handle without a Stream object around it, where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _launch(stream, device):
+    """(context, stream handle) of a launch: what is allocated within the context
+    belongs to the stream.  The current stream of the current device, the usual
+    case, needs no context (entering one costs as much as a small kernel)."""
+    if stream is not None:
+        return torch.cuda.stream(stream), stream.cuda_stream
+    index = device.index
+    return (_HERE if index == torch.cuda.current_device() else torch.cuda.device(device)), _raw_stream(index)
+
+
 def _workspace(workspace, n: int, device):
     """The caller's workspace, or one of n bytes from the current stream's allocator."""
     if workspace is not None or n == 0:
@@ -513,8 +530,8 @@ def _workspace(workspace, n: int, device):
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _ws_bytes(workspace) -> ctypes.c_size_t:
-    return ctypes.c_size_t(0 if workspace is None else workspace.numel())
+def _ws_bytes(workspace) -> int:
+    return 0 if workspace is None else workspace.numel()
 
 
 def _norm_desc(x, weight, bias, eps):
@@ -548,8 +565,8 @@ def layer_norm_fwd(x, weight=None, bias=None, *, eps: float = 1e-6, y=None, mean
     if rstd is not None:
         _check(rstd, "rstd", torch.float32, stats)
     _same_device(x.device, weight=weight, bias=bias, y=y, mean=mean, rstd=rstd)
-    stream = _launch_stream(stream, x.device)
-    with torch.cuda.stream(stream):   # allocations belong to the launch stream
+    where, handle = _launch(stream, x.device)
+    with where:   # allocations belong to the launch stream
         if y is None:
             y = torch.empty_like(x)
         if mean is None and return_stats:
@@ -557,7 +574,7 @@ def layer_norm_fwd(x, weight=None, bias=None, *, eps: float = 1e-6, y=None, mean
         if rstd is None and return_stats:
             rstd = torch.empty(stats, dtype=torch.float32, device=x.device)
         st = _lib.load().gdn_layer_norm_fwd(ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias), _ptr(y),
-                                            _ptr(mean), _ptr(rstd), ctypes.c_void_p(stream.cuda_stream))
+                                            _ptr(mean), _ptr(rstd), handle)
     if st != 0:
         raise GdnError(st, "gdn_layer_norm_fwd")
     return y, mean, rstd
@@ -590,8 +607,8 @@ def layer_norm_bwd(dy, x, mean, rstd, weight=None, bias=None, *, dx=None, dweigh
     _check_workspace(workspace, x.device)
     _same_device(x.device, dy=dy, mean=mean, rstd=rstd, weight=weight, bias=bias, dx=dx, dweight=dweight, dbias=dbias)
     lib = _lib.load()
-    stream = _launch_stream(stream, x.device)
-    with torch.cuda.stream(stream):   # allocations belong to the launch stream
+    where, handle = _launch(stream, x.device)
+    with where:   # allocations belong to the launch stream
         if dx is None:
             dx = torch.empty_like(x)
         if dweight is None and weight is not None:
@@ -602,7 +619,7 @@ def layer_norm_bwd(dy, x, mean, rstd, weight=None, bias=None, *, dx=None, dweigh
             workspace = _workspace(workspace, int(lib.gdn_layer_norm_workspace_size(ctypes.byref(desc))), x.device)
         st = lib.gdn_layer_norm_bwd(ctypes.byref(desc), _ptr(dy), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd),
                                     _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(workspace), _ws_bytes(workspace),
-                                    ctypes.c_void_p(stream.cuda_stream))
+                                    handle)
     if st != 0:
         raise GdnError(st, "gdn_layer_norm_bwd")
     return dx, dweight, dbias
@@ -664,14 +681,14 @@ def rotary(q, k, pos, *, axes, theta: float = 10000.0, halves: bool = False, inv
     dims = (ctypes.c_int32 * _lib.GDN_ROTARY_MAX_AXES)(*axes)
     desc = _lib.GdnRotaryDesc(tokens, pos.numel() // len(axes), heads["q"], heads["k"], D, len(axes), dims,
                               _io(x.dtype, "q and k"), flags, float(theta))
-    stream = _launch_stream(stream, x.device)
-    with torch.cuda.stream(stream):   # allocations belong to the launch stream
+    where, handle = _launch(stream, x.device)
+    with where:   # allocations belong to the launch stream
         if q is not None and q_out is None:
             q_out = torch.empty_like(q)
         if k is not None and k_out is None:
             k_out = torch.empty_like(k)
         st = _lib.load().gdn_rotary(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(pos), _ptr(q_out), _ptr(k_out),
-                                    ctypes.c_void_p(stream.cuda_stream))
+                                    handle)
     if st != 0:
         raise GdnError(st, "gdn_rotary")
     return q_out, k_out
@@ -783,8 +800,8 @@ def attention_fwd(q, k, v, *, causal: bool = False, causal_block: Optional[int] 
     _check_workspace(workspace, q.device)
     _same_device(q.device, k_len=k_len, o=o, lse=lse)
     lib = _lib.load()
-    stream = _launch_stream(stream, q.device)
-    with torch.cuda.stream(stream):   # allocations belong to the launch stream
+    where, handle = _launch(stream, q.device)
+    with where:   # allocations belong to the launch stream
         if o is None:
             o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         if lse is None and return_lse:
@@ -792,7 +809,7 @@ def attention_fwd(q, k, v, *, causal: bool = False, causal_block: Optional[int] 
         workspace = _workspace(workspace, int(lib.gdn_attn_workspace_size(ctypes.byref(desc))), q.device)
         st = lib.gdn_attn_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k), _ptr(k_len),
                               _ptr(o), _ptr(lse), _ptr(workspace), _ws_bytes(workspace),
-                              ctypes.c_void_p(stream.cuda_stream))
+                              handle)
     if st != 0:
         raise GdnError(st, "gdn_attn_fwd")
     return o, lse
@@ -814,14 +831,14 @@ def attention_bwd(q, k, v, o, lse, dO, *, causal: bool = False, causal_block: Op
     _check_workspace(workspace, q.device)
     _same_device(q.device, o=o, lse=lse, dO=dO, dq=dq, dk=dk, dv=dv)
     lib = _lib.load()
-    stream = _launch_stream(stream, q.device)
-    with torch.cuda.stream(stream):   # allocations belong to the launch stream
+    where, handle = _launch(stream, q.device)
+    with where:   # allocations belong to the launch stream
         dq, dk, dv = [t if t is not None else torch.empty(like.shape, dtype=like.dtype, device=like.device)
                       for t, like in ((dq, q), (dk, k), (dv, v))]
         workspace = _workspace(workspace, int(lib.gdn_attn_workspace_size_bwd(ctypes.byref(desc))), q.device)
         st = lib.gdn_attn_bwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dO), _ptr(cu_q),
                               _ptr(cu_k), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), _ws_bytes(workspace),
-                              ctypes.c_void_p(stream.cuda_stream))
+                              handle)
     if st != 0:
         raise GdnError(st, "gdn_attn_bwd")
     return dq, dk, dv

@@ -91,8 +91,8 @@ __global__ __launch_bounds__(kThreads) void attn_fwd_f32_kernel(const AttnArgs a
     const bool valid = row < rows;
     const int n = valid ? visible(a, z, row / a.G) : 0;
     const int upto = visible(a, z, (min(r0 + kRows, rows) - 1) / a.G);
-    int lo, hi;
-    split_range(upto, kTile, a.splits, p.split, lo, hi);
+    const int lo = min(p.split * a.chunk, upto), hi = min(lo + a.chunk, upto);
+    if (p.split > 0 && p.split * a.chunk >= z.lk) return;     // a shorter sequence has fewer splits
     f32x4 q[D / 16], acc[D / 16];
     row_frag<T, D>(q, valid ? q_row<T>(a, z, p.hk, row) : nullptr, valid, g);
 #pragma unroll
@@ -168,22 +168,20 @@ template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void attn_join_kernel(const AttnArgs a) {
     const int per = kThreads / 16;
     const int tiles = (a.max_q * a.Hq + per - 1) / per;
-    const int s = (int)(blockIdx.x / (unsigned)tiles);
-    int64_t q0;
-    int lq;
-    seq_range(a.cu_q, s, a.total_q, a.max_q, q0, lq);
+    const Seq z = sequence(a, (int)(blockIdx.x / (unsigned)tiles));
     const int64_t r = (int64_t)(blockIdx.x % (unsigned)tiles) * per + (threadIdx.x >> 4);
-    if (r >= (int64_t)lq * a.Hq) return;
-    const int64_t gr = q0 * a.Hq + r, all = a.total_q * a.Hq;
+    if (r >= (int64_t)z.lq * a.Hq) return;
+    const int64_t gr = z.q0 * a.Hq + r, all = a.total_q * a.Hq;
+    const int splits = max(1, (z.lk + a.chunk - 1) / a.chunk);
     float m = -INFINITY;
-    for (int i = 0; i < a.splits; ++i) m = fmaxf(m, a.part_lse[i * all + gr]);
+    for (int i = 0; i < splits; ++i) m = fmaxf(m, a.part_lse[i * all + gr]);
     const float ms = m == -INFINITY ? 0.f : m;
     float l = 0.f;
     f32x4 acc[(D + 63) / 64];
     const int c = 4 * (threadIdx.x & 15);
 #pragma unroll
     for (int e = 0; e < (D + 63) / 64; ++e) acc[e] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int i = 0; i < a.splits; ++i) {
+    for (int i = 0; i < splits; ++i) {
         const float pl = a.part_lse[i * all + gr];
         if (pl == -INFINITY) continue;                    // a split that saw nothing wrote zeros
         const float w = exp2_f((pl - ms) * kLog2e);
@@ -381,15 +379,24 @@ int fwd_rows(const gdn_attn_desc* d) {
     return fast(d) ? attn_fwd_bf16_rows(d->max_q, d->Hq / d->Hk, d->D) : kRows;
 }
 
-// Splits of the key axis: where the row tiles alone would leave compute units
-// idle, enough for about two workgroups on each of the 256, but no less than
-// 256 keys a split (a split's partial result is written and read in fp32).
-int fwd_splits(const gdn_attn_desc* d) {
+// Keys of a split of the key axis; max_k or more: not split.  Split where the
+// row tiles alone would leave compute units idle: as many splits as fill two
+// workgroups on each of the 256 in one round.  A decode step (a few rows a key
+// head) is cut four times finer, because the lengths of its caches differ and
+// short work spreads evenly; a split's fp32 partial result is then small
+// against its keys, of which it takes 512 at least.
+int fwd_chunk(const gdn_attn_desc* d) {
     const int64_t rows = (int64_t)d->max_q * (d->Hq / d->Hk);
     const int64_t units = (int64_t)d->n_seq * d->Hk * std::max<int64_t>(1, (rows + fwd_rows(d) - 1) / fwd_rows(d));
-    if (units >= 256) return 1;
-    const int64_t most = std::max<int64_t>(1, d->max_k / 256);
-    return (int)std::min<int64_t>(std::min<int64_t>(most, (512 + units - 1) / std::max<int64_t>(units, 1)), 128);
+    int64_t n = 512 / std::max<int64_t>(units, 1);
+    if (rows <= 32) n *= 4;
+    if (n < 2) return std::max(d->max_k, 1);
+    const int64_t chunk = std::max<int64_t>(((d->max_k + n - 1) / n + 63) / 64 * 64, 512);
+    return (int)std::min<int64_t>(chunk, std::max(d->max_k, 1));
+}
+int fwd_splits(const gdn_attn_desc* d) {
+    const int chunk = fwd_chunk(d);
+    return std::max(1, (d->max_k + chunk - 1) / chunk);
 }
 
 // Splits of the query rows in the bf16 dk/dv kernel.  Its workgroups each walk
@@ -512,6 +519,7 @@ gdn_status gdn_attn_fwd(const gdn_attn_desc* d, const void* q, const void* k, co
     if ((st = check_device(&cus)) != GDN_OK) return st;
     a.q = q, a.k = k, a.v = v, a.out = o, a.lse = lse, a.cu_q = cu_q, a.cu_k = cu_k, a.k_len = k_len;
     a.splits = fwd_splits(d);
+    a.chunk = fwd_chunk(d);
     if (a.splits > 1) {
         a.part_o = static_cast<float*>(workspace);
         a.part_lse = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +

@@ -31,6 +31,7 @@ struct AttnArgs {
     int max_q, max_k;
     int tiles;                           // row (or key) tiles of the longest sequence
     int splits, k_splits;                // of the key axis (forward), of the row axis (dk, dv)
+    int chunk;                           // keys of a split (the longest sequence's fill them all)
     int causal, block;
     float scale;
 };
@@ -80,7 +81,7 @@ __device__ __forceinline__ int first_query(const AttnArgs& a, const Seq& z, int 
     if (!a.causal) return 0;
     return max(0, j / a.block * a.block - (z.lk - z.lq));
 }
-// Keys [lo, hi) of split sp of n, of the first `upto` keys, in whole tiles.
+// Part sp of n of [0, upto), in whole tiles.
 __device__ __forceinline__ void split_range(int upto, int tile, int n, int sp, int& lo, int& hi) {
     const int t = (upto + tile - 1) / tile, per = (t + n - 1) / n;
     lo = min(sp * per * tile, upto);

@@ -148,8 +148,8 @@ __global__ __launch_bounds__(64 * NW, NW * QB <= 8 && QB == 1 ? 2 : 1) void attn
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int w0 = r0 + 32 * QB * wave;                       // the wave's first row
     const int upto = visible(a, z, (min(r0 + BM, rows) - 1) / a.G);
-    int lo, hi;
-    split_range(upto, kKeys, a.splits, p.split, lo, hi);
+    const int lo = min(p.split * a.chunk, upto), hi = min(lo + a.chunk, upto);
+    if (p.split > 0 && p.split * a.chunk >= z.lk) return;     // a shorter sequence has fewer splits
     // the wave's rows see the keys below n_first all, and none from n_last on
     const int n_first = w0 < rows ? visible(a, z, w0 / a.G) : 0;
     const int n_last = w0 < rows ? visible(a, z, (min(w0 + 32 * QB, rows) - 1) / a.G) : 0;

@@ -33,9 +33,30 @@ struct RotArgs {
     int heads[2];
     int D, pairs, axes, tb;          // tb: tokens per workgroup
     int pos_f32, inverse;
-    uint8_t axis_of[kMaxPairs];
-    double turns[kMaxPairs];         // theta^(-2i/d) / (2 pi)
+    int axis_pairs[GDN_ROTARY_MAX_AXES];
+    double step[GDN_ROTARY_MAX_AXES];   // theta^(-2/d)
 };
+
+// Turns per position of pair j, theta^(-2i/d) / (2 pi), and its axis: a power
+// by squaring, off by at most 14 half steps of 2^-53 (a table in the kernel's
+// arguments made them 1.3 KB and the launch 3 us longer).
+__device__ __forceinline__ double turns_of(const RotArgs& a, int j, int& axis) {
+    axis = 0;
+#pragma unroll
+    for (int x = 0; x < GDN_ROTARY_MAX_AXES - 1; ++x)
+        if (axis == x && j >= a.axis_pairs[x]) {
+            j -= a.axis_pairs[x];
+            axis = x + 1;
+        }
+    double b = axis == 0 ? a.step[0] : axis == 1 ? a.step[1] : axis == 2 ? a.step[2] : a.step[3];
+    double r = 0.15915494309189535;     // 1 / (2 pi)
+#pragma unroll
+    for (int bit = 0; bit < 7; ++bit) {
+        if (j >> bit & 1) r *= b;
+        b *= b;
+    }
+    return r;
+}
 
 template <typename T, int VW> struct VecN;     // VW consecutive elements, aligned
 template <> struct VecN<uint16_t, 8> { using R = u32x4; };
@@ -100,10 +121,12 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(const RotArgs a) {
     const int nt = (int)min((int64_t)a.tb, a.tokens - t0);
     for (int i = tid; i < nt * P; i += kThreads) {
         const int tk = i / P, j = i - tk * P;
-        const int64_t at = ((t0 + tk) % a.pos_rows) * a.axes + a.axis_of[j];
+        int axis;
+        const double turns = turns_of(a, j, axis);
+        const int64_t at = ((t0 + tk) % a.pos_rows) * a.axes + axis;
         const double p = a.pos_f32 ? (double)static_cast<const float*>(a.pos)[at]
                                    : (double)static_cast<const int32_t*>(a.pos)[at];
-        double u = p * a.turns[j];
+        double u = p * turns;
         u -= rint(u);
         float sn, cs;
         sincospif(2.0f * (float)u, &sn, &cs);
@@ -229,12 +252,10 @@ extern "C" gdn_status gdn_rotary(const gdn_rotary_desc* d, const void* q, const 
     a.D = d->D, a.pairs = pairs, a.axes = d->n_axes;
     a.pos_f32 = (d->flags & GDN_FLAG_ROTARY_POS_F32) != 0;
     a.inverse = (d->flags & GDN_FLAG_ROTARY_INVERSE) != 0;
-    int j = 0;
-    for (int x = 0; x < d->n_axes; ++x)
-        for (int i = 0; i < d->axis_dim[x] / 2; ++i, ++j) {
-            a.axis_of[j] = (uint8_t)x;
-            a.turns[j] = pow(d->theta, -2.0 * i / d->axis_dim[x]) / (2.0 * M_PI);
-        }
+    for (int x = 0; x < d->n_axes; ++x) {
+        a.axis_pairs[x] = d->axis_dim[x] / 2;
+        a.step[x] = d->axis_dim[x] ? pow(d->theta, -2.0 / d->axis_dim[x]) : 1.0;
+    }
     int cus;
     if ((st = check_device(&cus)) != GDN_OK) return st;
     // Tokens a workgroup: about 16 16-byte vectors a thread, so that the angles
