@@ -162,39 +162,56 @@ __global__ __launch_bounds__(kThreads) void attn_fwd_f32_kernel(const AttnArgs a
     if (g == 0 && a.lse) a.lse[gr] = ls;
 }
 
-// o = sum over the splits of exp(lse_s - lse) o_s.  A quarter-wave a row; the
-// rows are the sequences' own, so what lies behind the last one is left alone.
+// o = sum over the splits of exp(lse_s - lse) o_s, a wave a row.  Every lane
+// weighs one split (64 at a time), then each quarter of the wave adds every
+// fourth split's row, several loads in flight; the quarters add up in order.
+// The rows are the sequences' own, so what lies behind the last is left alone.
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void attn_join_kernel(const AttnArgs a) {
-    const int per = kThreads / 16;
-    const int tiles = (a.max_q * a.Hq + per - 1) / per;
+    constexpr int E = (D + 63) / 64, per = kThreads / 64;
+    const int tiles = (int)(((int64_t)a.max_q * a.Hq + per - 1) / per);
     const Seq z = sequence(a, (int)(blockIdx.x / (unsigned)tiles));
-    const int64_t r = (int64_t)(blockIdx.x % (unsigned)tiles) * per + (threadIdx.x >> 4);
+    const int lane = threadIdx.x & 63, g = lane >> 4, c = 4 * (lane & 15);
+    const int64_t r = (int64_t)(blockIdx.x % (unsigned)tiles) * per + (threadIdx.x >> 6);
     if (r >= (int64_t)z.lq * a.Hq) return;
     const int64_t gr = z.q0 * a.Hq + r, all = a.total_q * a.Hq;
     const int splits = max(1, (z.lk + a.chunk - 1) / a.chunk);
-    float m = -INFINITY;
-    for (int i = 0; i < splits; ++i) m = fmaxf(m, a.part_lse[i * all + gr]);
-    const float ms = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    f32x4 acc[(D + 63) / 64];
-    const int c = 4 * (threadIdx.x & 15);
+    float m = -INFINITY, l = 0.f;
+    f32x4 acc[E];
 #pragma unroll
-    for (int e = 0; e < (D + 63) / 64; ++e) acc[e] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int i = 0; i < splits; ++i) {
-        const float pl = a.part_lse[i * all + gr];
-        if (pl == -INFINITY) continue;                    // a split that saw nothing wrote zeros
-        const float w = exp2_f((pl - ms) * kLog2e);
-        l += w;
+    for (int e = 0; e < E; ++e) acc[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int s0 = 0; s0 < splits; s0 += 64) {
+        const float pl = s0 + lane < splits ? a.part_lse[(s0 + lane) * all + gr] : -INFINITY;
+        float top = pl;
 #pragma unroll
-        for (int e = 0; e < (D + 63) / 64; ++e)
-            if (64 * e + c < D) acc[e] += w * load4(a.part_o + (i * all + gr) * D + 64 * e + c);
+        for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+        top = fmaxf(top, m);
+        const float ms = top == -INFINITY ? 0.f : top;
+        const float w = exp2_f((pl - ms) * kLog2e), al = exp2_f((m - ms) * kLog2e);   // 0 for a split that saw nothing
+        m = top;
+        l = l * al + wave_sum(w);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] *= al;
+        const int n = min(64, splits - s0);
+#pragma unroll 4
+        for (int i = g; i < n; i += 4) {
+            const float wi = __shfl(w, i);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (64 * e + c < D) acc[e] += wi * load4(a.part_o + ((s0 + i) * all + gr) * D + 64 * e + c);
+        }
     }
     const float inv = l > 0.f ? 1.0f / l : l;
 #pragma unroll
-    for (int e = 0; e < (D + 63) / 64; ++e)
-        if (64 * e + c < D) store4(static_cast<T*>(a.out) + gr * D + 64 * e + c, acc[e] * inv);
-    if (c == 0 && a.lse) a.lse[gr] = l == 0.f ? -INFINITY : ms + log2_f(l) * kLn2;
+    for (int e = 0; e < E; ++e) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            acc[e][j] += __shfl_xor(acc[e][j], 16);
+            acc[e][j] += __shfl_xor(acc[e][j], 32);
+        }
+        if (g == 0 && 64 * e + c < D) store4(static_cast<T*>(a.out) + gr * D + 64 * e + c, acc[e] * inv);
+    }
+    if (lane == 0 && a.lse) a.lse[gr] = l == 0.f ? -INFINITY : m + log2_f(l) * kLn2;
 }
 
 // dq, and <d_o, o> for the dk/dv kernel: query rows as columns, as in the
@@ -382,14 +399,14 @@ int fwd_rows(const gdn_attn_desc* d) {
 // Keys of a split of the key axis; max_k or more: not split.  Split where the
 // row tiles alone would leave compute units idle: as many splits as fill two
 // workgroups on each of the 256 in one round.  A decode step (a few rows a key
-// head) is cut four times finer, because the lengths of its caches differ and
+// head) is cut eight times finer, because the lengths of its caches differ and
 // short work spreads evenly; a split's fp32 partial result is then small
 // against its keys, of which it takes 512 at least.
 int fwd_chunk(const gdn_attn_desc* d) {
     const int64_t rows = (int64_t)d->max_q * (d->Hq / d->Hk);
     const int64_t units = (int64_t)d->n_seq * d->Hk * std::max<int64_t>(1, (rows + fwd_rows(d) - 1) / fwd_rows(d));
     int64_t n = 512 / std::max<int64_t>(units, 1);
-    if (rows <= 32) n *= 4;
+    if (rows <= 32) n *= 8;
     if (n < 2) return std::max(d->max_k, 1);
     const int64_t chunk = std::max<int64_t>(((d->max_k + n - 1) / n + 63) / 64 * 64, 512);
     return (int)std::min<int64_t>(chunk, std::max(d->max_k, 1));
@@ -454,7 +471,7 @@ gdn_status run_fwd(AttnArgs a, hipStream_t s) {
 template <typename T, int D>
 gdn_status run_join(const AttnArgs& a, hipStream_t s) {
     unsigned grid;
-    if (!grid_of(((int64_t)a.max_q * a.Hq + 15) / 16 * a.n_seq, &grid)) return GDN_ERR_UNSUPPORTED;
+    if (!grid_of(((int64_t)a.max_q * a.Hq + 3) / 4 * a.n_seq, &grid)) return GDN_ERR_UNSUPPORTED;
     hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3(grid), dim3(kThreads), 0, s, a);
     return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
