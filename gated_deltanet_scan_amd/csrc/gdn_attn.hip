@@ -397,15 +397,15 @@ int fwd_rows(const gdn_attn_desc* d) {
 }
 
 // Keys of a split of the key axis; max_k or more: not split.  Split where the
-// row tiles alone would leave compute units idle: as many splits as fill two
-// workgroups on each of the 256 in one round.  A decode step (a few rows a key
+// row tiles alone would leave compute units idle: as many splits as fill the
+// 256 in one round (with two waves a SIMD).  A decode step (a few rows a key
 // head) is cut eight times finer, because the lengths of its caches differ and
 // short work spreads evenly; a split's fp32 partial result is then small
 // against its keys, of which it takes 512 at least.
 int fwd_chunk(const gdn_attn_desc* d) {
     const int64_t rows = (int64_t)d->max_q * (d->Hq / d->Hk);
     const int64_t units = (int64_t)d->n_seq * d->Hk * std::max<int64_t>(1, (rows + fwd_rows(d) - 1) / fwd_rows(d));
-    int64_t n = 512 / std::max<int64_t>(units, 1);
+    int64_t n = (fwd_rows(d) == 256 ? 256 : 512) / std::max<int64_t>(units, 1);
     if (rows <= 32) n *= 8;
     if (n < 2) return std::max(d->max_k, 1);
     const int64_t chunk = std::max<int64_t>(((d->max_k + n - 1) / n + 63) / 64 * 64, 512);

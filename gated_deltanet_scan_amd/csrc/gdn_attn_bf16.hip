@@ -44,43 +44,45 @@ __device__ __forceinline__ float half_sum(float x) {
 }
 
 // LDS tiles hold rows of D features in 16-byte chunks whose place within the
-// row is permuted by the row.  Row-wise fragments read one chunk column of
-// eight consecutive rows at a time, transposed ones 32 bytes of four; the
-// permutation sends both to different banks: the row's lowest two bits move
-// pairs of chunks, the third exchanges the two of a pair (at D = 32 two rows
-// share the 128 bytes of one bank cycle, so one bit less of each).
+// row is permuted by the row.  LDS serves 256 bytes a cycle: sixteen lanes of a
+// row-wise fragment (one chunk column of sixteen rows) and 32 lanes of a
+// transposed one (64 bytes of four rows).  The permutation sends each of these
+// to different banks: the row's lowest two bits move groups of four chunks, the
+// next two permute within a group (a row of D = 64 is half of the 256 bytes and
+// one of D = 32 a quarter, so they need one bit and two bits less).  With a
+// permutation made for 128 bytes a cycle both reads took twice the cycles.
 template <int D>
 __device__ __forceinline__ uint32_t chunk_at(int row, int c) {
-    const int f = D >= 64 ? 2 * (row & 3) + ((row >> 2) & 1) : (row & 2) + ((row >> 2) & 1);
+    const int f = (D == 128 ? (row & 3) << 2 : D == 64 ? (row & 2) << 1 : 0) + ((row >> 2) & 3);
     return (uint32_t)(row * 2 * D) + (uint32_t)((c ^ f) << 4);
 }
 __device__ __forceinline__ u32x2 read_tr(const unsigned char* p) {
     typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
     return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p));
 }
-// A lane's addresses in a tile.  The permutation acts on the low bits of the
-// chunk alone, so a few registers hold all of them and the rest is constant.
+// A lane's addresses in a tile.
 template <int D>
 struct Addr {
-    static constexpr int NR = D >= 64 ? 4 : 2, NC = D >= 64 ? 2 : 1;
-    uint32_t row[NR], col[NC];
+    uint32_t row[D / 16], lo[D / 32], hi[D / 32];
     __device__ __forceinline__ void init(int lane) {
         const int h = lane >> 5, r = lane & 31, j = lane >> 4, q = lane & 15;
 #pragma unroll
-        for (int x = 0; x < NR; ++x) row[x] = chunk_at<D>(r, 2 * x + h);
+        for (int e = 0; e < D / 16; ++e) row[e] = chunk_at<D>(r, 2 * e + h);
 #pragma unroll
-        for (int x = 0; x < NC; ++x)
-            col[x] = chunk_at<D>(4 * (j >> 1) + (q >> 2), 4 * x + 2 * (j & 1) + ((q >> 1) & 1)) + (q & 1) * 8;
+        for (int e = 0; e < D / 32; ++e) {
+            const int k = 4 * (j >> 1) + (q >> 2), c = 4 * e + 2 * (j & 1) + ((q >> 1) & 1);
+            lo[e] = chunk_at<D>(k, c) + (q & 1) * 8;
+            hi[e] = chunk_at<D>(k + 8, c) + (q & 1) * 8;
+        }
     }
     // rows 32 t + r, features 16 e + 8 h .. + 7
     __device__ __forceinline__ u32x4 rows(const unsigned char* tile, int t, int e) const {
-        return *reinterpret_cast<const u32x4*>(tile + row[e % NR] + (e / NR) * 128 + t * 64 * D);
+        return *reinterpret_cast<const u32x4*>(tile + row[e] + t * 64 * D);
     }
     // features 32 e + r, rows 16 s + 4 h + 0..3 and 16 s + 8 + 4 h + 0..3
     __device__ __forceinline__ u32x4 cols(const unsigned char* tile, int e, int s) const {
-        const unsigned char* p = tile + col[e % NC] + (e / NC) * 128 + s * 32 * D;
-        const u32x2 lo = read_tr(p), hi = read_tr(p + 16 * D);
-        return u32x4{lo[0], lo[1], hi[0], hi[1]};
+        const u32x2 a = read_tr(tile + lo[e] + s * 32 * D), b = read_tr(tile + hi[e] + s * 32 * D);
+        return u32x4{a[0], a[1], b[0], b[1]};
     }
 };
 
@@ -104,40 +106,43 @@ constexpr int kKeys = 64;       // keys per tile
 // bf16 or fp32), so most tiles skip the rescaling of the outputs.
 constexpr float kSlack = 8.0f;
 
-// Staging of one tile of K and V: global memory to registers to LDS.
+// Staging of one tile of keys: global memory to registers to LDS.  Rows past the
+// range read as zeros.
 template <int D, int NT>
-struct Stage {
-    static constexpr int N = kKeys * D / 8 / NT;         // 16-byte chunks a thread and tensor
+struct Tile {
+    static constexpr int N = kKeys * D / 8 / NT;         // 16-byte chunks a thread
     static_assert(N >= 1, "every thread stages something");
-    u32x4 k[N], v[N];
-    __device__ __forceinline__ void load(const uint16_t* kb, const uint16_t* vb, int64_t ldk, int64_t ldv, int n0,
-                                         int hi, int tid) {
+    u32x4 x[N];
+    __device__ __forceinline__ void load(const uint16_t* base, int64_t ld, int n0, int hi, int tid) {
         const int rows = min(kKeys, hi - n0);
-        // rows past the range read as zeros
-        const rsrc_t rk = make_rsrc(kb + (int64_t)n0 * ldk, (uint32_t)(((rows - 1) * ldk + D) * 2));
-        const rsrc_t rv = make_rsrc(vb + (int64_t)n0 * ldv, (uint32_t)(((rows - 1) * ldv + D) * 2));
+        const rsrc_t rs = make_rsrc(base + (int64_t)n0 * ld, (uint32_t)(((rows - 1) * ld + D) * 2));
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const int i = tid + j * NT, row = i / (D / 8), c = i % (D / 8);
-            k[j] = __builtin_amdgcn_raw_buffer_load_b128(rk, (uint32_t)(row * (int)ldk * 2 + c * 16), 0, 0);
-            v[j] = __builtin_amdgcn_raw_buffer_load_b128(rv, (uint32_t)(row * (int)ldv * 2 + c * 16), 0, 0);
+            x[j] = __builtin_amdgcn_raw_buffer_load_b128(rs, (uint32_t)(row * (int)ld * 2 + c * 16), 0, 0);
         }
     }
-    __device__ __forceinline__ void store(unsigned char* kt, unsigned char* vt, int tid) const {
+    __device__ __forceinline__ void store(unsigned char* t, int tid) const {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const int i = tid + j * NT, row = i / (D / 8), c = i % (D / 8);
-            *reinterpret_cast<u32x4*>(kt + chunk_at<D>(row, c)) = k[j];
-            *reinterpret_cast<u32x4*>(vt + chunk_at<D>(row, c)) = v[j];
+            *reinterpret_cast<u32x4*>(t + chunk_at<D>(row, c)) = x[j];
         }
     }
 };
 
-// One workgroup: NW waves of 32 QB packed query rows each, all walking the same
+// One workgroup: NW waves of 32 packed query rows each, all walking the same
 // key tiles, double-buffered in LDS.
-template <int D, int QB, int NW>
-__global__ __launch_bounds__(64 * NW, NW * QB <= 8 && QB == 1 ? 2 : 1) void attn_fwd_kernel(const AttnArgs a) {
-    constexpr int NT = 64 * NW, BM = 32 * QB * NW, KS = D / 16, DB = D / 32, TB = kKeys * D * 2;
+//
+// A wave walks the keys in steps of 32 and keeps three of them in flight: the
+// scores of the next step and the output products of the last one (16 matrix
+// instructions, 512 cycles) stand beside the exponentials of this one (about
+// 450 cycles of vector instructions), with no dependence between them, so both
+// pipes of a SIMD work at once.  K of a tile is therefore in LDS half a tile
+// before V of it.
+template <int D, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void attn_fwd_kernel(const AttnArgs a) {
+    constexpr int NT = 64 * NW, BM = 32 * NW, KS = D / 16, DB = D / 32, TB = kKeys * D * 2, HB = TB / 2;
     __shared__ __attribute__((aligned(16))) unsigned char kt[2][TB], vt[2][TB];
     const Place p = find_place<false>(a, BM);
     if (p.s < 0) return;
@@ -146,152 +151,142 @@ __global__ __launch_bounds__(64 * NW, NW * QB <= 8 && QB == 1 ? 2 : 1) void attn
     if (r0 >= rows) return;
     const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, r = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int w0 = r0 + 32 * QB * wave;                       // the wave's first row
+    const int w0 = r0 + 32 * wave, row = w0 + r;              // the wave's first row, the lane's
+    const bool valid = row < rows;
     const int upto = visible(a, z, (min(r0 + BM, rows) - 1) / a.G);
     const int lo = min(p.split * a.chunk, upto), hi = min(lo + a.chunk, upto);
     if (p.split > 0 && p.split * a.chunk >= z.lk) return;     // a shorter sequence has fewer splits
     // the wave's rows see the keys below n_first all, and none from n_last on
     const int n_first = w0 < rows ? visible(a, z, w0 / a.G) : 0;
-    const int n_last = w0 < rows ? visible(a, z, (min(w0 + 32 * QB, rows) - 1) / a.G) : 0;
+    const int n_last = w0 < rows ? visible(a, z, (min(w0 + 32, rows) - 1) / a.G) : 0;
+    const int n = valid ? visible(a, z, row / a.G) : 0;
 
-    u32x4 q[QB][KS];
-    f32x16 acc[QB][DB];
-    float m[QB], l[QB];
-    int n[QB];
-#pragma unroll
-    for (int b = 0; b < QB; ++b) {
-        const int row = w0 + 32 * b + r;
-        const bool valid = row < rows;
-        n[b] = valid ? visible(a, z, row / a.G) : 0;
+    u32x4 q[KS];
+    f32x16 acc[DB];
+    const u32x4 none = {0u, 0u, 0u, 0u};
+    {
         const uint16_t* src = valid ? q_row(a, z, p.hk, row) : nullptr;
 #pragma unroll
         for (int s = 0; s < KS; ++s)
-            q[b][s] = valid ? *reinterpret_cast<const u32x4*>(src + 16 * s + 8 * h) : u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-        for (int e = 0; e < DB; ++e) acc[b][e] = zero16();
-        m[b] = -INFINITY;
-        l[b] = 0.f;
+            q[s] = valid ? *reinterpret_cast<const u32x4*>(src + 16 * s + 8 * h) : none;
     }
+#pragma unroll
+    for (int e = 0; e < DB; ++e) acc[e] = zero16();
+    const float c2 = a.scale * kLog2e, slack = kSlack / c2;
+    // running maximum (powers of two), the same with 0 before any key, the raw
+    // score from which it has to be raised, and the lane's part of the sum
+    float m = -INFINITY, ms = 0.f, limit = -INFINITY, l = 0.f;
+
     const uint16_t* kb = static_cast<const uint16_t*>(a.k) + z.k0 * a.ldk + (int64_t)p.hk * D;
     const uint16_t* vb = static_cast<const uint16_t*>(a.v) + z.k0 * a.ldv + (int64_t)p.hk * D;
-    const float c2 = a.scale * kLog2e;
     Addr<D> ad;
     ad.init(lane);
-    Stage<D, NT> st;
+    Tile<D, NT> sk, sv;                                       // on their way: K of the next tile, V of this one
+
+    // keys [base, base + 32): scores in `cur`; `nxt` takes the next scores, `last`
+    // holds the step before, `now` takes this one's exponentials
+    auto step = [&](f32x16& cur, f32x16& nxt, u32x4(&last)[2], u32x4(&now)[2], const unsigned char* k_next,
+                    const unsigned char* v_last, int base) {
+        if (base + 32 > n_first) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (base + 8 * (i >> 2) + 4 * h + (i & 3) >= n) cur[i] = -INFINITY;
+        }
+        float top = cur[0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) top = fmaxf(top, cur[i]);
+        if (__any(top > limit)) {
+            // a row's two lanes share one maximum; what they hold is scaled to it
+            const float mn = fmaxf(m, half_max(top) * c2);
+            const float al = mn == -INFINITY ? 1.f : exp2_f(m - mn);
+            m = mn;
+            ms = mn == -INFINITY ? 0.f : mn;
+            limit = mn / c2 + slack;
+            l *= al;
+#pragma unroll
+            for (int e = 0; e < DB; ++e) acc[e] *= al;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    last[u][i] = pack_bf16x2(__uint_as_float(last[u][i] << 16) * al,
+                                             __uint_as_float(last[u][i] & 0xffff0000u) * al);
+        }
+        __builtin_amdgcn_s_setprio(1);                        // over a wave that stages or masks: 1.3% faster
+        nxt = zero16();
+#pragma unroll
+        for (int e = 0; e < KS; ++e) nxt = mma(ad.rows(k_next, 0, e), q[e], nxt);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < DB; ++e) acc[e] = mma(ad.cols(v_last, e, u), last[u], acc[e]);
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            cur[i] = exp2_f(__builtin_fmaf(cur[i], c2, -ms));
+            sum += cur[i];
+        }
+        l += sum;                                             // this lane's keys; joined at the end
+        now[0] = pack8(cur, 0);
+        now[1] = pack8(cur, 8);
+        __builtin_amdgcn_s_setprio(0);
+    };
+
     if (lo < hi) {
-        st.load(kb, vb, a.ldk, a.ldv, lo, hi, tid);
-        st.store(kt[0], vt[0], tid);
-    }
-    __syncthreads();
-    int buf = 0;
-    for (int n0 = lo; n0 < hi; n0 += kKeys, buf ^= 1) {
-        const bool more = n0 + kKeys < hi;
-        if (more) st.load(kb, vb, a.ldk, a.ldv, n0 + kKeys, hi, tid);
-        if (n0 < n_last) {
-            f32x16 s[2][QB];
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int b = 0; b < QB; ++b) s[t][b] = zero16();
-#pragma unroll
-            for (int e = 0; e < KS; ++e)
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const u32x4 kf = ad.rows(kt[buf], t, e);
-#pragma unroll
-                    for (int b = 0; b < QB; ++b) s[t][b] = mma(kf, q[b][e], s[t][b]);
-                }
-            if (n0 + kKeys > n_first) {
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int b = 0; b < QB; ++b)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (n0 + 32 * t + 8 * (i >> 2) + 4 * h + (i & 3) >= n[b]) s[t][b][i] = -INFINITY;
-            }
-            float mt[QB];
-            bool raise = false;
-#pragma unroll
-            for (int b = 0; b < QB; ++b) {
-                float x = s[0][b][0];
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) x = fmaxf(x, s[t][b][i]);
-                mt[b] = half_max(x) * c2;
-                raise = raise || mt[b] > m[b] + kSlack;
-            }
-            if (__any(raise)) {
-#pragma unroll
-                for (int b = 0; b < QB; ++b) {
-                    const float mn = fmaxf(m[b], mt[b]);
-                    const float al = mn == -INFINITY ? 1.f : exp2_f(m[b] - mn);
-                    m[b] = mn;
-                    l[b] *= al;
-#pragma unroll
-                    for (int e = 0; e < DB; ++e) acc[b][e] *= al;
-                }
-            }
-            u32x4 pf[2][QB][2];
-#pragma unroll
-            for (int b = 0; b < QB; ++b) {
-                const float ms = m[b] == -INFINITY ? 0.f : m[b];      // nothing visible so far
-                float sum = 0.f;
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        s[t][b][i] = exp2_f(__builtin_fmaf(s[t][b][i], c2, -ms));
-                        sum += s[t][b][i];
-                    }
-                    pf[t][b][0] = pack8(s[t][b], 0);
-                    pf[t][b][1] = pack8(s[t][b], 8);
-                }
-                l[b] += sum;                                          // this lane's keys; joined at the end
-            }
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int e = 0; e < DB; ++e) {
-                        const u32x4 vf = ad.cols(vt[buf], e, 2 * t + u);
-#pragma unroll
-                        for (int b = 0; b < QB; ++b) acc[b][e] = mma(vf, pf[t][b][u], acc[b][e]);
-                    }
-        }
-        if (more) st.store(kt[buf ^ 1], vt[buf ^ 1], tid);
+        sk.load(kb, a.ldk, lo, hi, tid);
+        sk.store(kt[0], tid);
+        if (lo + kKeys < hi) sk.load(kb, a.ldk, lo + kKeys, hi, tid);
+        sv.load(vb, a.ldv, lo, hi, tid);
+        for (int i = tid; i < HB / 16; i += NT) *reinterpret_cast<u32x4*>(vt[1] + HB + 16 * i) = none;
         __syncthreads();
-    }
+        f32x16 s0 = zero16(), s1;
+        u32x4 p0[2], p1[2] = {none, none};                    // no step before the first
 #pragma unroll
-    for (int b = 0; b < QB; ++b) {
-        const float ls = half_sum(l[b]);
-        const int row = w0 + 32 * b + r;
-        if (row >= rows) continue;
-        const float inv = ls > 0.f ? 1.0f / ls : ls;
-        const float lg = ls == 0.f ? -INFINITY : (m[b] + log2_f(ls)) * kLn2;
-        const int64_t gr = packed_row(a, z, p.hk, row);
-        if (a.splits > 1) {
-            const int64_t pr = (int64_t)p.split * a.total_q * a.Hq + gr;
-#pragma unroll
-            for (int e = 0; e < DB; ++e)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<f32x4*>(a.part_o + pr * D + 32 * e + 8 * i + 4 * h) =
-                        f32x4{acc[b][e][4 * i] * inv, acc[b][e][4 * i + 1] * inv, acc[b][e][4 * i + 2] * inv,
-                              acc[b][e][4 * i + 3] * inv};
-            if (h == 0) a.part_lse[pr] = lg;
-        } else {
-#pragma unroll
-            for (int e = 0; e < DB; ++e)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + gr * D + 32 * e + 8 * i + 4 * h) =
-                        u32x2{pack_bf16x2(acc[b][e][4 * i] * inv, acc[b][e][4 * i + 1] * inv),
-                              pack_bf16x2(acc[b][e][4 * i + 2] * inv, acc[b][e][4 * i + 3] * inv)};
-            if (h == 0 && a.lse) a.lse[gr] = lg;
+        for (int e = 0; e < KS; ++e) s0 = mma(ad.rows(kt[0], 0, e), q[e], s0);
+        int buf = 0;
+        for (int n0 = lo; n0 < hi; n0 += kKeys, buf ^= 1) {
+            // a step past the wave's last key still adds the step before it
+            if (n0 < n_last + 32) step(s0, s1, p1, p0, kt[buf] + HB, vt[buf ^ 1] + HB, n0);
+            sk.store(kt[buf ^ 1], tid);                       // past the last tile: never used
+            sv.store(vt[buf], tid);
+            __syncthreads();
+            if (n0 + kKeys < hi) {
+                if (n0 + 2 * kKeys < hi) sk.load(kb, a.ldk, n0 + 2 * kKeys, hi, tid);
+                sv.load(vb, a.ldv, n0 + kKeys, hi, tid);
+            }
+            if (n0 + 32 < n_last + 32) step(s1, s0, p0, p1, kt[buf ^ 1], vt[buf], n0 + 32);
         }
+        if ((hi - 1 - lo) / kKeys * kKeys + lo + 32 < n_last) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < DB; ++e) acc[e] = mma(ad.cols(vt[buf ^ 1] + HB, e, u), p1[u], acc[e]);
+        }
+    }
+    l = half_sum(l);
+    if (!valid) return;
+    const float inv = l > 0.f ? 1.0f / l : l;
+    const float lg = l == 0.f ? -INFINITY : (m + log2_f(l)) * kLn2;
+    const int64_t gr = packed_row(a, z, p.hk, row);
+    if (a.splits > 1) {
+        const int64_t pr = (int64_t)p.split * a.total_q * a.Hq + gr;
+#pragma unroll
+        for (int e = 0; e < DB; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<f32x4*>(a.part_o + pr * D + 32 * e + 8 * i + 4 * h) =
+                    f32x4{acc[e][4 * i] * inv, acc[e][4 * i + 1] * inv, acc[e][4 * i + 2] * inv,
+                          acc[e][4 * i + 3] * inv};
+        if (h == 0) a.part_lse[pr] = lg;
+    } else {
+#pragma unroll
+        for (int e = 0; e < DB; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + gr * D + 32 * e + 8 * i + 4 * h) =
+                    u32x2{pack_bf16x2(acc[e][4 * i] * inv, acc[e][4 * i + 1] * inv),
+                          pack_bf16x2(acc[e][4 * i + 2] * inv, acc[e][4 * i + 3] * inv)};
+        if (h == 0 && a.lse) a.lse[gr] = lg;
     }
 }
 
@@ -344,16 +339,21 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_dq_kernel(const AttnArgs a) {
     const float c2 = a.scale * kLog2e;
     Addr<D> ad;
     ad.init(lane);
-    Stage<D, NT> st;
+    Tile<D, NT> sk, sv;
     if (upto > 0) {
-        st.load(kb, vb, a.ldk, a.ldv, 0, upto, tid);
-        st.store(kt[0], vt[0], tid);
+        sk.load(kb, a.ldk, 0, upto, tid);
+        sv.load(vb, a.ldv, 0, upto, tid);
+        sk.store(kt[0], tid);
+        sv.store(vt[0], tid);
     }
     __syncthreads();
     int buf = 0;
     for (int n0 = 0; n0 < upto; n0 += kKeys, buf ^= 1) {
         const bool more = n0 + kKeys < upto;
-        if (more) st.load(kb, vb, a.ldk, a.ldv, n0 + kKeys, upto, tid);
+        if (more) {
+            sk.load(kb, a.ldk, n0 + kKeys, upto, tid);
+            sv.load(vb, a.ldv, n0 + kKeys, upto, tid);
+        }
         if (n0 < n_last) {
             const bool mask = n0 + kKeys > n_first;
 #pragma unroll
@@ -379,7 +379,10 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_dq_kernel(const AttnArgs a) {
                 }
             }
         }
-        if (more) st.store(kt[buf ^ 1], vt[buf ^ 1], tid);
+        if (more) {
+            sk.store(kt[buf ^ 1], tid);
+            sv.store(vt[buf ^ 1], tid);
+        }
         __syncthreads();
     }
     if (!valid) return;
@@ -583,12 +586,12 @@ bool grid_of(int64_t n, unsigned* g) {
     return true;
 }
 
-template <int D, int QB, int NW>
+template <int D, int NW>
 gdn_status launch_fwd(AttnArgs a, hipStream_t s) {
     unsigned grid;
-    const int64_t n = places(a.total_q * a.G, (int64_t)a.max_q * a.G, a.n_seq, 32 * QB * NW, a.cu_q, &a.tiles);
+    const int64_t n = places(a.total_q * a.G, (int64_t)a.max_q * a.G, a.n_seq, 32 * NW, a.cu_q, &a.tiles);
     if (!grid_of(n * a.splits * a.Hk, &grid)) return GDN_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL((attn_fwd_kernel<D, QB, NW>), dim3(grid), dim3(64 * NW), 0, s, a);
+    hipLaunchKernelGGL((attn_fwd_kernel<D, NW>), dim3(grid), dim3(64 * NW), 0, s, a);
     return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
@@ -640,12 +643,17 @@ int attn_bwd_bf16_splits(int64_t total_k, int max_q, int max_k, int n_seq, int H
     return (int)std::min<int64_t>(std::min<int64_t>((1024 + items - 1) / items, most), 64);
 }
 
-int attn_fwd_bf16_rows(int max_q, int G, int D) { return 128; }
+// Rows of a workgroup.  At D = 128 two waves fill a SIMD's registers: as one
+// workgroup of eight they share every key tile, where two of four stage each
+// tile twice (frame-causal clip of 18480 tokens, 16 heads: 1440 us against
+// 1476).  A decode step, whose rows fill a wave, takes the small one, since its
+// other waves only help to stage (eight requests: 80 us against 101).
+int attn_fwd_bf16_rows(int max_q, int G, int D) { return D == 128 && (int64_t)max_q * G > 256 ? 256 : 128; }
 
 gdn_status attn_fwd_bf16(const AttnArgs& a, hipStream_t s) {
-    if (a.D == 32) return launch_fwd<32, 1, 4>(a, s);
-    if (a.D == 64) return launch_fwd<64, 1, 4>(a, s);
-    return launch_fwd<128, 1, 4>(a, s);
+    if (a.D == 32) return launch_fwd<32, 4>(a, s);
+    if (a.D == 64) return launch_fwd<64, 4>(a, s);
+    return attn_fwd_bf16_rows(a.max_q, a.G, a.D) == 256 ? launch_fwd<128, 8>(a, s) : launch_fwd<128, 4>(a, s);
 }
 
 gdn_status attn_bwd_bf16(const AttnArgs& a, hipStream_t s) {
