@@ -23,11 +23,11 @@ def _ptr(t: Optional[torch.Tensor]):
 def _check(t: torch.Tensor, name: str, dtype, shape):
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("%s must be a device tensor (got %s)" % (name, t.device))
     if t.dtype != dtype:
         raise TypeError("%s must be %s (got %s)" % (name, dtype, t.dtype))
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError("%s must have shape %s (got %s)" % (name, tuple(shape), tuple(t.shape)))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
@@ -501,13 +501,15 @@ def _io(dtype: torch.dtype, what: str) -> int:
     raise TypeError("%s must be bfloat16 or float32 (got %s)" % (what, dtype))
 
 
-def _same_device(device, **tensors):
+def _same_device(x, **tensors):
+    index = x.get_device()
     for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError("%s must be on %s (got %s)" % (name, device, t.device))
+        if t is not None and t.get_device() != index:
+            raise ValueError("%s must be on %s (got %s)" % (name, x.device, t.device))
 
 
 _HERE = contextlib.nullcontext()
+_current_device = torch.cuda.current_device
 # the current stream's handle without a Stream object around it, where torch has it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -520,7 +522,7 @@ def _launch(stream, device):
     if stream is not None:
         return torch.cuda.stream(stream), stream.cuda_stream
     index = device.index
-    return (_HERE if index == torch.cuda.current_device() else torch.cuda.device(device)), _raw_stream(index)
+    return (_HERE if index == _current_device() else torch.cuda.device(device)), _raw_stream(index)
 
 
 def _workspace(workspace, n: int, device):
@@ -537,11 +539,12 @@ def _ws_bytes(workspace) -> int:
 def _norm_desc(x, weight, bias, eps):
     C = x.shape[-1] if x.dim() else 0
     rows = x.numel() // C if C else 0
-    w_dtype = next((t.dtype for t in (weight, bias) if t is not None), torch.float32)
-    for name, t in (("weight", weight), ("bias", bias)):
-        if t is not None:
-            _check(t, name, w_dtype, (C,))
-    return _lib.GdnNormDesc(rows, C, _io(x.dtype, "x"), _io(w_dtype, "weight"), float(eps))
+    w_dtype = torch.float32 if weight is None and bias is None else (bias if weight is None else weight).dtype
+    if weight is not None:
+        _check(weight, "weight", w_dtype, (C,))
+    if bias is not None:
+        _check(bias, "bias", w_dtype, (C,))
+    return _lib.GdnNormDesc(rows, C, _io(x.dtype, "x"), _io(w_dtype, "weight"), eps)
 
 
 def layer_norm_fwd(x, weight=None, bias=None, *, eps: float = 1e-6, y=None, mean=None, rstd=None,
@@ -557,14 +560,14 @@ def layer_norm_fwd(x, weight=None, bias=None, *, eps: float = 1e-6, y=None, mean
         raise TypeError("x must be a torch.Tensor")
     _check(x, "x", x.dtype, x.shape)
     desc = _norm_desc(x, weight, bias, eps)
-    stats = tuple(x.shape[:-1])
+    stats = x.shape[:-1]
     if y is not None:
         _check(y, "y", x.dtype, x.shape)
     if mean is not None:
         _check(mean, "mean", torch.float32, stats)
     if rstd is not None:
         _check(rstd, "rstd", torch.float32, stats)
-    _same_device(x.device, weight=weight, bias=bias, y=y, mean=mean, rstd=rstd)
+    _same_device(x, weight=weight, bias=bias, y=y, mean=mean, rstd=rstd)
     where, handle = _launch(stream, x.device)
     with where:   # allocations belong to the launch stream
         if y is None:
@@ -594,7 +597,7 @@ def layer_norm_bwd(dy, x, mean, rstd, weight=None, bias=None, *, dx=None, dweigh
     _check(x, "x", x.dtype, x.shape)
     _check(dy, "dy", x.dtype, x.shape)
     desc = _norm_desc(x, weight, bias, 1.0)   # eps acts through rstd
-    stats = tuple(x.shape[:-1])
+    stats = x.shape[:-1]
     _check(mean, "mean", torch.float32, stats)
     _check(rstd, "rstd", torch.float32, stats)
     if dx is not None:
@@ -605,7 +608,7 @@ def layer_norm_bwd(dy, x, mean, rstd, weight=None, bias=None, *, dx=None, dweigh
                 raise ValueError("%s needs its parameter" % name)
             _check(t, name, p.dtype, p.shape)
     _check_workspace(workspace, x.device)
-    _same_device(x.device, dy=dy, mean=mean, rstd=rstd, weight=weight, bias=bias, dx=dx, dweight=dweight, dbias=dbias)
+    _same_device(x, dy=dy, mean=mean, rstd=rstd, weight=weight, bias=bias, dx=dx, dweight=dweight, dbias=dbias)
     lib = _lib.load()
     where, handle = _launch(stream, x.device)
     with where:   # allocations belong to the launch stream
@@ -672,7 +675,7 @@ def rotary(q, k, pos, *, axes, theta: float = 10000.0, halves: bool = False, inv
     if n < 0 or n > len(lead):
         raise ValueError("pos must be [..., %d] over q's last token axes" % len(axes))
     _check(pos, "pos", pos.dtype, lead[len(lead) - n:] + (len(axes),))
-    _same_device(x.device, q=q, k=k, pos=pos, q_out=q_out, k_out=k_out)
+    _same_device(x, q=q, k=k, pos=pos, q_out=q_out, k_out=k_out)
     tokens = 1
     for s in lead:
         tokens *= s
@@ -766,7 +769,7 @@ def _attn_args(q, k, v, causal, causal_block, scale, cu_q, cu_k, max_q, max_k):
         if k.shape[0] != n_seq:
             raise ValueError("q and k must have the same batch size")
         max_q, max_k = (tq // n_seq, tk // n_seq) if n_seq else (0, 0)
-    _same_device(q.device, k=k, v=v, cu_q=cu_q, cu_k=cu_k)
+    _same_device(q, k=k, v=v, cu_q=cu_q, cu_k=cu_k)
     desc = _lib.GdnAttnDesc(tq, tk, ldq, ldk, ldv, rk, n_seq, Hq, Hk, D, max_q, max_k, int(causal_block),
                             _io(q.dtype, "q"), _lib.GDN_FLAG_ATTN_CAUSAL if causal else 0,
                             float(D ** -0.5 if scale is None else scale))
@@ -798,7 +801,7 @@ def attention_fwd(q, k, v, *, causal: bool = False, causal_block: Optional[int] 
     if lse is not None:
         _check(lse, "lse", torch.float32, q.shape[:-1])
     _check_workspace(workspace, q.device)
-    _same_device(q.device, k_len=k_len, o=o, lse=lse)
+    _same_device(q, k_len=k_len, o=o, lse=lse)
     lib = _lib.load()
     where, handle = _launch(stream, q.device)
     with where:   # allocations belong to the launch stream
@@ -829,7 +832,7 @@ def attention_bwd(q, k, v, o, lse, dO, *, causal: bool = False, causal_block: Op
         if t is not None:
             _check(t, name, like.dtype, like.shape)
     _check_workspace(workspace, q.device)
-    _same_device(q.device, o=o, lse=lse, dO=dO, dq=dq, dk=dk, dv=dv)
+    _same_device(q, o=o, lse=lse, dO=dO, dq=dq, dk=dk, dv=dv)
     lib = _lib.load()
     where, handle = _launch(stream, q.device)
     with where:   # allocations belong to the launch stream

@@ -69,14 +69,28 @@ __device__ __forceinline__ void row_frag(f32x4 (&f)[D / 16], const T* row, bool 
     for (int s = 0; s < D / 16; ++s) f[s] = valid ? load4(row + 16 * s + 4 * g) : f32x4{0.f, 0.f, 0.f, 0.f};
 }
 
-// Rows [n0, n0 + kTile) of a key tensor into LDS as fp32, zeros from hi on.
+// Rows [n0, n0 + kTile) of a key tensor, zeros from hi on: to registers while
+// the tile before is computed on, then to LDS as fp32.
 template <typename T, int D>
-__device__ __forceinline__ void stage(float (*t)[D + 4], const T* base, int64_t ld, int n0, int hi) {
-    for (int c = threadIdx.x; c < kTile * D / 4; c += kThreads) {
-        const int n = c / (D / 4), e = c % (D / 4) * 4;
-        store4(&t[n][e], n0 + n < hi ? load4(base + (int64_t)(n0 + n) * ld + e) : f32x4{0.f, 0.f, 0.f, 0.f});
+struct Stage {
+    static constexpr int C = kTile * D / 4, N = (C + kThreads - 1) / kThreads;
+    f32x4 x[N];
+    __device__ __forceinline__ void load(const T* base, int64_t ld, int n0, int hi) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int c = (int)threadIdx.x + j * kThreads, n = c / (D / 4), e = c % (D / 4) * 4;
+            x[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (n0 + n < hi && c < C) x[j] = load4(base + (int64_t)(n0 + n) * ld + e);
+        }
     }
-}
+    __device__ __forceinline__ void store(float (*t)[D + 4]) const {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int c = (int)threadIdx.x + j * kThreads;
+            if (c < C) store4(&t[c / (D / 4)][c % (D / 4) * 4], x[j]);
+        }
+    }
+};
 
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void attn_fwd_f32_kernel(const AttnArgs a) {
@@ -101,11 +115,16 @@ __global__ __launch_bounds__(kThreads) void attn_fwd_f32_kernel(const AttnArgs a
     const T* vb = static_cast<const T*>(a.v) + z.k0 * a.ldv + (int64_t)p.hk * D;
     const float c2 = a.scale * kLog2e;
     float m = -INFINITY, l = 0.f;
+    Stage<T, D> sk, sv;
+    sk.load(kb, a.ldk, lo, hi);
+    sv.load(vb, a.ldv, lo, hi);
     for (int n0 = lo; n0 < hi; n0 += kTile) {
         __syncthreads();
-        stage<T, D>(kt, kb, a.ldk, n0, hi);
-        stage<T, D>(vt, vb, a.ldv, n0, hi);
+        sk.store(kt);
+        sv.store(vt);
         __syncthreads();
+        sk.load(kb, a.ldk, n0 + kTile, hi);
+        sv.load(vb, a.ldv, n0 + kTile, hi);
         f32x4 s[2];
         float mt = -INFINITY;
 #pragma unroll
@@ -252,11 +271,16 @@ __global__ __launch_bounds__(kThreads) void attn_dq_f32_kernel(const AttnArgs a)
     for (int e = 0; e < D / 16; ++e) acc[e] = f32x4{0.f, 0.f, 0.f, 0.f};
     const T* kb = static_cast<const T*>(a.k) + z.k0 * a.ldk + (int64_t)p.hk * D;
     const T* vb = static_cast<const T*>(a.v) + z.k0 * a.ldv + (int64_t)p.hk * D;
+    Stage<T, D> sk, sv;
+    sk.load(kb, a.ldk, 0, upto);
+    sv.load(vb, a.ldv, 0, upto);
     for (int n0 = 0; n0 < upto; n0 += kTile) {
         __syncthreads();
-        stage<T, D>(kt, kb, a.ldk, n0, upto);
-        stage<T, D>(vt, vb, a.ldv, n0, upto);
+        sk.store(kt);
+        sv.store(vt);
         __syncthreads();
+        sk.load(kb, a.ldk, n0 + kTile, upto);
+        sv.load(vb, a.ldv, n0 + kTile, upto);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f}, dp = s;
@@ -304,33 +328,56 @@ __global__ __launch_bounds__(kThreads) void attn_dkv_f32_kernel(const AttnArgs a
     for (int e = 0; e < D / 16; ++e) ak[e] = av[e] = f32x4{0.f, 0.f, 0.f, 0.f};
     const float c2 = a.scale * kLog2e;
     const int rows = z.lq * a.G;
-    for (int r0 = first_query(a, z, k0) * a.G; r0 < rows; r0 += kTile) {
-        __syncthreads();
-        for (int x = threadIdx.x; x < kTile * D / 4; x += kThreads) {
-            const int n = x / (D / 4), e = x % (D / 4) * 4;
-            f32x4 qv = f32x4{0.f, 0.f, 0.f, 0.f}, dv = qv;
-            if (r0 + n < rows) {
-                qv = load4(q_row<T>(a, z, p.hk, r0 + n) + e);
-                dv = load4(static_cast<const T*>(a.d_o) + packed_row(a, z, p.hk, r0 + n) * D + e);
+    int start = min(first_query(a, z, k0) * a.G, rows), end = rows;
+    if (a.k_splits > 1) {
+        int lo, hi;
+        split_range(rows - start, kTile, a.k_splits, p.split, lo, hi);
+        end = start + hi;
+        start += lo;
+    }
+    constexpr int C = kTile * D / 4, N = (C + kThreads - 1) / kThreads;
+    f32x4 xq[N], xd[N];
+    float xl = 0.f, xs = 0.f;
+    int xn = 0;
+    auto load = [&](int r0) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int x = (int)threadIdx.x + j * kThreads, r = r0 + x / (D / 4), e = x % (D / 4) * 4;
+            xq[j] = xd[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (x < C && r < end) {
+                xq[j] = load4(q_row<T>(a, z, p.hk, r) + e);
+                xd[j] = load4(static_cast<const T*>(a.d_o) + packed_row(a, z, p.hk, r) * D + e);
             }
-            store4(&qt[n][e], qv);
-            store4(&dt[n][e], dv);
+        }
+        const int r = r0 + (int)threadIdx.x;
+        xl = xs = 0.f;
+        xn = 0;
+        if (threadIdx.x < kTile && r < end) {
+            const int64_t gr = packed_row(a, z, p.hk, r);
+            xl = a.lse[gr] * kLog2e;
+            xs = a.delta[gr];
+            xn = xl == -INFINITY ? 0 : visible(a, z, r / a.G);
+            if (xl == -INFINITY) xl = 0.f;
+        }
+    };
+    load(start);
+    for (int r0 = start; r0 < end; r0 += kTile) {
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int x = (int)threadIdx.x + j * kThreads;
+            if (x < C) {
+                store4(&qt[x / (D / 4)][x % (D / 4) * 4], xq[j]);
+                store4(&dt[x / (D / 4)][x % (D / 4) * 4], xd[j]);
+            }
         }
         if (threadIdx.x < kTile) {
-            const int r = r0 + threadIdx.x;
-            float l = -INFINITY, d = 0.f;
-            int n = 0;
-            if (r < rows) {
-                const int64_t gr = packed_row(a, z, p.hk, r);
-                l = a.lse[gr] * kLog2e;
-                d = a.delta[gr];
-                n = visible(a, z, r / a.G);
-            }
-            ls[threadIdx.x] = l == -INFINITY ? 0.f : l;
-            dl[threadIdx.x] = d;
-            nv[threadIdx.x] = l == -INFINITY ? 0 : n;
+            ls[threadIdx.x] = xl;
+            dl[threadIdx.x] = xs;
+            nv[threadIdx.x] = xn;
         }
         __syncthreads();
+        load(r0 + kTile);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f}, dp = s;
@@ -357,12 +404,40 @@ __global__ __launch_bounds__(kThreads) void attn_dkv_f32_kernel(const AttnArgs a
         }
     }
     if (!valid) return;
+    if (a.k_splits > 1) {
+        const int64_t at = (((int64_t)p.split * a.total_k + z.ko + key) * a.Hk + p.hk) * D;
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e) {
+            store4(a.part_k + at + 16 * e + 4 * g, ak[e]);
+            store4(a.part_v + at + 16 * e + 4 * g, av[e]);
+        }
+        return;
+    }
     const int64_t kr = ((z.ko + key) * a.Hk + p.hk) * D;
 #pragma unroll
     for (int e = 0; e < D / 16; ++e) {
         store4(static_cast<T*>(a.dk) + kr + 16 * e + 4 * g, ak[e] * a.scale);
         store4(static_cast<T*>(a.dv) + kr + 16 * e + 4 * g, av[e]);
     }
+}
+
+// dk and dv from the splits' sums, four features a thread.  The keys are the
+// sequences' own; what lies outside them is left alone.
+template <typename T, int D>
+__global__ __launch_bounds__(kThreads) void attn_sum_kernel(const AttnArgs a) {
+    const unsigned per = kThreads / (D / 4), groups = ((unsigned)a.max_k * a.Hk + per - 1) / per;
+    const Seq z = sequence(a, (int)(blockIdx.x / groups));
+    const int64_t r = (int64_t)(blockIdx.x % groups) * per + threadIdx.x / (D / 4);
+    if (r >= (int64_t)z.lk * a.Hk) return;
+    const int64_t at = (z.ko * a.Hk + r) * D + threadIdx.x % (D / 4) * 4, all = a.total_k * a.Hk * D;
+    f32x4 k = {0.f, 0.f, 0.f, 0.f}, v = k;
+    for (int i = 0; i < a.k_splits; ++i) {
+        k += *reinterpret_cast<const f32x4*>(a.part_k + i * all + at);
+        v += *reinterpret_cast<const f32x4*>(a.part_v + i * all + at);
+    }
+    k *= a.scale;
+    store4(static_cast<T*>(a.dk) + at, k);
+    store4(static_cast<T*>(a.dv) + at, v);
 }
 
 // ---------------------------------------------------------------- launch
@@ -401,14 +476,14 @@ int fwd_rows(const gdn_attn_desc* d) {
 // 256 in one round (with two waves a SIMD).  A decode step (a few rows a key
 // head) is cut eight times finer, because the lengths of its caches differ and
 // short work spreads evenly; a split's fp32 partial result is then small
-// against its keys, of which it takes 512 at least.
+// against its keys, of which it takes 512 at least (128 at the fp32 rate).
 int fwd_chunk(const gdn_attn_desc* d) {
     const int64_t rows = (int64_t)d->max_q * (d->Hq / d->Hk);
     const int64_t units = (int64_t)d->n_seq * d->Hk * std::max<int64_t>(1, (rows + fwd_rows(d) - 1) / fwd_rows(d));
     int64_t n = (fwd_rows(d) == 256 ? 256 : 512) / std::max<int64_t>(units, 1);
     if (rows <= 32) n *= 8;
     if (n < 2) return std::max(d->max_k, 1);
-    const int64_t chunk = std::max<int64_t>(((d->max_k + n - 1) / n + 63) / 64 * 64, 512);
+    const int64_t chunk = std::max<int64_t>(((d->max_k + n - 1) / n + 63) / 64 * 64, fast(d) ? 512 : 128);
     return (int)std::min<int64_t>(chunk, std::max(d->max_k, 1));
 }
 int fwd_splits(const gdn_attn_desc* d) {
@@ -416,16 +491,20 @@ int fwd_splits(const gdn_attn_desc* d) {
     return std::max(1, (d->max_k + chunk - 1) / chunk);
 }
 
-// Splits of the query rows in the bf16 dk/dv kernel.  Its workgroups each walk
-// all the rows that see their keys; with few key tiles (grouped heads: few
-// heads with many rows each) that leaves compute units idle and the first
-// tiles' long walks last, so below two workgroups a unit the rows are split for
-// about four.  A split's fp32 sums cost 16 D bytes a key, its products 8 D
-// flops a (row, key): from 1024 rows a split on, the former stay a small part.
-// The sizes do not depend on the lengths on the device, nor on whether the
-// sequences are packed (uniform ones count the same tiles).
+// Splits of the query rows in the dk/dv kernel.  Its workgroups each walk all
+// the rows that see their keys; with few key tiles (grouped heads: few heads
+// with many rows each) that leaves compute units idle and the first tiles' long
+// walks last, so below two workgroups a unit the rows are split for about four.
+// A split's fp32 sums cost 16 D bytes a key, its products 8 D flops a (row,
+// key): from 1024 rows a split on (128 at the fp32 rate) the former stay a
+// small part.  The sizes do not depend on the lengths on the device, nor on
+// whether the sequences are packed (uniform ones count the same tiles).
 int bwd_splits(const gdn_attn_desc* d) {
-    return fast(d) ? attn_bwd_bf16_splits(d->total_k, d->max_q, d->max_k, d->n_seq, d->Hk, d->Hq / d->Hk) : 1;
+    int tiles;
+    const int64_t items = places(d->total_k, d->max_k, d->n_seq, fast(d) ? 128 : kRows, true, &tiles) * d->Hk;
+    const int64_t most = (int64_t)d->max_q * (d->Hq / d->Hk) / (fast(d) ? 1024 : 128);
+    if (items < 1 || items >= 512 || most < 2) return 1;
+    return (int)std::min<int64_t>(std::min<int64_t>((1024 + items - 1) / items, most), 64);
 }
 
 AttnArgs fill(const gdn_attn_desc* d) {
@@ -482,8 +561,17 @@ gdn_status run_bwd(AttnArgs a, hipStream_t s) {
     if (!grid_of(n * a.Hk, &grid)) return GDN_ERR_UNSUPPORTED;
     if (grid) hipLaunchKernelGGL((attn_dq_f32_kernel<T, D>), dim3(grid), dim3(kThreads), 0, s, a);
     n = places(a.total_k, a.max_k, a.n_seq, kRows, a.cu_k, &a.tiles);
-    if (!grid_of(n * a.Hk, &grid)) return GDN_ERR_UNSUPPORTED;
+    if (!grid_of(n * a.Hk * a.k_splits, &grid)) return GDN_ERR_UNSUPPORTED;
     if (grid) hipLaunchKernelGGL((attn_dkv_f32_kernel<T, D>), dim3(grid), dim3(kThreads), 0, s, a);
+    return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
+template <typename T, int D>
+gdn_status run_sum(const AttnArgs& a, hipStream_t s) {
+    unsigned grid;
+    const int64_t per = kThreads / (D / 4);
+    if (!grid_of(((int64_t)a.max_k * a.Hk + per - 1) / per * a.n_seq, &grid)) return GDN_ERR_UNSUPPORTED;
+    if (grid) hipLaunchKernelGGL((attn_sum_kernel<T, D>), dim3(grid), dim3(kThreads), 0, s, a);
     return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
@@ -600,7 +688,10 @@ gdn_status gdn_attn_bwd(const gdn_attn_desc* d, const void* q, const void* k, co
         a.part_v = reinterpret_cast<float*>(w + round256((size_t)a.k_splits * d->total_k * d->Hk * d->D * 4));
     }
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    return d->io_dtype == GDN_F32 ? GDN_BY_D(run_bwd, float, a, s) : fast(d) ? attn_bwd_bf16(a, s) : run_bwd<uint16_t, 16>(a, s);
+    const bool f32 = d->io_dtype == GDN_F32;
+    st = f32 ? GDN_BY_D(run_bwd, float, a, s) : fast(d) ? attn_bwd_bf16(a, s) : run_bwd<uint16_t, 16>(a, s);
+    if (st != GDN_OK || a.k_splits == 1) return st;
+    return f32 ? GDN_BY_D(run_sum, float, a, s) : GDN_BY_D(run_sum, uint16_t, a, s);
 }
 
 }  // extern "C"

@@ -202,8 +202,6 @@ __device__ __forceinline__ float log2_f(float x) { return __builtin_amdgcn_logf(
 // Kernels in bf16 matrix instructions (gdn_attn_bf16.hip), D in {32, 64, 128}.
 gdn_status attn_fwd_bf16(const AttnArgs& a, hipStream_t s);
 gdn_status attn_bwd_bf16(const AttnArgs& a, hipStream_t s);
-// Splits of the row axis in the dk/dv kernel.
-int attn_bwd_bf16_splits(int64_t total_k, int max_q, int max_k, int n_seq, int Hk, int G);
 // Row tile of the forward kernel that these arguments select.
 int attn_fwd_bf16_rows(int max_q, int G, int D);
 

@@ -60,28 +60,29 @@ __device__ __forceinline__ u32x2 read_tr(const unsigned char* p) {
     typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
     return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p));
 }
-// A lane's addresses in a tile.
+// A lane's addresses in a tile.  The permutation is an exclusive or within the
+// bits that the chunk alone sets, so all of them follow from three.  renew()
+// keeps the compiler from holding the rest (16 registers at D = 128) across the
+// whole loop, where the backward kernels have none to spare.
 template <int D>
 struct Addr {
-    uint32_t row[D / 16], lo[D / 32], hi[D / 32];
+    uint32_t row, lo, hi;
     __device__ __forceinline__ void init(int lane) {
         const int h = lane >> 5, r = lane & 31, j = lane >> 4, q = lane & 15;
-#pragma unroll
-        for (int e = 0; e < D / 16; ++e) row[e] = chunk_at<D>(r, 2 * e + h);
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) {
-            const int k = 4 * (j >> 1) + (q >> 2), c = 4 * e + 2 * (j & 1) + ((q >> 1) & 1);
-            lo[e] = chunk_at<D>(k, c) + (q & 1) * 8;
-            hi[e] = chunk_at<D>(k + 8, c) + (q & 1) * 8;
-        }
+        const int k = 4 * (j >> 1) + (q >> 2), c = 2 * (j & 1) + ((q >> 1) & 1);
+        row = chunk_at<D>(r, h);
+        lo = chunk_at<D>(k, c) + (q & 1) * 8;
+        hi = chunk_at<D>(k + 8, c) + (q & 1) * 8;
     }
+    __device__ __forceinline__ void renew() { asm volatile("" : "+v"(row), "+v"(lo), "+v"(hi)); }
     // rows 32 t + r, features 16 e + 8 h .. + 7
     __device__ __forceinline__ u32x4 rows(const unsigned char* tile, int t, int e) const {
-        return *reinterpret_cast<const u32x4*>(tile + row[e] + t * 64 * D);
+        return *reinterpret_cast<const u32x4*>(tile + (row ^ (uint32_t)(32 * e)) + t * 64 * D);
     }
     // features 32 e + r, rows 16 s + 4 h + 0..3 and 16 s + 8 + 4 h + 0..3
     __device__ __forceinline__ u32x4 cols(const unsigned char* tile, int e, int s) const {
-        const u32x2 a = read_tr(tile + lo[e] + s * 32 * D), b = read_tr(tile + hi[e] + s * 32 * D);
+        const u32x2 a = read_tr(tile + (lo ^ (uint32_t)(64 * e)) + s * 32 * D);
+        const u32x2 b = read_tr(tile + (hi ^ (uint32_t)(64 * e)) + s * 32 * D);
         return u32x4{a[0], a[1], b[0], b[1]};
     }
 };
@@ -359,13 +360,15 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_dq_kernel(const AttnArgs a) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 f32x16 s = zero16(), dp = zero16();
+                ad.renew();
 #pragma unroll
-                for (int e = 0; e < KS; ++e) {
-                    s = mma(ad.rows(kt[buf], t, e), q[e], s);
-                    dp = mma(ad.rows(vt[buf], t, e), g[e], dp);
-                }
+                for (int e = 0; e < KS; ++e) s = mma(ad.rows(kt[buf], t, e), q[e], s);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) s[i] = exp2_f(__builtin_fmaf(s[i], c2, -ls)) * (dp[i] - delta);
+                for (int e = 0; e < KS; ++e) dp = mma(ad.rows(vt[buf], t, e), g[e], dp);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[i] = exp2_f(__builtin_fmaf(s[i], c2, -ls));
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[i] *= dp[i] - delta;
                 if (mask) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
@@ -516,35 +519,40 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_kernel(const AttnArgs a) 
 #pragma unroll
             for (int t = 0; t < RT / 32; ++t) {
                 f32x16 s = zero16(), dp = zero16();
+                ad.renew();
 #pragma unroll
-                for (int e = 0; e < KS; ++e) {
-                    s = mma(ad.rows(qt[buf], t, e), kf[e], s);
+                for (int e = 0; e < KS; ++e) s = mma(ad.rows(qt[buf], t, e), kf[e], s);
+#pragma unroll
+                for (int e = 0; e < KS; ++e)
                     dp = mma(ad.rows(gt[buf], t, e), VL ? ad.rows(vl + wave * 64 * D, 0, e) : vf[VL ? 0 : e], dp);
-                }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const f32x4 l4 = *reinterpret_cast<const f32x4*>(&lt[buf][32 * t + 8 * i + 4 * h]);
-                    const f32x4 d4 = *reinterpret_cast<const f32x4*>(&dt[buf][32 * t + 8 * i + 4 * h]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float pr = exp2_f(__builtin_fmaf(s[4 * i + j], c2, -l4[j]));
-                        dp[4 * i + j] = pr * (dp[4 * i + j] - d4[j]);
-                        s[4 * i + j] = pr;
-                    }
+                    for (int j = 0; j < 4; ++j) s[4 * i + j] = exp2_f(__builtin_fmaf(s[4 * i + j], c2, -l4[j]));
                 }
                 if (mask) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        if (r0 + 32 * t + 8 * (i >> 2) + 4 * h + (i & 3) < from) s[i] = dp[i] = 0.f;
+                        if (r0 + 32 * t + 8 * (i >> 2) + 4 * h + (i & 3) < from) s[i] = 0.f;
                 }
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const u32x4 pp = pack8(s, 8 * u), ds = pack8(dp, 8 * u);
+                    const u32x4 pp = pack8(s, 8 * u);
 #pragma unroll
-                    for (int e = 0; e < DB; ++e) {
-                        av[e] = mma(ad.cols(gt[buf], e, 2 * t + u), pp, av[e]);
-                        ak[e] = mma(ad.cols(qt[buf], e, 2 * t + u), ds, ak[e]);
-                    }
+                    for (int e = 0; e < DB; ++e) av[e] = mma(ad.cols(gt[buf], e, 2 * t + u), pp, av[e]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const f32x4 d4 = *reinterpret_cast<const f32x4*>(&dt[buf][32 * t + 8 * i + 4 * h]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[4 * i + j] *= dp[4 * i + j] - d4[j];
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const u32x4 ds = pack8(s, 8 * u);
+#pragma unroll
+                    for (int e = 0; e < DB; ++e) ak[e] = mma(ad.cols(qt[buf], e, 2 * t + u), ds, ak[e]);
                 }
             }
         }
@@ -595,53 +603,19 @@ gdn_status launch_fwd(AttnArgs a, hipStream_t s) {
     return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
-// dk and dv from the splits' sums, four features a thread.  The keys are the
-// sequences' own; what lies outside them is left alone.
-template <int D>
-__global__ __launch_bounds__(256) void attn_sum_kernel(const AttnArgs a) {
-    const unsigned per = 256 / (D / 4), groups = ((unsigned)a.max_k * a.Hk + per - 1) / per;
-    const Seq z = sequence(a, (int)(blockIdx.x / groups));
-    const int64_t r = (int64_t)(blockIdx.x % groups) * per + threadIdx.x / (D / 4);
-    if (r >= (int64_t)z.lk * a.Hk) return;
-    const int64_t at = (z.ko * a.Hk + r) * D + threadIdx.x % (D / 4) * 4, all = a.total_k * a.Hk * D;
-    f32x4 k = {0.f, 0.f, 0.f, 0.f}, v = k;
-    for (int i = 0; i < a.k_splits; ++i) {
-        k += *reinterpret_cast<const f32x4*>(a.part_k + i * all + at);
-        v += *reinterpret_cast<const f32x4*>(a.part_v + i * all + at);
-    }
-    k *= a.scale;
-    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.dk) + at) =
-        u32x2{pack_bf16x2(k[0], k[1]), pack_bf16x2(k[2], k[3])};
-    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.dv) + at) =
-        u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-}
-
-template <int D>
+template <int D, int NW>
 gdn_status launch_bwd(AttnArgs a, hipStream_t s) {
     unsigned grid;
-    int64_t n = places(a.total_q * a.G, (int64_t)a.max_q * a.G, a.n_seq, 128, a.cu_q, &a.tiles);
+    int64_t n = places(a.total_q * a.G, (int64_t)a.max_q * a.G, a.n_seq, 32 * NW, a.cu_q, &a.tiles);
     if (!grid_of(n * a.Hk, &grid)) return GDN_ERR_UNSUPPORTED;
-    if (grid) hipLaunchKernelGGL((attn_dq_kernel<D, 4>), dim3(grid), dim3(256), 0, s, a);
-    n = places(a.total_k, a.max_k, a.n_seq, 128, a.cu_k, &a.tiles);
+    if (grid) hipLaunchKernelGGL((attn_dq_kernel<D, NW>), dim3(grid), dim3(64 * NW), 0, s, a);
+    n = places(a.total_k, a.max_k, a.n_seq, 32 * NW, a.cu_k, &a.tiles);
     if (!grid_of(n * a.Hk * a.k_splits, &grid)) return GDN_ERR_UNSUPPORTED;
-    if (grid) hipLaunchKernelGGL((attn_dkv_kernel<D, 4, (D == 128 ? 32 : 64)>), dim3(grid), dim3(256), 0, s, a);
-    if (grid && a.k_splits > 1) {
-        const int64_t per = 256 / (D / 4);
-        if (!grid_of(((int64_t)a.max_k * a.Hk + per - 1) / per * a.n_seq, &grid)) return GDN_ERR_UNSUPPORTED;
-        hipLaunchKernelGGL(attn_sum_kernel<D>, dim3(grid), dim3(256), 0, s, a);
-    }
+    if (grid) hipLaunchKernelGGL((attn_dkv_kernel<D, NW, (D == 128 ? 32 : 64)>), dim3(grid), dim3(64 * NW), 0, s, a);
     return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
 }  // namespace
-
-int attn_bwd_bf16_splits(int64_t total_k, int max_q, int max_k, int n_seq, int Hk, int G) {
-    int tiles;
-    const int64_t items = places(total_k, max_k, n_seq, 128, true, &tiles) * Hk;
-    const int64_t most = (int64_t)max_q * G / 1024;
-    if (items < 1 || items >= 512 || most < 2) return 1;
-    return (int)std::min<int64_t>(std::min<int64_t>((1024 + items - 1) / items, most), 64);
-}
 
 // Rows of a workgroup.  At D = 128 two waves fill a SIMD's registers: as one
 // workgroup of eight they share every key tile, where two of four stage each
@@ -657,9 +631,9 @@ gdn_status attn_fwd_bf16(const AttnArgs& a, hipStream_t s) {
 }
 
 gdn_status attn_bwd_bf16(const AttnArgs& a, hipStream_t s) {
-    if (a.D == 32) return launch_bwd<32>(a, s);
-    if (a.D == 64) return launch_bwd<64>(a, s);
-    return launch_bwd<128>(a, s);
+    if (a.D == 32) return launch_bwd<32, 4>(a, s);
+    if (a.D == 64) return launch_bwd<64, 4>(a, s);
+    return launch_bwd<128, 4>(a, s);
 }
 
 }  // namespace gdnattn

@@ -345,31 +345,31 @@ __global__ __launch_bounds__(kThreads) void norm_wide_dw_kernel(const NormArgs a
     pw[a.C + c] = db;
 }
 
-// dw[c] = sum over the groups' partial rows, 64 columns a workgroup; the four
-// waves take every fourth row and add up through LDS in order.
+// dw[c] = sum over the groups' partial rows, 64 columns a workgroup; its 16
+// waves take every sixteenth row and add up through LDS in order.
+constexpr int kColWaves = 16;
 template <typename W>
-__global__ __launch_bounds__(kThreads) void norm_colsum_kernel(const float* __restrict__ part, int groups, int C,
-                                                               W* __restrict__ dw, W* __restrict__ db) {
-    __shared__ float red[kWaves][64];
+__global__ __launch_bounds__(64 * kColWaves) void norm_colsum_kernel(const float* __restrict__ part, int groups, int C,
+                                                                     W* __restrict__ dw, W* __restrict__ db) {
+    __shared__ float red[kColWaves][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int n = blockIdx.x * 64 + lane;                // columns of [2][C]
     float s = 0.f;
     if (n < 2 * C) {
+        float u[4] = {0.f, 0.f, 0.f, 0.f};
         int p = wave;
-        float u0 = 0.f, u1 = 0.f, u2 = 0.f, u3 = 0.f;
-        for (; p + 12 < groups; p += 16) {
-            u0 += part[(size_t)p * 2 * C + n];
-            u1 += part[(size_t)(p + 4) * 2 * C + n];
-            u2 += part[(size_t)(p + 8) * 2 * C + n];
-            u3 += part[(size_t)(p + 12) * 2 * C + n];
-        }
-        for (; p < groups; p += 4) u0 += part[(size_t)p * 2 * C + n];
-        s = (u0 + u1) + (u2 + u3);
+        for (; p + 3 * kColWaves < groups; p += 4 * kColWaves)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[i] += part[(size_t)(p + i * kColWaves) * 2 * C + n];
+        for (; p < groups; p += kColWaves) u[0] += part[(size_t)p * 2 * C + n];
+        s = (u[0] + u[1]) + (u[2] + u[3]);
     }
     red[wave][lane] = s;
     __syncthreads();
     if (wave == 0 && n < 2 * C) {
-        s = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+        s = 0.f;
+#pragma unroll
+        for (int w = 0; w < kColWaves; ++w) s += red[w][lane];
         if (n < C) {
             if (dw) dw[n] = from_f<W>(s);
         } else if (db) {
@@ -400,15 +400,16 @@ bool shape_of(int C, int* nv, int* wpr) {
             }
     return false;
 }
-// Workgroups of the backward pass: enough to fill the card (four a compute
-// unit), and no more than leaves each wave a few rows, since every workgroup
-// writes a row of partial sums that is read back (64 MiB of them at most, or 16
+// Workgroups of the backward pass: one a compute unit first, then as many as
+// leave each wave a few rows (up to four a unit), since every workgroup writes
+// a row of partial sums that is read back (64 MiB of them at most, or 16
 // rows).
 int bwd_groups(const gdn_norm_desc* d) {
     int nv = 0, wpr = 4;
     shape_of(d->C, &nv, &wpr);
     const int64_t rpb = kWaves / wpr;
-    const int64_t g = (d->rows + 4 * rpb - 1) / (4 * rpb);
+    const int64_t g = std::max((d->rows + 4 * rpb - 1) / (4 * rpb),
+                               std::min<int64_t>((d->rows + rpb - 1) / rpb, 256));
     const int64_t most = std::min<int64_t>(kMaxPartials, std::max<int64_t>(16, ((int64_t)64 << 20) / (8 * (int64_t)d->C)));
     return (int)std::min(std::max<int64_t>(g, 1), most);
 }
@@ -464,7 +465,7 @@ gdn_status launch_bwd(const NormArgs& a, int groups, void* dw, void* db, int cus
         if (hipGetLastError() != hipSuccess) return GDN_ERR_LAUNCH;
     }
     if (dw || db) {
-        hipLaunchKernelGGL(norm_colsum_kernel<W>, dim3((2 * a.C + 63) / 64), dim3(kThreads), 0, s, a.part,
+        hipLaunchKernelGGL(norm_colsum_kernel<W>, dim3((2 * a.C + 63) / 64), dim3(64 * kColWaves), 0, s, a.part,
                            a.rows > 0 ? groups : 0, a.C, static_cast<W*>(dw), static_cast<W*>(db));
         if (hipGetLastError() != hipSuccess) return GDN_ERR_LAUNCH;
     }
