@@ -354,10 +354,9 @@ __global__ __launch_bounds__(kThreads) void attn_dkv_f32_kernel(const AttnArgs a
         xn = 0;
         if (threadIdx.x < kTile && r < end) {
             const int64_t gr = packed_row(a, z, p.hk, r);
-            xl = a.lse[gr] * kLog2e;
+            xl = a.lse[gr];                                   // used after the tile before
             xs = a.delta[gr];
-            xn = xl == -INFINITY ? 0 : visible(a, z, r / a.G);
-            if (xl == -INFINITY) xl = 0.f;
+            xn = visible(a, z, r / a.G);
         }
     };
     load(start);
@@ -372,9 +371,9 @@ __global__ __launch_bounds__(kThreads) void attn_dkv_f32_kernel(const AttnArgs a
             }
         }
         if (threadIdx.x < kTile) {
-            ls[threadIdx.x] = xl;
+            ls[threadIdx.x] = xl == -INFINITY ? 0.f : xl * kLog2e;
             dl[threadIdx.x] = xs;
-            nv[threadIdx.x] = xn;
+            nv[threadIdx.x] = xl == -INFINITY ? 0 : xn;
         }
         __syncthreads();
         load(r0 + kTile);

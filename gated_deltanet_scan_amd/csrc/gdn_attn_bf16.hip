@@ -419,18 +419,20 @@ struct RowStage {
             const int i = tid + j * NT, rr = i / (D / 8), c = i % (D / 8);
             const uint32_t x = (uint32_t)(g0 + rr);
             const uint32_t tok = a.G == 1 ? x : __umulhi(x, inv), gg = x - tok * a.G;
-            const bool in = r0 + rr < rows;                    // rows past the last read as zeros
+            const uint32_t past = r0 + rr < rows ? 0u : 0x80000000u;   // rows past the last read as zeros
             const uint32_t at = gg * (2 * D) + c * 16;
-            q[j] = __builtin_amdgcn_raw_buffer_load_b128(rq, in ? tok * (uint32_t)(a.ldq * 2) + at : 0x80000000u, 0, 0);
-            g[j] = __builtin_amdgcn_raw_buffer_load_b128(rg, in ? tok * (uint32_t)(a.Hq * D * 2) + at : 0x80000000u, 0, 0);
+            q[j] = __builtin_amdgcn_raw_buffer_load_b128(rq, (tok * (uint32_t)(a.ldq * 2) + at) | past, 0, 0);
+            g[j] = __builtin_amdgcn_raw_buffer_load_b128(rg, (tok * (uint32_t)(a.Hq * D * 2) + at) | past, 0, 0);
         }
-        ls = 0.f, dl = 0.f;
-        if (tid < RT && r0 + tid < rows) {
-            const int64_t gr = packed_row(a, z, hk, r0 + tid);
-            ls = a.lse[gr] * kLog2e;
-            if (ls == -INFINITY) ls = INFINITY;                // a row that saw nothing: p = 0
-            dl = a.delta[gr];
-        }
+        // nothing is computed from the loads here: that would wait for them all
+        const rsrc_t rl = make_rsrc(a.lse + (z.q0 + i0) * a.Hq + hk * a.G, 0x7ffffff0u);
+        const rsrc_t rd = make_rsrc(a.delta + (z.q0 + i0) * a.Hq + hk * a.G, 0x7ffffff0u);
+        const uint32_t x = (uint32_t)(g0 + (tid & (RT - 1)));
+        const uint32_t tok = a.G == 1 ? x : __umulhi(x, inv);
+        const uint32_t past = r0 + (tid & (RT - 1)) < rows ? 0u : 0x80000000u;
+        const uint32_t at = (tok * (uint32_t)a.Hq + (x - tok * a.G)) * 4 | past;
+        ls = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rl, at, 0, 0));
+        dl = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rd, at, 0, 0));
     }
     __device__ __forceinline__ void store(unsigned char* qt, unsigned char* gt, float* lt, float* dt, int tid) const {
 #pragma unroll
@@ -440,7 +442,7 @@ struct RowStage {
             *reinterpret_cast<u32x4*>(gt + chunk_at<D>(rr, c)) = g[j];
         }
         if (tid < RT) {
-            lt[tid] = ls;
+            lt[tid] = ls == -INFINITY ? INFINITY : ls * kLog2e;   // a row that saw nothing: p = 0
             dt[tid] = dl;
         }
     }
