@@ -399,40 +399,53 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_dq_kernel(const AttnArgs a) {
 }
 
 // Staging of RT packed query rows: q, d_o, and each row's logarithm and
-// <d_o, o>.  A row's token is found from the tile's first by a multiplication
-// (place within the tile times 2^32 / G, exact for G <= 2^15).
+// <d_o, o>.  A row's token, counted from the tile's first, comes from a
+// multiplication (place within the tile times 2^32 / G, exact for G <= 2^15);
+// tiles that start at the same head share the addresses, which is all of them
+// where G divides RT.  Rows past the last lie past the descriptors' ends and
+// read as zeros.
 template <int D, int NT, int RT>
 struct RowStage {
     static constexpr int N = RT * D / 8 / NT;
     static_assert(N >= 1 && RT <= NT, "every thread stages something");
     u32x4 q[N], g[N];
     float ls, dl;
-    __device__ __forceinline__ void load(const AttnArgs& a, const Seq& z, int hk, int r0, int rows, uint32_t inv,
-                                         int tid) {
+    uint32_t at_q[N], at_g[N], at_l;
+    int first = -1;                                       // head of the tile's first row
+    __device__ __forceinline__ void load(const AttnArgs& a, const Seq& z, int hk, int r0, uint32_t inv, int tid) {
         const int i0 = r0 / a.G, g0 = r0 - i0 * a.G;
-        const rsrc_t rq = make_rsrc(static_cast<const uint16_t*>(a.q) + (z.q0 + i0) * a.ldq + (int64_t)hk * a.G * D,
-                                    0x7ffffff0u);
-        const rsrc_t rg = make_rsrc(static_cast<const uint16_t*>(a.d_o) +
-                                        ((z.q0 + i0) * a.Hq + (int64_t)hk * a.G) * D, 0x7ffffff0u);
+        if (g0 != first) {
+            first = g0;
+            auto token = [&](int rr, uint32_t& gg) {
+                const uint32_t x = (uint32_t)(g0 + rr), tok = a.G == 1 ? x : __umulhi(x, inv);
+                gg = x - tok * a.G;
+                return tok;
+            };
+            uint32_t gg;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const int i = tid + j * NT, c = i % (D / 8);
+                const uint32_t tok = token(i / (D / 8), gg);
+                at_q[j] = tok * (uint32_t)(a.ldq * 2) + gg * (2 * D) + c * 16;
+                at_g[j] = tok * (uint32_t)(a.Hq * D * 2) + gg * (2 * D) + c * 16;
+            }
+            const uint32_t tok = token(tid & (RT - 1), gg);
+            at_l = (tok * (uint32_t)a.Hq + gg) * 4;
+        }
+        // the last token's heads end each range
+        auto range = [&](const void* p, int64_t tok_bytes, int64_t head_bytes) {
+            return make_rsrc(static_cast<const unsigned char*>(p) + (z.q0 + i0) * tok_bytes + hk * a.G * head_bytes,
+                             (uint32_t)min((z.lq - i0 - 1) * tok_bytes + a.G * head_bytes, (int64_t)0x7ffffff0));
+        };
+        const rsrc_t rq = range(a.q, a.ldq * 2, 2 * D), rg = range(a.d_o, (int64_t)a.Hq * D * 2, 2 * D);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const int i = tid + j * NT, rr = i / (D / 8), c = i % (D / 8);
-            const uint32_t x = (uint32_t)(g0 + rr);
-            const uint32_t tok = a.G == 1 ? x : __umulhi(x, inv), gg = x - tok * a.G;
-            const uint32_t past = r0 + rr < rows ? 0u : 0x80000000u;   // rows past the last read as zeros
-            const uint32_t at = gg * (2 * D) + c * 16;
-            q[j] = __builtin_amdgcn_raw_buffer_load_b128(rq, (tok * (uint32_t)(a.ldq * 2) + at) | past, 0, 0);
-            g[j] = __builtin_amdgcn_raw_buffer_load_b128(rg, (tok * (uint32_t)(a.Hq * D * 2) + at) | past, 0, 0);
+            q[j] = __builtin_amdgcn_raw_buffer_load_b128(rq, at_q[j], 0, 0);
+            g[j] = __builtin_amdgcn_raw_buffer_load_b128(rg, at_g[j], 0, 0);
         }
         // nothing is computed from the loads here: that would wait for them all
-        const rsrc_t rl = make_rsrc(a.lse + (z.q0 + i0) * a.Hq + hk * a.G, 0x7ffffff0u);
-        const rsrc_t rd = make_rsrc(a.delta + (z.q0 + i0) * a.Hq + hk * a.G, 0x7ffffff0u);
-        const uint32_t x = (uint32_t)(g0 + (tid & (RT - 1)));
-        const uint32_t tok = a.G == 1 ? x : __umulhi(x, inv);
-        const uint32_t past = r0 + (tid & (RT - 1)) < rows ? 0u : 0x80000000u;
-        const uint32_t at = (tok * (uint32_t)a.Hq + (x - tok * a.G)) * 4 | past;
-        ls = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rl, at, 0, 0));
-        dl = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rd, at, 0, 0));
+        ls = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(range(a.lse, (int64_t)a.Hq * 4, 4), at_l, 0, 0));
+        dl = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(range(a.delta, (int64_t)a.Hq * 4, 4), at_l, 0, 0));
     }
     __device__ __forceinline__ void store(unsigned char* qt, unsigned char* gt, float* lt, float* dt, int tid) const {
 #pragma unroll
@@ -508,14 +521,14 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_kernel(const AttnArgs a) 
         start += lo;
     }
     if (start < end) {
-        st.load(a, z, p.hk, start, rows, inv, tid);
+        st.load(a, z, p.hk, start, inv, tid);
         st.store(qt[0], gt[0], lt[0], dt[0], tid);
     }
     __syncthreads();
     int buf = 0;
     for (int r0 = start; r0 < end; r0 += RT, buf ^= 1) {
         const bool more = r0 + RT < end;
-        if (more) st.load(a, z, p.hk, r0 + RT, rows, inv, tid);
+        if (more) st.load(a, z, p.hk, r0 + RT, inv, tid);
         if (r0 + RT > w_first) {
             const bool mask = r0 < w_all;
 #pragma unroll
