@@ -124,6 +124,9 @@ CASES = [
     ([300], [300], 8, 1, 32, True, 7),
     ([200, 3, 129], [77, 700, 128], 4, 4, 128, False, 1),
     ([513], [513], 2, 1, 16, True, 1),
+    ([700], [900], 4, 1, 128, True, 1),                 # many rows to a key head: rows split in the dk/dv kernel
+    ([1100, 30], [1100, 30], 2, 1, 64, False, 1),
+    ([290], [290], 3, 1, 64, True, 1),                  # heads that do not divide a row tile
 ]
 
 
@@ -140,6 +143,41 @@ def test_packed_forward_and_backward(case, dtype):
     torch.cuda.synchronize()
     compare(q, k, v, do, cu_q, cu_k, lens_q, lens_k, causal, block, D ** -0.5, (o, lse, *grads),
             ("o", "lse", "dq", "dk", "dv"))
+
+
+@pytest.mark.parametrize("n", [64, 65, 150])
+def test_many_sequences(n):
+    """More sequences than a wave has lanes, of several tiles or none."""
+    r = np.random.default_rng(n)
+    lens = [int(x) for x in r.choice([0, 1, 20, 64, 129, 300], n)]
+    cu = starts(lens)
+    q, k, v, do = inputs(cu, cu, 4, 2, 32, BF, seed=n)
+    c = torch.from_numpy(cu).cuda()
+    kw = dict(causal=True, cu_q=c, cu_k=c, max_q=300, max_k=300)
+    o, lse = api.attention_fwd(q, k, v, **kw)
+    grads = api.attention_bwd(q, k, v, o, lse, do, **kw)
+    torch.cuda.synchronize()
+    compare(q, k, v, do, cu, cu, lens, lens, True, 1, 32 ** -0.5, (o, lse, *grads), ("o", "lse", "dq", "dk", "dv"))
+
+
+def test_two_streams_at_once():
+    """Calls that overlap on two streams, each with a workspace of its own."""
+    sets = [inputs([0, 600], [0, 600], 4, 1, 128, BF, seed=s) for s in (20, 21)]
+    ref = []
+    for q, k, v, do in sets:
+        o, lse = api.attention_fwd(q[None], k[None], v[None], causal=True)
+        ref.append((o, lse, *api.attention_bwd(q[None], k[None], v[None], o, lse, do[None], causal=True)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [None, None]
+    for _ in range(3):
+        for i, ((q, k, v, do), s) in enumerate(zip(sets, streams)):
+            o, lse = api.attention_fwd(q[None], k[None], v[None], causal=True, stream=s)
+            got[i] = (o, lse, *api.attention_bwd(q[None], k[None], v[None], o, lse, do[None], causal=True, stream=s))
+        torch.cuda.synchronize()
+        for a, b in zip(got, ref):
+            for x, y in zip(a, b):
+                assert torch.equal(x, y)
 
 
 def test_dense_form_is_the_oracle():
