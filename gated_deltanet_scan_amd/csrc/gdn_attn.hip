@@ -212,12 +212,15 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(const AttnArgs a) {
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] *= al;
         const int n = min(64, splits - s0);
+        // every lane takes part in every exchange: a lane that had left the loop
+        // early would no longer hand out its split's weight
 #pragma unroll 4
-        for (int i = g; i < n; i += 4) {
-            const float wi = __shfl(w, i);
+        for (int i0 = 0; i0 < n; i0 += 4) {
+            const float wi = __shfl(w, i0 + g);           // 0 past the last split
+            const int64_t row = (s0 + min(i0 + g, n - 1)) * all + gr;
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                if (64 * e + c < D) acc[e] += wi * load4(a.part_o + ((s0 + i) * all + gr) * D + 64 * e + c);
+                if (64 * e + c < D) acc[e] += wi * load4(a.part_o + row * D + 64 * e + c);
         }
     }
     const float inv = l > 0.f ? 1.0f / l : l;

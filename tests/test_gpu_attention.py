@@ -214,6 +214,24 @@ def test_cache_filled_in_part(lq, G, D, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("D", [16, 32, 128])
+def test_every_number_of_splits(D, dtype):
+    """A single query against caches that take 1 to 70 splits, all remainders of
+    the join's four-way sums and both sides of its 64-lane batches among them."""
+    unit = 512 if dtype == BF and D > 16 else 128
+    counts = [1, 2, 3, 4, 5, 15, 16, 17, 18, 19, 21, 34, 47, 58, 61, 62, 63, 64, 65, 66, 70]
+    lens_k = [c * unit - (7 * c) % unit for c in counts]
+    n, room = len(counts), 70 * unit
+    cu_q, cu_k = starts([1] * n), (np.arange(n + 1) * room).astype(np.int32)
+    q, k, v, _ = inputs(cu_q, cu_k, 2, 1, D, dtype, seed=D)
+    kl = torch.tensor(lens_k, dtype=torch.int32, device="cuda")
+    o, lse = api.attention_fwd(q[:, None], k.reshape(n, room, 1, D), v.reshape(n, room, 1, D), causal=True, k_len=kl)
+    torch.cuda.synchronize()
+    compare(q, k, v, torch.zeros_like(q), cu_q, cu_k, [1] * n, lens_k, True, 1, D ** -0.5,
+            (o.reshape(q.shape), lse.reshape(-1, 2)), ("o", "lse"))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
 def test_frames_are_frame_causal(dtype):
     """[B, F, N, H, D]: causal means whole frames by default; every frame of a
     clip equals one streamed call of that frame against the frames so far."""
