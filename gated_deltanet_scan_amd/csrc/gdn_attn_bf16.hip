@@ -12,6 +12,7 @@
 #include "gdn_attn.hpp"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace gdnattn {
 namespace {
@@ -293,6 +294,13 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_fwd_kernel(const AttnArgs a) 
 
 // dq, and <d_o, o> for the dk/dv kernel.  Query rows as columns, as in the
 // forward kernel; the key tile is read both ways (S^T = K Q^T, dQ^T += K^T dS^T).
+//
+// <d_o, o> = sum_j p_j dp_j.  From the rounded o it is off by 2^-9 |d_o| |o|,
+// which matters where a row sees few keys and o is as large as v (a causal
+// sequence of 300 tokens: dq off by 2.40e-3 with it and 2.26e-3 without, of
+// which 1.68e-3 are dq's own rounding).  Where the workgroup's rows see at most
+// kExactKeys keys the sum is formed in fp32 by a first walk over them.
+constexpr int kExactKeys = 256;
 template <int D, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void attn_dq_kernel(const AttnArgs a) {
     constexpr int NT = 64 * NW, BM = 32 * NW, KS = D / 16, DB = D / 32, TB = kKeys * D * 2;
@@ -329,66 +337,78 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_dq_kernel(const AttnArgs a) {
         }
     }
     delta = half_sum(delta);
-    if (valid && h == 0) a.delta[gr] = delta;
     float ls = valid ? a.lse[gr] * kLog2e : INFINITY;
     if (ls == -INFINITY) ls = INFINITY;                       // a row that saw nothing: p = 0
     f32x16 acc[DB];
-#pragma unroll
-    for (int e = 0; e < DB; ++e) acc[e] = zero16();
     const uint16_t* kb = static_cast<const uint16_t*>(a.k) + z.k0 * a.ldk + (int64_t)p.hk * D;
     const uint16_t* vb = static_cast<const uint16_t*>(a.v) + z.k0 * a.ldv + (int64_t)p.hk * D;
     const float c2 = a.scale * kLog2e;
     Addr<D> ad;
     ad.init(lane);
     Tile<D, NT> sk, sv;
-    if (upto > 0) {
-        sk.load(kb, a.ldk, 0, upto, tid);
-        sv.load(vb, a.ldv, 0, upto, tid);
-        sk.store(kt[0], tid);
-        sv.store(vt[0], tid);
-    }
-    __syncthreads();
-    int buf = 0;
-    for (int n0 = 0; n0 < upto; n0 += kKeys, buf ^= 1) {
-        const bool more = n0 + kKeys < upto;
-        if (more) {
-            sk.load(kb, a.ldk, n0 + kKeys, upto, tid);
-            sv.load(vb, a.ldv, n0 + kKeys, upto, tid);
-        }
-        if (n0 < n_last) {
-            const bool mask = n0 + kKeys > n_first;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                f32x16 s = zero16(), dp = zero16();
-                ad.renew();
-#pragma unroll
-                for (int e = 0; e < KS; ++e) s = mma(ad.rows(kt[buf], t, e), q[e], s);
-#pragma unroll
-                for (int e = 0; e < KS; ++e) dp = mma(ad.rows(vt[buf], t, e), g[e], dp);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) s[i] = exp2_f(__builtin_fmaf(s[i], c2, -ls));
-#pragma unroll
-                for (int i = 0; i < 16; ++i) s[i] *= dp[i] - delta;
-                if (mask) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (n0 + 32 * t + 8 * (i >> 2) + 4 * h + (i & 3) >= n) s[i] = 0.f;
-                }
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const u32x4 ds = pack8(s, 8 * u);
-#pragma unroll
-                    for (int e = 0; e < DB; ++e) acc[e] = mma(ad.cols(kt[buf], e, 2 * t + u), ds, acc[e]);
-                }
-            }
-        }
-        if (more) {
-            sk.store(kt[buf ^ 1], tid);
-            sv.store(vt[buf ^ 1], tid);
+    auto walk = [&](auto first) {
+        constexpr bool kFirst = decltype(first)::value;
+        float exact = 0.f;
+        if (upto > 0) {
+            sk.load(kb, a.ldk, 0, upto, tid);
+            sv.load(vb, a.ldv, 0, upto, tid);
+            sk.store(kt[0], tid);
+            sv.store(vt[0], tid);
         }
         __syncthreads();
-    }
+        int buf = 0;
+        for (int n0 = 0; n0 < upto; n0 += kKeys, buf ^= 1) {
+            const bool more = n0 + kKeys < upto;
+            if (more) {
+                sk.load(kb, a.ldk, n0 + kKeys, upto, tid);
+                sv.load(vb, a.ldv, n0 + kKeys, upto, tid);
+            }
+            if (n0 < n_last) {
+                const bool mask = n0 + kKeys > n_first;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    f32x16 s = zero16(), dp = zero16();
+                    ad.renew();
+#pragma unroll
+                    for (int e = 0; e < KS; ++e) s = mma(ad.rows(kt[buf], t, e), q[e], s);
+#pragma unroll
+                    for (int e = 0; e < KS; ++e) dp = mma(ad.rows(vt[buf], t, e), g[e], dp);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) s[i] = exp2_f(__builtin_fmaf(s[i], c2, -ls));
+                    if (mask) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (n0 + 32 * t + 8 * (i >> 2) + 4 * h + (i & 3) >= n) s[i] = 0.f;
+                    }
+                    if constexpr (kFirst) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) exact += s[i] * dp[i];
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) s[i] *= dp[i] - delta;
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const u32x4 ds = pack8(s, 8 * u);
+#pragma unroll
+                            for (int e = 0; e < DB; ++e) acc[e] = mma(ad.cols(kt[buf], e, 2 * t + u), ds, acc[e]);
+                        }
+                    }
+                }
+            }
+            if (more) {
+                sk.store(kt[buf ^ 1], tid);
+                sv.store(vt[buf ^ 1], tid);
+            }
+            __syncthreads();
+        }
+        if constexpr (kFirst) delta = half_sum(exact);
+    };
+    if (upto <= kExactKeys) walk(std::true_type());
+#pragma unroll
+    for (int e = 0; e < DB; ++e) acc[e] = zero16();
+    walk(std::false_type());
     if (!valid) return;
+    if (h == 0) a.delta[gr] = delta;
 #pragma unroll
     for (int e = 0; e < DB; ++e)
 #pragma unroll
