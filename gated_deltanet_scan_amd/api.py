@@ -697,13 +697,9 @@ def rotary(q, k, pos, *, axes, theta: float = 10000.0, halves: bool = False, inv
     return q_out, k_out
 
 
-def _token_strides(t, name, dtype):
+def _token_strides(t, name):
     """(token stride, tokens between sequences or 0 for packed) of t [..., H, D]:
     heads packed, a sequence's tokens evenly apart."""
-    if t.device.type != "cuda":
-        raise ValueError("%s must be a device tensor (got %s)" % (name, t.device))
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s (got %s)" % (name, dtype, t.dtype))
     H, D = t.shape[-2:]
     if t.is_contiguous() or t.numel() == 0:
         return H * D, 0
@@ -734,46 +730,60 @@ def _attn_args(q, k, v, causal, causal_block, scale, cu_q, cu_k, max_q, max_k):
     for name, t in (("q", q), ("k", k), ("v", v)):
         if not isinstance(t, torch.Tensor):
             raise TypeError("%s must be a torch.Tensor" % name)
-    if q.dim() not in (3, 4, 5) or k.dim() != q.dim() or v.shape != k.shape:
+    sq, sk = q.shape, k.shape
+    dims = len(sq)
+    if not 3 <= dims <= 5 or len(sk) != dims or v.shape != sk:
         raise ValueError("q, k and v must be [T, H, D], [B, L, H, D] or [B, F, N, H, D], k and v alike (got %s, %s, %s)"
-                         % (tuple(q.shape), tuple(k.shape), tuple(v.shape)))
-    Hq, D = q.shape[-2:]
-    Hk = k.shape[-2]
-    if k.shape[-1] != D:
+                         % (tuple(sq), tuple(sk), tuple(v.shape)))
+    Hq, D = sq[-2:]
+    Hk = sk[-2]
+    if sk[-1] != D:
         raise ValueError("q and k must have the same head size")
-    tq, tk = q.shape[:-2].numel(), k.shape[:-2].numel()
-    _io(q.dtype, "q, k and v")
-    (ldq, rq), (ldk, rk), (ldv, rv) = [_token_strides(t, n, q.dtype)
-                                       for t, n in ((q, "q"), (k, "k"), (v, "v"))]
-    if rq:
-        raise ValueError("q must have packed heads and evenly spaced tokens")
-    if rk != rv:
-        raise ValueError("the sequences of k and v must lie equally far apart")
-    if causal_block is None:
-        causal_block = q.shape[2] if q.dim() == 5 else 1
-    if q.dim() == 3:
+    io = _io(q.dtype, "q, k and v")
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if not t.is_cuda:
+            raise ValueError("%s must be a device tensor (got %s)" % (name, t.device))
+        if t.dtype != q.dtype:
+            raise TypeError("%s must be %s (got %s)" % (name, q.dtype, t.dtype))
+    if q.is_contiguous() and k.is_contiguous() and v.is_contiguous():
+        ldq = ldk = ldv = rk = 0
+    else:
+        (ldq, rq), (ldk, rk), (ldv, rv) = [_token_strides(t, n) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
+        if rq:
+            raise ValueError("q must have packed heads and evenly spaced tokens")
+        if rk != rv:
+            raise ValueError("the sequences of k and v must lie equally far apart")
+    if dims == 3:
         if cu_q is None:
             raise ValueError("packed q [T, H, D] needs cu_q")
+        tq, tk = sq[0], sk[0]
         cu_k = cu_q if cu_k is None else cu_k
         n_seq = cu_q.numel() - 1
-        for name, t in (("cu_q", cu_q), ("cu_k", cu_k)):
-            _check(t, name, torch.int32, (n_seq + 1,))
         if n_seq < 0:
             raise ValueError("cu_q must hold n_seq + 1 offsets")
+        _check(cu_q, "cu_q", torch.int32, (n_seq + 1,))
+        _check(cu_k, "cu_k", torch.int32, (n_seq + 1,))
         max_q = tq if max_q is None else int(max_q)
         max_k = tk if max_k is None else int(max_k)
     else:
         if cu_q is not None or cu_k is not None or max_q is not None or max_k is not None:
             raise ValueError("cu_q, cu_k, max_q and max_k belong to packed q [T, H, D]")
-        n_seq = q.shape[0]
-        if k.shape[0] != n_seq:
+        n_seq = sq[0]
+        if sk[0] != n_seq:
             raise ValueError("q and k must have the same batch size")
-        max_q, max_k = (tq // n_seq, tk // n_seq) if n_seq else (0, 0)
+        max_q, max_k = sq[1:-2].numel(), sk[1:-2].numel()
+        tq, tk = n_seq * max_q, n_seq * max_k
+    if causal_block is None:
+        causal_block = sq[2] if dims == 5 else 1
     _same_device(q, k=k, v=v, cu_q=cu_q, cu_k=cu_k)
-    desc = _lib.GdnAttnDesc(tq, tk, ldq, ldk, ldv, rk, n_seq, Hq, Hk, D, max_q, max_k, int(causal_block),
-                            _io(q.dtype, "q"), _lib.GDN_FLAG_ATTN_CAUSAL if causal else 0,
-                            float(D ** -0.5 if scale is None else scale))
+    desc = _lib.GdnAttnDesc(tq, tk, ldq, ldk, ldv, rk, n_seq, Hq, Hk, D, max_q, max_k, int(causal_block), io,
+                            _lib.GDN_FLAG_ATTN_CAUSAL if causal else 0, D ** -0.5 if scale is None else scale)
     return desc, cu_q, cu_k
+
+
+def _like(t):
+    """An uninitialised contiguous tensor like t."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def attention_fwd(q, k, v, *, causal: bool = False, causal_block: Optional[int] = None, scale=None, cu_q=None,
@@ -806,9 +816,9 @@ def attention_fwd(q, k, v, *, causal: bool = False, causal_block: Optional[int] 
     where, handle = _launch(stream, q.device)
     with where:   # allocations belong to the launch stream
         if o is None:
-            o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            o = _like(q)
         if lse is None and return_lse:
-            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+            lse = q.new_empty(q.shape[:-1], dtype=torch.float32)
         workspace = _workspace(workspace, int(lib.gdn_attn_workspace_size(ctypes.byref(desc))), q.device)
         st = lib.gdn_attn_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k), _ptr(k_len),
                               _ptr(o), _ptr(lse), _ptr(workspace), _ws_bytes(workspace),
@@ -836,8 +846,9 @@ def attention_bwd(q, k, v, o, lse, dO, *, causal: bool = False, causal_block: Op
     lib = _lib.load()
     where, handle = _launch(stream, q.device)
     with where:   # allocations belong to the launch stream
-        dq, dk, dv = [t if t is not None else torch.empty(like.shape, dtype=like.dtype, device=like.device)
-                      for t, like in ((dq, q), (dk, k), (dv, v))]
+        dq = _like(q) if dq is None else dq
+        dk = _like(k) if dk is None else dk
+        dv = _like(v) if dv is None else dv
         workspace = _workspace(workspace, int(lib.gdn_attn_workspace_size_bwd(ctypes.byref(desc))), q.device)
         st = lib.gdn_attn_bwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dO), _ptr(cu_q),
                               _ptr(cu_k), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), _ws_bytes(workspace),
