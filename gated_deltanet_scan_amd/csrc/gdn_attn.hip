@@ -481,7 +481,8 @@ int fwd_rows(const gdn_attn_desc* d) {
 // against its keys, of which it takes 512 at least (128 at the fp32 rate).
 int fwd_chunk(const gdn_attn_desc* d) {
     const int64_t rows = (int64_t)d->max_q * (d->Hq / d->Hk);
-    const int64_t units = (int64_t)d->n_seq * d->Hk * std::max<int64_t>(1, (rows + fwd_rows(d) - 1) / fwd_rows(d));
+    int tiles;
+    const int64_t units = places(d->total_q * (d->Hq / d->Hk), rows, d->n_seq, fwd_rows(d), true, &tiles) * d->Hk;
     int64_t n = (fwd_rows(d) == 256 ? 256 : 512) / std::max<int64_t>(units, 1);
     if (rows <= 32) n *= 8;
     if (n < 2) return std::max(d->max_k, 1);
@@ -504,7 +505,10 @@ int fwd_splits(const gdn_attn_desc* d) {
 int bwd_splits(const gdn_attn_desc* d) {
     int tiles;
     const int64_t items = places(d->total_k, d->max_k, d->n_seq, fast(d) ? 128 : kRows, true, &tiles) * d->Hk;
-    const int64_t most = (int64_t)d->max_q * (d->Hq / d->Hk) / (fast(d) ? 1024 : 128);
+    const int64_t rows = (int64_t)d->max_q * (d->Hq / d->Hk);
+    // what 32 MiB of sums allow stays in the caches
+    const int64_t near = ((int64_t)32 << 20) / std::max<int64_t>(1, d->total_k * d->Hk * d->D * 8);
+    const int64_t most = std::max(rows / (fast(d) ? 1024 : 128), std::min(rows / (fast(d) ? 256 : 64), near));
     if (items < 1 || items >= 512 || most < 2) return 1;
     return (int)std::min<int64_t>(std::min<int64_t>((1024 + items - 1) / items, most), 64);
 }

@@ -8,7 +8,7 @@
 // backward reads x and dy and writes dx.  A row stays in registers between its
 // statistics and its result, so nothing is read twice; the variance is a second
 // sum over the registers, about the mean (no cancellation of <x^2> - mu^2).
-// One wave holds a row of up to 4096 elements, so rows of the usual widths need
+// One wave holds a row of up to 2048 elements, so rows of the usual widths need
 // no barrier at all; four waves share a row of up to 16384, and wider rows are
 // read again from memory (norm_wide_*).
 #include "gdn_ops.hpp"
@@ -389,10 +389,11 @@ gdn_status check_norm(const gdn_norm_desc* d) {
 }
 int elem(int dt) { return dt == GDN_BF16 ? 2 : 4; }
 
-// Waves a row and chunks a lane: the smallest that hold the row.
+// Waves a row and chunks a lane: the smallest that hold the row.  (Eight chunks
+// a lane in one wave leave a SIMD a single wave: XXX.)
 bool shape_of(int C, int* nv, int* wpr) {
     for (int w = 1; w <= 4; w *= 4)
-        for (int v = 1; v <= 8; v *= 2)
+        for (int v = 1; v <= (w == 1 ? 4 : 8); v *= 2)
             if (C <= 512 * v * w) {
                 *nv = v;
                 *wpr = w;
@@ -429,8 +430,8 @@ gdn_status launch_fwd(const NormArgs& a, int cus, hipStream_t s) {
         if (nv == 1) GDN_NORM(1, 1);
         if (nv == 2) GDN_NORM(2, 1);
         if (nv == 4) GDN_NORM(4, 1);
-        if (nv == 8) GDN_NORM(8, 1);
     } else {
+        if (nv == 2) GDN_NORM(2, 4);
         if (nv == 4) GDN_NORM(4, 4);
         if (nv == 8) GDN_NORM(8, 4);
     }
@@ -455,8 +456,8 @@ gdn_status launch_bwd(const NormArgs& a, int groups, void* dw, void* db, int cus
                 if (nv == 1) GDN_NORM(1, 1);
                 if (nv == 2) GDN_NORM(2, 1);
                 if (nv == 4) GDN_NORM(4, 1);
-                if (nv == 8) GDN_NORM(8, 1);
             } else {
+                if (nv == 2) GDN_NORM(2, 4);
                 if (nv == 4) GDN_NORM(4, 4);
                 if (nv == 8) GDN_NORM(8, 4);
             }
