@@ -38,13 +38,6 @@ template <typename T> struct Vec8;
 template <> struct Vec8<uint16_t> {
     u32x4 v;
     __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const u32x4_a2*>(p); }
-    __device__ __forceinline__ void load_tail(const uint16_t* p, int n) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t lo = 2 * i < n ? p[2 * i] : 0, hi = 2 * i + 1 < n ? p[2 * i + 1] : 0;
-            v[i] = lo | hi << 16;
-        }
-    }
     __device__ __forceinline__ void zero() { v = u32x4{0u, 0u, 0u, 0u}; }
     __device__ __forceinline__ float get(int i) const {
         const uint32_t w = v[i >> 1];
@@ -55,24 +48,12 @@ template <> struct Vec8<uint16_t> {
         for (int i = 0; i < 4; ++i) v[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
     }
     __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<u32x4_a2*>(p) = v; }
-    __device__ __forceinline__ void store_tail(uint16_t* p, int n) const {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) p[i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
-    }
 };
 template <> struct Vec8<float> {
     f32x4 a, b;
     __device__ __forceinline__ void load(const float* p) {
         a = *reinterpret_cast<const f32x4_a4*>(p);
         b = *reinterpret_cast<const f32x4_a4*>(p + 4);
-    }
-    __device__ __forceinline__ void load_tail(const float* p, int n) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            a[i] = i < n ? p[i] : 0.f;
-            b[i] = i + 4 < n ? p[i + 4] : 0.f;
-        }
     }
     __device__ __forceinline__ void zero() { a = b = f32x4{0.f, 0.f, 0.f, 0.f}; }
     __device__ __forceinline__ float get(int i) const { return i < 4 ? a[i & 3] : b[i & 3]; }
@@ -86,11 +67,6 @@ template <> struct Vec8<float> {
     __device__ __forceinline__ void store(float* p) const {
         *reinterpret_cast<f32x4_a4*>(p) = a;
         *reinterpret_cast<f32x4_a4*>(p + 4) = b;
-    }
-    __device__ __forceinline__ void store_tail(float* p, int n) const {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) p[i] = get(i);
     }
 };
 
