@@ -32,6 +32,7 @@ struct AttnArgs {
     int tiles;                           // row (or key) tiles of the longest sequence
     int splits, k_splits;                // of the key axis (forward), of the row axis (dk, dv)
     int chunk;                           // keys of a split (the longest sequence's fill them all)
+    int join_rows;                       // rows of a workgroup of the join
     int causal, block;
     float scale;
 };
