@@ -149,7 +149,8 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(const NormArgs a) {
         row_sum2<WPR>(q, e, red2, phase2);
         e /= (float)C;
         mu += e;
-        const float r = 1.0f / sqrtf(fmaxf(q * a.inv_c - e * e, 0.f) + a.eps);
+        const float var = q * a.inv_c - e * e;
+        const float r = 1.0f / sqrtf((var < 0.f ? 0.f : var) + a.eps);   // a NaN stays one
         T* yr = static_cast<T*>(a.y) + row * C;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -297,7 +298,8 @@ __global__ __launch_bounds__(kThreads) void norm_wide_fwd_kernel(const NormArgs 
         row_sum2<4>(q, e, red2, phase2);
         e /= (float)a.C;
         mu += e;
-        const float r = 1.0f / sqrtf(fmaxf(q * a.inv_c - e * e, 0.f) + a.eps);
+        const float var = q * a.inv_c - e * e;
+        const float r = 1.0f / sqrtf((var < 0.f ? 0.f : var) + a.eps);
         for (int c = threadIdx.x; c < a.C; c += kThreads) {
             const float h = (to_f<T>(x[c]) - mu) * r;
             const float w = a.w ? to_f<W>(static_cast<const W*>(a.w)[c]) : 1.f;

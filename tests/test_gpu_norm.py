@@ -197,3 +197,13 @@ def test_gradient_against_differences():
             v.append((ops.layer_norm(*a)[0] * host(dy)).sum())
         num, ana = (v[0] - v[1]) / 2e-4, (g * d).sum()
         assert abs(num - ana) <= 1e-5 * np.linalg.norm(g) * np.linalg.norm(d)
+
+
+def test_statistics_of_a_bad_row():
+    """The saved statistics say so too: a NaN is no rstd of 1 / sqrt(eps)."""
+    for C in (100, 20000):
+        x = torch.randn(3, C, device="cuda")
+        x[1, 5] = float("nan")
+        _, mean, rstd = api.layer_norm_fwd(x)
+        torch.cuda.synchronize()
+        assert torch.isfinite(rstd[[0, 2]]).all() and rstd[1].isnan() and mean[1].isnan()
