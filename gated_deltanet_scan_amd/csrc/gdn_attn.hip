@@ -92,6 +92,19 @@ struct Stage {
     }
 };
 
+// The lane's features of one row times its own, and the sum over the column.
+template <typename T, int D>
+__device__ __forceinline__ float dot_row(const f32x4 (&f)[D / 16], const T* row, int g) {
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < D / 16; ++e) {
+        const f32x4 x = load4(row + 16 * e + 4 * g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s += x[j] * f[e][j];
+    }
+    return col_sum(s);
+}
+
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void attn_fwd_f32_kernel(const AttnArgs a) {
     __shared__ float kt[kTile][D + 4], vt[kTile][D + 4];
@@ -163,6 +176,25 @@ __global__ __launch_bounds__(kThreads) void attn_fwd_f32_kernel(const AttnArgs a
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int e = 0; e < D / 16; ++e) acc[e] = mma(vt[16 * t + 4 * g + i][16 * e + c], s[t][i], acc[e]);
+    }
+    if (a.causal && !finite(acc)) {                           // see finite()
+        m = -INFINITY;
+        l = 0.f;
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e) acc[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int j = lo; j < hi; ++j) {
+            const float s = dot_row<T, D>(q, kb + (int64_t)j * a.ldk, g) * c2;
+            if (j < n) {
+                const float mn = fmaxf(m, s), ms = mn == -INFINITY ? 0.f : mn;
+                const float al = exp2_f(m - ms), pj = exp2_f(s - ms);
+                m = mn;
+                l = l * al + (g == 0 ? pj : 0.f);
+#pragma unroll
+                for (int e = 0; e < D / 16; ++e)
+                    acc[e] = acc[e] * al + pj * load4(vb + (int64_t)j * a.ldv + 16 * e + 4 * g);
+            }
+        }
     }
     l = col_sum(l);
     if (!valid) return;
@@ -307,6 +339,20 @@ __global__ __launch_bounds__(kThreads) void attn_dq_f32_kernel(const AttnArgs a)
             }
         }
     }
+    if (a.causal && !finite(acc)) {                           // see finite()
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e) acc[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int j = 0; j < upto; ++j) {
+            const T* kr = kb + (int64_t)j * a.ldk;
+            const float s = dot_row<T, D>(q, kr, g), dp = dot_row<T, D>(dout, vb + (int64_t)j * a.ldv, g);
+            if (j < nn) {
+                const float ds = exp2_f(__builtin_fmaf(s, c2, -ls)) * (dp - delta);
+#pragma unroll
+                for (int e = 0; e < D / 16; ++e) acc[e] += ds * load4(kr + 16 * e + 4 * g);
+            }
+        }
+    }
     if (!valid) return;
 #pragma unroll
     for (int e = 0; e < D / 16; ++e) store4(static_cast<T*>(a.dq) + gr * D + 16 * e + 4 * g, acc[e] * a.scale);
@@ -407,6 +453,24 @@ __global__ __launch_bounds__(kThreads) void attn_dkv_f32_kernel(const AttnArgs a
             }
         }
     }
+    if (a.causal && (!finite(ak) || !finite(av))) {           // see finite()
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e) ak[e] = av[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int r = start; r < end; ++r) {
+            const int64_t gr = packed_row(a, z, p.hk, r);
+            const T *qr = q_row<T>(a, z, p.hk, r), *dr = static_cast<const T*>(a.d_o) + gr * D;
+            const float s = dot_row<T, D>(kf, qr, g), dp = dot_row<T, D>(vf, dr, g), lr = a.lse[gr];
+            if (lr != -INFINITY && valid && key < visible(a, z, r / a.G)) {
+                const float pr = exp2_f(__builtin_fmaf(s, c2, -lr * kLog2e)), ds = pr * (dp - a.delta[gr]);
+#pragma unroll
+                for (int e = 0; e < D / 16; ++e) {
+                    av[e] += pr * load4(dr + 16 * e + 4 * g);
+                    ak[e] += ds * load4(qr + 16 * e + 4 * g);
+                }
+            }
+        }
+    }
     if (!valid) return;
     if (a.k_splits > 1) {
         const int64_t at = (((int64_t)p.split * a.total_k + z.ko + key) * a.Hk + p.hk) * D;
@@ -455,7 +519,8 @@ gdn_status check_attn(const gdn_attn_desc* d) {
     if (d->io_dtype != GDN_BF16 && d->io_dtype != GDN_F32) return GDN_ERR_INVALID_ARG;
     if (d->flags & ~(uint32_t)GDN_FLAG_ATTN_CAUSAL) return GDN_ERR_INVALID_ARG;
     if ((d->flags & GDN_FLAG_ATTN_CAUSAL) && d->causal_block < 1) return GDN_ERR_INVALID_ARG;
-    if (!(d->scale > 0.0f) || !(d->scale < 1e30f)) return GDN_ERR_INVALID_ARG;
+    // below, what a row's maximum may rise by without rescaling is no finite score
+    if (!(d->scale >= 1e-30f) || !(d->scale < 1e30f)) return GDN_ERR_INVALID_ARG;
     if (d->k_room && d->k_room < d->max_k) return GDN_ERR_INVALID_ARG;
     const int64_t rq = (int64_t)d->Hq * d->D, rk = (int64_t)d->Hk * d->D;
     if ((d->q_stride && d->q_stride < rq) || (d->k_stride && d->k_stride < rk) || (d->v_stride && d->v_stride < rk))

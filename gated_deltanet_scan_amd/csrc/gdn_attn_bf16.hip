@@ -102,6 +102,38 @@ __device__ __forceinline__ const uint16_t* q_row(const AttnArgs& a, const Seq& z
     return static_cast<const uint16_t*>(a.q) + (z.q0 + r / a.G) * a.ldq + (int64_t)(hk * a.G + r % a.G) * a.D;
 }
 
+// For the sums formed again element by element: a lane's half of the features
+// of one row (16 s + 8 h .. + 7) times its own, summed over both halves, and
+// w times the features that its result registers stand for (32 e + 8 i + 4 h ..).
+template <int KS>
+__device__ __forceinline__ float dot_row(const u32x4 (&f)[KS], const uint16_t* row, int h) {
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < KS; ++e) {
+        const u32x4 x = *reinterpret_cast<const u32x4*>(row + 16 * e + 8 * h);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            s += __uint_as_float(f[e][j] << 16) * __uint_as_float(x[j] << 16);
+            s += __uint_as_float(f[e][j] & 0xffff0000u) * __uint_as_float(x[j] & 0xffff0000u);
+        }
+    }
+    return half_sum(s);
+}
+template <int DB>
+__device__ __forceinline__ void add_row(f32x16 (&acc)[DB], float w, const uint16_t* row, int h) {
+#pragma unroll
+    for (int e = 0; e < DB; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const u32x2 x = *reinterpret_cast<const u32x2*>(row + 32 * e + 8 * i + 4 * h);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                acc[e][4 * i + 2 * j] += w * __uint_as_float(x[j] << 16);
+                acc[e][4 * i + 2 * j + 1] += w * __uint_as_float(x[j] & 0xffff0000u);
+            }
+        }
+}
+
 constexpr int kKeys = 64;       // keys per tile
 // The running maximum is raised only when a row's scores pass it by this many
 // powers of two (the exponentials then reach 2^8, which costs no precision in
@@ -265,6 +297,26 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_fwd_kernel(const AttnArgs a) 
                 for (int e = 0; e < DB; ++e) acc[e] = mma(ad.cols(vt[buf ^ 1] + HB, e, u), p1[u], acc[e]);
         }
     }
+    if (a.causal && !finite(acc)) {                           // see finite()
+        m = -INFINITY;
+        l = 0.f;
+#pragma unroll
+        for (int e = 0; e < DB; ++e) acc[e] = zero16();
+        const int end = min(hi, n_last);
+#pragma unroll 1
+        for (int j = lo; j < end; ++j) {
+            const float s = dot_row(q, kb + (int64_t)j * a.ldk, h) * c2;
+            if (j < n) {
+                const float mn = fmaxf(m, s), mj = mn == -INFINITY ? 0.f : mn;
+                const float al = exp2_f(m - mj), pj = exp2_f(s - mj);
+                m = mn;
+                l = l * al + (h == 0 ? pj : 0.f);
+#pragma unroll
+                for (int e = 0; e < DB; ++e) acc[e] *= al;
+                add_row(acc, pj, vb + (int64_t)j * a.ldv, h);
+            }
+        }
+    }
     l = half_sum(l);
     if (!valid) return;
     const float inv = l > 0.f ? 1.0f / l : l;
@@ -378,7 +430,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_dq_kernel(const AttnArgs a) {
                     if (mask) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            if (n0 + 32 * t + 8 * (i >> 2) + 4 * h + (i & 3) >= n) s[i] = 0.f;
+                            if (n0 + 32 * t + 8 * (i >> 2) + 4 * h + (i & 3) >= n) s[i] = dp[i] = 0.f;
                     }
                     if constexpr (kFirst) {
 #pragma unroll
@@ -407,6 +459,16 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_dq_kernel(const AttnArgs a) {
 #pragma unroll
     for (int e = 0; e < DB; ++e) acc[e] = zero16();
     walk(std::false_type());
+    if (a.causal && !finite(acc)) {                           // see finite()
+#pragma unroll
+        for (int e = 0; e < DB; ++e) acc[e] = zero16();
+#pragma unroll 1
+        for (int j = 0; j < n_last; ++j) {
+            const uint16_t* kr = kb + (int64_t)j * a.ldk;
+            const float s = dot_row(q, kr, h), dp = dot_row(g, vb + (int64_t)j * a.ldv, h);
+            if (j < n) add_row(acc, exp2_f(__builtin_fmaf(s, c2, -ls)) * (dp - delta), kr, h);
+        }
+    }
     if (!valid) return;
     if (h == 0) a.delta[gr] = delta;
 #pragma unroll
@@ -467,7 +529,7 @@ struct RowStage {
         ls = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(range(a.lse, (int64_t)a.Hq * 4, 4), at_l, 0, 0));
         dl = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(range(a.delta, (int64_t)a.Hq * 4, 4), at_l, 0, 0));
     }
-    __device__ __forceinline__ void store(unsigned char* qt, unsigned char* gt, float* lt, float* dt, int tid) const {
+    __device__ __forceinline__ void store(unsigned char* qt, unsigned char* gt, float* ld, int tid) const {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const int i = tid + j * NT, rr = i / (D / 8), c = i % (D / 8);
@@ -475,8 +537,8 @@ struct RowStage {
             *reinterpret_cast<u32x4*>(gt + chunk_at<D>(rr, c)) = g[j];
         }
         if (tid < RT) {
-            lt[tid] = ls == -INFINITY ? INFINITY : ls * kLog2e;   // a row that saw nothing: p = 0
-            dt[tid] = dl;
+            ld[tid] = ls == -INFINITY ? INFINITY : ls * kLog2e;   // a row that saw nothing: p = 0
+            ld[RT + tid] = dl;
         }
     }
 };
@@ -490,7 +552,7 @@ template <int D, int NW, int RT>
 __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_kernel(const AttnArgs a) {
     constexpr int NT = 64 * NW, BN = 32 * NW, KS = D / 16, DB = D / 32, TB = RT * D * 2;
     __shared__ __attribute__((aligned(16))) unsigned char qt[2][TB], gt[2][TB];
-    __shared__ __attribute__((aligned(16))) float lt[2][RT], dt[2][RT];
+    __shared__ __attribute__((aligned(16))) float ld[2][2 * RT];   // logarithms, then <d_o, o>
     constexpr bool VL = D == 128;
     __shared__ __attribute__((aligned(16))) unsigned char vl[VL ? BN * D * 2 : 16];
     const Place p = find_place<true>(a, BN);
@@ -542,7 +604,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_kernel(const AttnArgs a) 
     }
     if (start < end) {
         st.load(a, z, p.hk, start, inv, tid);
-        st.store(qt[0], gt[0], lt[0], dt[0], tid);
+        st.store(qt[0], gt[0], ld[0], tid);
     }
     __syncthreads();
     int buf = 0;
@@ -562,7 +624,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_kernel(const AttnArgs a) 
                     dp = mma(ad.rows(gt[buf], t, e), VL ? ad.rows(vl + wave * 64 * D, 0, e) : vf[VL ? 0 : e], dp);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const f32x4 l4 = *reinterpret_cast<const f32x4*>(&lt[buf][32 * t + 8 * i + 4 * h]);
+                    const f32x4 l4 = *reinterpret_cast<const f32x4*>(&ld[buf][32 * t + 8 * i + 4 * h]);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) s[4 * i + j] = exp2_f(__builtin_fmaf(s[4 * i + j], c2, -l4[j]));
                 }
@@ -579,7 +641,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_kernel(const AttnArgs a) 
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const f32x4 d4 = *reinterpret_cast<const f32x4*>(&dt[buf][32 * t + 8 * i + 4 * h]);
+                    const f32x4 d4 = *reinterpret_cast<const f32x4*>(&ld[buf][RT + 32 * t + 8 * i + 4 * h]);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) s[4 * i + j] *= dp[4 * i + j] - d4[j];
                 }
@@ -591,17 +653,42 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_kernel(const AttnArgs a) 
                 }
             }
         }
-        if (more) st.store(qt[buf ^ 1], gt[buf ^ 1], lt[buf ^ 1], dt[buf ^ 1], tid);
+        if (more) st.store(qt[buf ^ 1], gt[buf ^ 1], ld[buf ^ 1], tid);
         __syncthreads();
     }
-    if (!valid) return;
+    // The lane's place once more, from the lane's number: held over the loop it
+    // would take the registers of what the loop needs (4% slower).
+    const int lane2 = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u)), h2 = lane2 >> 5;
+    const int key2 = w0 + (lane2 & 31);
+    const bool valid2 = key2 < z.lk;
+    // see finite(); a hidden value that spoils dv spoils dS, and so dk, as well
+    if (a.causal && !finite(ak)) {
+#pragma unroll
+        for (int e = 0; e < DB; ++e) ak[e] = av[e] = zero16();
+        const int from2 = first_query(a, z, min(key2, z.lk - 1)) * a.G;
+        u32x4 vr[KS];
+#pragma unroll
+        for (int e = 0; e < KS; ++e) vr[e] = VL ? ad.rows(vl + wave * 64 * D, 0, e) : vf[VL ? 0 : e];
+#pragma unroll 1
+        for (int i = max(start, w_first); i < end; ++i) {
+            const int64_t gr = packed_row(a, z, p.hk, i);
+            const uint16_t *qr = q_row(a, z, p.hk, i), *gi = static_cast<const uint16_t*>(a.d_o) + gr * D;
+            const float s = dot_row(kf, qr, h2), dp = dot_row(vr, gi, h2), lr = a.lse[gr];
+            if (lr != -INFINITY && valid2 && i >= from2) {
+                const float pr = exp2_f(__builtin_fmaf(s, c2, -lr * kLog2e));
+                add_row(av, pr, gi, h2);
+                add_row(ak, pr * (dp - a.delta[gr]), qr, h2);
+            }
+        }
+    }
+    if (!valid2) return;
     if (a.k_splits > 1) {
-        const int64_t at = (((int64_t)p.split * a.total_k + z.ko + key) * a.Hk + p.hk) * D;
+        const int64_t at = (((int64_t)p.split * a.total_k + z.ko + key2) * a.Hk + p.hk) * D;
 #pragma unroll
         for (int e = 0; e < DB; ++e)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int d = 32 * e + 8 * i + 4 * h;
+                const int d = 32 * e + 8 * i + 4 * h2;
                 *reinterpret_cast<f32x4*>(a.part_k + at + d) =
                     f32x4{ak[e][4 * i], ak[e][4 * i + 1], ak[e][4 * i + 2], ak[e][4 * i + 3]};
                 *reinterpret_cast<f32x4*>(a.part_v + at + d) =
@@ -609,12 +696,12 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_kernel(const AttnArgs a) 
             }
         return;
     }
-    const int64_t at = ((z.ko + key) * a.Hk + p.hk) * D;
+    const int64_t at = ((z.ko + key2) * a.Hk + p.hk) * D;
 #pragma unroll
     for (int e = 0; e < DB; ++e)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int d = 32 * e + 8 * i + 4 * h;
+            const int d = 32 * e + 8 * i + 4 * h2;
             *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.dk) + at + d) =
                 u32x2{pack_bf16x2(ak[e][4 * i] * a.scale, ak[e][4 * i + 1] * a.scale),
                       pack_bf16x2(ak[e][4 * i + 2] * a.scale, ak[e][4 * i + 3] * a.scale)};

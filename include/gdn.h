@@ -454,8 +454,9 @@ gdn_status gdn_rotary(const gdn_rotary_desc* d, const void* q, const void* k, co
  * arrays are read on the device; offsets outside the tensors are clamped.
  * Tokens of no sequence are neither read nor written, in any output, and key
  * values that no query of a sequence may see, past k_len included, are not used,
- * whatever they hold.  (Within a sequence a non-finite value may reach any of
- * its rows, as it does in a masked matrix product.)
+ * whatever they hold.  An infinity or a NaN reaches the rows that see it and no
+ * others (a masked place is left out, not multiplied by 0), in the gradients too;
+ * row tiles that hold such a value under a mask are computed many times slower.
  *
  * gdn_attn_bwd takes the forward call's q, k, v, o and lse and dO = dL/do, and
  * writes dq, dk and dv (sums over the query heads that share a key head
@@ -463,7 +464,7 @@ gdn_status gdn_rotary(const gdn_rotary_desc* d, const void* q, const void* k, co
  * inputs: bf16 products, the probabilities and dS rounded to bf16 between them),
  * the softmax's statistics float32; results are bitwise reproducible.
  *
- * Hq a multiple of Hk, scale finite and > 0, causal_block >= 1
+ * Hq a multiple of Hk, 1e-30 <= scale < 1e30, causal_block >= 1
  * (GDN_ERR_INVALID_ARG); D in {16, 32, 64, 128}, Hq D and the strides at most
  * 2^20, tokens below 2^31, max_q Hq and max_k at most 2^30 (GDN_ERR_UNSUPPORTED).  Tensors and token
  * strides are multiples of 16 bytes, workspace 256 (its size depends on the

@@ -216,3 +216,9 @@ def test_attn_torch_refusals():
         api.attention_fwd(q, q[..., :32], q[..., :32])
     with pytest.raises(TypeError):
         api.attention_fwd(q.half(), q.half(), q.half())
+
+
+@pytest.mark.parametrize("scale,status", [(0.9e-30, INVALID), (1e-38, INVALID), (2e30, INVALID), (2e-30, None)])
+def test_attn_range_of_scale(lib, scale, status):
+    st = attn_fwd(lib, attn(scale=scale))
+    assert st == status if status is not None else st != INVALID
