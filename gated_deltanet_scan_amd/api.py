@@ -763,8 +763,8 @@ def _attn_args(q, k, v, causal, causal_block, scale, cu_q, cu_k, max_q, max_k):
             raise ValueError("cu_q must hold n_seq + 1 offsets")
         _check(cu_q, "cu_q", torch.int32, (n_seq + 1,))
         _check(cu_k, "cu_k", torch.int32, (n_seq + 1,))
-        max_q = tq if max_q is None else int(max_q)
-        max_k = tk if max_k is None else int(max_k)
+        max_q = tq if max_q is None else min(int(max_q), tq)
+        max_k = tk if max_k is None else min(int(max_k), tk)
     else:
         if cu_q is not None or cu_k is not None or max_q is not None or max_k is not None:
             raise ValueError("cu_q, cu_k, max_q and max_k belong to packed q [T, H, D]")
@@ -776,7 +776,8 @@ def _attn_args(q, k, v, causal, causal_block, scale, cu_q, cu_k, max_q, max_k):
     if causal_block is None:
         causal_block = sq[2] if dims == 5 else 1
     _same_device(q, k=k, v=v, cu_q=cu_q, cu_k=cu_k)
-    desc = _lib.GdnAttnDesc(tq, tk, ldq, ldk, ldv, rk, n_seq, Hq, Hk, D, max_q, max_k, int(causal_block), io,
+    desc = _lib.GdnAttnDesc(tq, tk, ldq, ldk, ldv, rk, n_seq, Hq, Hk, D, max_q, max_k,
+                            min(int(causal_block), 2 ** 31 - 1), io,
                             _lib.GDN_FLAG_ATTN_CAUSAL if causal else 0, D ** -0.5 if scale is None else scale)
     return desc, cu_q, cu_k
 

@@ -9,10 +9,17 @@ the graph is freed), and the backward pass is gdn_frame_scan_bwd_saved.  With
 ``recompute=True`` the forward pass keeps nothing and the backward pass
 (gdn_frame_scan_bwd) recomputes the operands instead.  Both give the same
 gradients bit for bit.
+
+``layer_norm``, ``rotary`` and ``attention`` are differentiable once.  A training
+step captured into a graph takes its leaves' first gradients inside the capture:
+torch ties a leaf's accumulation to the stream of the first graph that uses it,
+so no eager graph of the same leaves may be alive meanwhile.  Where one has to
+be, capture the api calls (layer_norm_fwd, layer_norm_bwd and so on) instead.
 """
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import api
 
@@ -59,6 +66,7 @@ class _LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, mean, rstd, weight, bias = ctx.saved_tensors
         dx, dweight, dbias = api.layer_norm_bwd(dy.contiguous(), x, mean, rstd, weight, bias)
@@ -79,6 +87,7 @@ class _Rotary(torch.autograd.Function):
         return api.rotary(q, k, pos, axes=axes, theta=theta, halves=halves, inverse=inverse)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq, dk):
         pos, = ctx.saved_tensors
         dq = None if dq is None else dq.contiguous()
@@ -106,6 +115,7 @@ class _Attention(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dO):
         q, k, v, o, lse, cu_q, cu_k = ctx.saved_tensors
         outs = [None] * 3 if cu_q is None else [torch.zeros(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v)]

@@ -159,30 +159,27 @@ __device__ __forceinline__ Place find_place(const AttnArgs& a, int size) {
             __ffsll((unsigned long long)__ballot(t > level && before == w - above)) - 1);
         count = __builtin_amdgcn_readlane(t, p.s);
     } else {
-        // many sequences: in their order, which by itself spreads the work
+        // Many sequences: in their order, which by itself spreads the work.
+        // Sequence s has the places from floor(rows before it / size) + s on, which
+        // are never fewer than its tiles, so a search of 64 places at a time finds
+        // it without adding up the tiles of all before it (8192 sequences of 1 to
+        // 299 tokens, forward and backward: 4670 us against 13900 with the sum).
         const int lane = threadIdx.x & 63;
-        int base = 0;
-        p.s = -1;
-        count = level = 0;
-        for (int s0 = 0; s0 < a.n_seq; s0 += 64) {
-            const int t = s0 + lane < a.n_seq ? tiles_of<KEYS>(a, s0 + lane, size) : 0;
-            int scan = t;
-#pragma unroll
-            for (int d = 1; d < 64; d *= 2) {
-                const int up = __shfl_up(scan, d);
-                if (lane >= d) scan += up;
-            }
-            const int total = __builtin_amdgcn_readlane(scan, 63);
-            if (w < base + total) {
-                const int hit =
-                    __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)__ballot(base + scan > w)) - 1);
-                count = __builtin_amdgcn_readlane(t, hit);
-                level = base + __builtin_amdgcn_readlane(scan, hit) - 1 - w;
-                p.s = s0 + hit;
-                break;
-            }
-            base += total;
+        auto start = [&](int s) {
+            const uint64_t at = (uint64_t)min(max((int64_t)cu[s], (int64_t)0), KEYS ? a.total_k : a.total_q);
+            return (int64_t)((KEYS ? at : at * (unsigned)a.G) / (unsigned)size) + s;
+        };
+        int lo = 0, hi = a.n_seq;                             // start(lo) <= w < start(hi)
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 63) / 64, s = lo + step * lane;
+            const uint64_t at = __ballot(s < hi && (lane == 0 || start(s) <= w));
+            lo += step * (63 - __clzll((long long)at));
+            hi = min(hi, lo + step);
         }
+        p.s = __builtin_amdgcn_readfirstlane(lo);
+        count = tiles_of<KEYS>(a, p.s, size);
+        level = count - 1 - (int)(w - start(p.s));
+        if (level < 0 || level >= count) p.s = -1;
         if (p.s < 0) return p;
     }
     p.s = __builtin_amdgcn_readfirstlane(p.s);
@@ -190,11 +187,14 @@ __device__ __forceinline__ Place find_place(const AttnArgs& a, int size) {
     return p;
 }
 // Workgroups of one split and key head that find_place hands out: no more than
-// every sequence's share of the tensor, rounded up.
+// every sequence's share of the tensor, rounded up (all of them where the places
+// are found by search).
 inline int64_t places(int64_t rows, int64_t most, int n_seq, int size, bool packed, int* tiles) {
     *tiles = (int)((most + size - 1) / size);
     const int64_t all = (int64_t)*tiles * n_seq;
-    return packed && *tiles > 1 ? (all < rows / size + n_seq ? all : rows / size + n_seq) : all;
+    if (!packed || *tiles <= 1) return all;
+    const int64_t share = rows / size + n_seq;
+    return n_seq > 64 || share < all ? share : all;
 }
 
 // Hidden places and values that are not finite.  A matrix product multiplies a

@@ -440,3 +440,31 @@ def test_long_cache_offsets_past_32_bits():
     o, lse = api.attention_fwd(q[:1], kf, vf, cu_q=cu_q, cu_k=cu_k, max_q=1, max_k=n, causal=True)
     torch.cuda.synchronize()
     compare(q[:1], kk, vv, q[:1], [0], [0], [1], [n], True, 1, D ** -0.5, (o, lse), ("o", "lse"))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_thousands_of_sequences(dtype):
+    """More sequences than one step of the tile search takes, a few of them of
+    several tiles."""
+    n = 1300
+    lens = [(3, 0, 1, 2)[i % 4] for i in range(n)]
+    for i in (0, 511, 512, 777, n - 1):
+        lens[i] = 150
+    cu = starts(lens)
+    q, k, v, do = inputs(cu, cu, 2, 1, 32, dtype, seed=n)
+    kw = dict(causal=True, cu_q=torch.from_numpy(cu).cuda(), max_q=150, max_k=150)
+    o, lse = api.attention_fwd(q, k, v, **kw)
+    grads = api.attention_bwd(q, k, v, o, lse, do, **kw)
+    torch.cuda.synchronize()
+    compare(q, k, v, do, cu, cu, lens, lens, True, 1, 32 ** -0.5, (o, lse, *grads), ("o", "lse", "dq", "dk", "dv"))
+
+
+def test_bounds_past_the_tensors():
+    """max_q, max_k and causal_block of more than 32 bits mean all tokens."""
+    q, k, v, do = inputs([0, 200], [0, 200], 2, 2, 32, BF, seed=3)
+    cu = torch.tensor([0, 80, 200], dtype=torch.int32, device="cuda")
+    a = api.attention_fwd(q, k, v, cu_q=cu, causal=True, causal_block=2 ** 32 + 1, max_q=2 ** 32 + 1, max_k=2 ** 40)
+    b = api.attention_fwd(q, k, v, cu_q=cu, max_q=120, max_k=120)
+    torch.cuda.synchronize()
+    compare(q, k, v, do, [0, 80], [0, 80], [80, 120], [80, 120], False, 1, 32 ** -0.5, a, ("o", "lse"))
+    compare(q, k, v, do, [0, 80], [0, 80], [80, 120], [80, 120], False, 1, 32 ** -0.5, b, ("o", "lse"))

@@ -164,3 +164,14 @@ def test_training_step_gradients(dtype):
         e = rel(host(a), r.detach().numpy())
         print("%s: rel %.2e" % (n, e))
         assert e <= bar, n
+
+
+def test_second_derivatives_are_refused():
+    x = torch.randn(4, 96, device="cuda", requires_grad=True)
+    q = torch.randn(1, 4, 2, 32, device="cuda", requires_grad=True)
+    pos = torch.zeros(4, 1, dtype=torch.int32, device="cuda")
+    for leaf, y in ((x, autograd.layer_norm(x)), (q, autograd.rotary(q, None, pos, axes=(32,))[0]),
+                    (q, autograd.attention(q, q, q))):
+        g, = torch.autograd.grad((y * y).sum(), leaf, create_graph=True)
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            g.sum().backward()
