@@ -105,6 +105,9 @@ __device__ __forceinline__ float dot_row(const f32x4 (&f)[D / 16], const T* row,
     return col_sum(s);
 }
 
+// Bound by the fp32 matrix instructions (154 TFLOP/s in a large product) and,
+// of two waves a SIMD, the wait between them: 4096 x 4096, 16 heads of 128, no
+// mask: 1326 us, 104 TFLOP/s (D = 64: 102, D = 32: 85).
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void attn_fwd_f32_kernel(const AttnArgs a) {
     __shared__ float kt[kTile][D + 4], vt[kTile][D + 4];
@@ -217,6 +220,8 @@ __global__ __launch_bounds__(kThreads) void attn_fwd_f32_kernel(const AttnArgs a
 // weighs one split (64 at a time), then each quarter of the wave adds every
 // fourth split's row, several loads in flight; the quarters add up in order.
 // The rows are the sequences' own, so what lies behind the last is left alone.
+// Bound by the latency of a few dependent trips to the partial results: 8
+// single queries of 32 heads in 8.5 us, 880 of 16 heads in 9.5.
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void attn_join_kernel(const AttnArgs a) {
     constexpr int E = (D + 63) / 64;
@@ -271,7 +276,8 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(const AttnArgs a) {
 }
 
 // dq, and <d_o, o> for the dk/dv kernel: query rows as columns, as in the
-// forward kernel.
+// forward kernel.  4096 x 4096, 16 heads of 128: 1659 us, 124 TFLOP/s of 6 D
+// flops a pair.
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void attn_dq_f32_kernel(const AttnArgs a) {
     __shared__ float kt[kTile][D + 4], vt[kTile][D + 4];
@@ -359,6 +365,8 @@ __global__ __launch_bounds__(kThreads) void attn_dq_f32_kernel(const AttnArgs a)
 }
 
 // dk and dv: a wave's 16 keys as columns, the packed query rows staged in LDS.
+// 4096 x 4096, 16 heads of 128: 2744 us, 100 TFLOP/s of 8 D flops a pair (one
+// wave a SIMD at D = 128: K, V and both sums take 300 registers).
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void attn_dkv_f32_kernel(const AttnArgs a) {
     __shared__ float qt[kTile][D + 4], dt[kTile][D + 4];
@@ -490,7 +498,9 @@ __global__ __launch_bounds__(kThreads) void attn_dkv_f32_kernel(const AttnArgs a
 }
 
 // dk and dv from the splits' sums, four features a thread.  The keys are the
-// sequences' own; what lies outside them is left alone.
+// sequences' own; what lies outside them is left alone.  Bound by reading the
+// sums: 4 splits of 8176 keys, 4 heads of 128 (134 MB, half of it still in the
+// caches) in 25 us.
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void attn_sum_kernel(const AttnArgs a) {
     const unsigned per = kThreads / (D / 4), groups = ((unsigned)a.max_k * a.Hk + per - 1) / per;

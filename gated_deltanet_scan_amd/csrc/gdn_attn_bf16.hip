@@ -174,6 +174,13 @@ struct Tile {
 // 450 cycles of vector instructions), with no dependence between them, so both
 // pipes of a SIMD work at once.  K of a tile is therefore in LDS half a tile
 // before V of it.
+//
+// Measured: frame-causal clip of 18480 tokens, 16 heads of 128: 1.40 ms, 1050
+// TFLOP/s, 76% of a large library product's rate; the matrix pipes are busy
+// half the time, two waves a SIMD leave the rest to dependences within a step.
+// 4096 x 4096, 16 heads, no mask: 908 TFLOP/s at D = 128 (256 workgroups, one
+// round), 655 at 64 and 473 at 32, where exponentials (16 a lane and step
+// whatever D is) bound it.
 template <int D, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void attn_fwd_kernel(const AttnArgs a) {
     constexpr int NT = 64 * NW, BM = 32 * NW, KS = D / 16, DB = D / 32, TB = kKeys * D * 2, HB = TB / 2;
@@ -352,6 +359,10 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_fwd_kernel(const AttnArgs a) 
 // sequence of 300 tokens: dq off by 2.40e-3 with it and 2.26e-3 without, of
 // which 1.68e-3 are dq's own rounding).  Where the workgroup's rows see at most
 // kExactKeys keys the sum is formed in fp32 by a first walk over them.
+//
+// Measured: 4096 x 4096, 16 heads of 128: 227 us, 910 TFLOP/s of 6 D flops a
+// pair (783 at D = 64, 603 at 32); two waves a SIMD wait on the products of one
+// step before its exponentials, and on those before the next products.
 constexpr int kExactKeys = 256;
 template <int D, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void attn_dq_kernel(const AttnArgs a) {
@@ -548,6 +559,8 @@ struct RowStage {
 // ways (S = Q K^T and dP = dO V^T by rows; dV^T += dO^T P, dK^T += Q^T dS).
 // At D = 128 the two accumulators take 128 registers; V then stays in LDS and
 // row tiles are half as long, so that two waves fit a SIMD.
+// Measured: 4096 x 4096, 16 heads of 128: 359 us, 765 TFLOP/s of 8 D flops a
+// pair (759 at D = 64, 565 at 32); bound as dq is, and by V's reads from LDS.
 template <int D, int NW, int RT>
 __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_kernel(const AttnArgs a) {
     constexpr int NT = 64 * NW, BN = 32 * NW, KS = D / 16, DB = D / 32, TB = RT * D * 2;

@@ -110,6 +110,9 @@ __device__ __forceinline__ void narrow(const float* f, float& r) { r = f[0]; }
 // A thread keeps its place within the head and takes (token, head) items in
 // batches of four, loading a batch whole before it stores any of it: the
 // outputs may be the inputs, so the compiler may not move a load past a store.
+// Measured: 106480 tokens of 16 + 16 heads of 128, bf16, in 317 us (1.74 GB,
+// 5.5 TB/s); 880 tokens in 6.9 us, of which the angles and one trip to memory
+// are most.  LDS conflicts (table rows read by all heads) stay hidden.
 template <typename T, int VW, bool HALVES>
 __global__ __launch_bounds__(kThreads) void rotary_kernel(const RotArgs a) {
     using R = typename VecN<T, VW>::R;
