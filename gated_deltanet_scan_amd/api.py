@@ -707,19 +707,17 @@ def _token_strides(t, name):
     axes = [i for i in range(t.dim() - 2) if t.shape[i] > 1]
     batch = bool(axes) and t.dim() > 3 and axes[0] == 0
     inner = axes[1:] if batch else axes
-    ld = t.stride(inner[-1]) if inner else H * D
-    ok = ok and ld >= H * D
+    # one token a sequence: the step between the sequences is the token stride
+    ld = t.stride(inner[-1]) if inner else t.stride(0) if batch else H * D
+    ok = ok and ld >= H * D                   # not broadcast (0 would mean packed), no tokens that overlap
     step = ld
     for i in reversed(inner):                 # the token axes continue one step
         ok = ok and t.stride(i) == step
         step *= t.shape[i]
     room = 0
-    if batch and t.stride(0) != step:
-        if not inner:                         # one token a sequence: any step between them will do
-            ld = t.stride(0)
-        else:
-            room = t.stride(0) // ld
-            ok = ok and t.stride(0) % ld == 0 and t.stride(0) > step
+    if ok and batch and inner and t.stride(0) != step:
+        room = t.stride(0) // ld
+        ok = t.stride(0) % ld == 0 and t.stride(0) > step
     if not ok:
         raise ValueError("%s must have packed heads and evenly spaced tokens" % name)
     return ld, room
