@@ -520,6 +520,12 @@ __global__ __launch_bounds__(kThreads) void attn_sum_kernel(const AttnArgs a) {
 }
 
 // ---------------------------------------------------------------- launch
+// A token stride that the kernels cannot address: see kMaxStride; 2^40 elements
+// in all are more than any tensor has.
+bool far(int64_t stride, int most, int64_t tokens) {
+    return stride > kMaxStride && (most > 1 || stride > ((int64_t)1 << 40) / std::max<int64_t>(tokens, 1));
+}
+
 gdn_status check_attn(const gdn_attn_desc* d) {
     if (!d) return GDN_ERR_INVALID_ARG;
     if (d->n_seq < 0 || d->Hq < 1 || d->Hk < 1 || d->D < 1 || d->total_q < 0 || d->total_k < 0 || d->max_q < 0 ||
@@ -536,11 +542,13 @@ gdn_status check_attn(const gdn_attn_desc* d) {
     if ((d->q_stride && d->q_stride < rq) || (d->k_stride && d->k_stride < rk) || (d->v_stride && d->v_stride < rk))
         return GDN_ERR_INVALID_ARG;
     if (d->D != 16 && d->D != 32 && d->D != 64 && d->D != 128) return GDN_ERR_UNSUPPORTED;
-    if (rq > (1 << 20) || d->q_stride > (1 << 20) || d->k_stride > (1 << 20) || d->v_stride > (1 << 20))
-        return GDN_ERR_UNSUPPORTED;
     // row numbers within a sequence are 32-bit, with room for a tile
     if (d->total_q > INT32_MAX || d->total_k > INT32_MAX || (int64_t)d->max_q * d->Hq > (1 << 30) ||
         d->max_k > (1 << 30) || d->k_room > INT32_MAX)
+        return GDN_ERR_UNSUPPORTED;
+    const int64_t tk = d->k_room ? d->k_room * d->n_seq : d->total_k;
+    if (rq > kMaxStride || far(d->q_stride, d->max_q, d->total_q) || far(d->k_stride, d->max_k, tk) ||
+        far(d->v_stride, d->max_k, tk))
         return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }

@@ -18,6 +18,13 @@ using namespace gdnops;
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// The widest token stride of sequences of several tokens, so that offsets
+// within a tile fit 32 bits.  Single tokens may lie further apart: they are
+// addressed in 64 bits as the first of their sequence, and the places of a tile
+// past them need no address but one past its end, which this stride gives too.
+constexpr int64_t kMaxStride = 1 << 20;
+__device__ __forceinline__ uint32_t tile_stride(int64_t ld) { return (uint32_t)min(ld, kMaxStride); }
+
 struct AttnArgs {
     const void *q, *k, *v, *o, *d_o;
     void *out, *dq, *dk, *dv;            // out: o of the forward call

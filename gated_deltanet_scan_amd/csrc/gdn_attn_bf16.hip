@@ -153,7 +153,7 @@ struct Tile {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const int i = tid + j * NT, row = i / (D / 8), c = i % (D / 8);
-            x[j] = __builtin_amdgcn_raw_buffer_load_b128(rs, (uint32_t)(row * (int)ld * 2 + c * 16), 0, 0);
+            x[j] = __builtin_amdgcn_raw_buffer_load_b128(rs, (uint32_t)row * tile_stride(ld) * 2 + c * 16, 0, 0);
         }
     }
     __device__ __forceinline__ void store(unsigned char* t, int tid) const {
@@ -519,7 +519,7 @@ struct RowStage {
             for (int j = 0; j < N; ++j) {
                 const int i = tid + j * NT, c = i % (D / 8);
                 const uint32_t tok = token(i / (D / 8), gg);
-                at_q[j] = tok * (uint32_t)(a.ldq * 2) + gg * (2 * D) + c * 16;
+                at_q[j] = tok * (tile_stride(a.ldq) * 2) + gg * (2 * D) + c * 16;
                 at_g[j] = tok * (uint32_t)(a.Hq * D * 2) + gg * (2 * D) + c * 16;
             }
             const uint32_t tok = token(tid & (RT - 1), gg);

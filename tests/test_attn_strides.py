@@ -1,10 +1,13 @@
 """Which views attention takes, on the host: the token stride that the torch
 wrapper passes across the ABI (0 there means packed), and the ABI's own bounds.
 """
+import ctypes
+import os
+
 import pytest
 import torch
 
-from gated_deltanet_scan_amd import api
+from gated_deltanet_scan_amd import _lib, api
 
 
 @pytest.mark.parametrize("one,shape", [
@@ -35,3 +38,39 @@ def test_views_that_are_taken(shape):
         cache = torch.zeros((shape[0], 9) + shape[2:])[:, :shape[1]]
         want = (9 * H * D, 0) if shape[1] == 1 else (H * D, 9)
         assert api._token_strides(cache, "k") == want
+
+
+# ------------------------------------------------------------------ the ABI's bounds
+OK, INVALID, UNSUPPORTED, ALIAS = 0, 1, 2, 4
+BASE = 0x7f0000000000
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(_lib.LIB_PATH):
+        from gated_deltanet_scan_amd import build
+        build.build()
+    return _lib.load()
+
+
+def both(lib, tq, tk, n, mq, mk, qs=0, ks=0, vs=0, room=0, Hq=4, Hk=2, D=64):
+    """Statuses of the two passes on addresses that are no memory.  The outputs
+    alias q, which is found last of all: what the ABI takes ends in ALIAS, and
+    nothing is launched."""
+    d = ctypes.byref(_lib.GdnAttnDesc(tq, tk, qs, ks, vs, room, n, Hq, Hk, D, mq, mk, 1, _lib.GDN_BF16, 0, 0.1))
+    p = [BASE + i * (1 << 44) for i in range(9)]
+    f = lib.gdn_attn_fwd(d, p[0], p[1], p[2], None, None, None, p[0], None, p[3], 1 << 40, None)
+    b = lib.gdn_attn_bwd(d, p[0], p[1], p[2], p[4], p[5], p[6], None, None, p[0], p[7], p[8], p[3], 1 << 40, None)
+    return f, b
+
+
+@pytest.mark.parametrize("stride,tokens,most,expect", [
+    (1 << 20, 4, 1, ALIAS), (1 << 20, 4, 2, ALIAS),
+    ((1 << 20) + 8, 4, 2, UNSUPPORTED),                       # two tokens of one sequence that far apart
+    ((1 << 20) + 8, 4, 1, ALIAS), (1 << 34, 4, 1, ALIAS),     # single tokens of a long cache's slots
+    ((1 << 38) + 8, 4, 1, UNSUPPORTED),                       # past any tensor
+])
+@pytest.mark.parametrize("which", ["qs", "ks", "vs"])
+def test_range_of_strides(lib, which, stride, tokens, most, expect):
+    n = tokens // most
+    assert both(lib, tokens, tokens, n, most, most, **{which: stride}) == (expect, expect)
