@@ -553,6 +553,15 @@ gdn_status check_attn(const gdn_attn_desc* d) {
     return GDN_OK;
 }
 
+// The call with its bounds no higher than the tensors allow (whatever lies above
+// them is the same call, and would only be more places to launch).
+gdn_attn_desc bounded(const gdn_attn_desc* d) {
+    gdn_attn_desc b = *d;
+    b.max_q = (int32_t)std::min<int64_t>(b.max_q, b.total_q);
+    b.max_k = (int32_t)std::min<int64_t>(b.max_k, b.total_k);
+    return b;
+}
+
 bool fast(const gdn_attn_desc* d) { return d->io_dtype == GDN_BF16 && d->D >= 32; }
 
 int fwd_rows(const gdn_attn_desc* d) {
@@ -591,7 +600,7 @@ int fwd_splits(const gdn_attn_desc* d) {
 // whether the sequences are packed (uniform ones count the same tiles).
 int bwd_splits(const gdn_attn_desc* d) {
     int tiles;
-    const int64_t items = places(d->total_k, d->max_k, d->n_seq, fast(d) ? 128 : kRows, true, &tiles) * d->Hk;
+    const int64_t items = places(d->total_k, d->max_k, d->n_seq, fast(d) ? kBwdTile : kRows, true, &tiles) * d->Hk;
     const int64_t rows = (int64_t)d->max_q * (d->Hq / d->Hk);
     // what 32 MiB of sums allow stays in the caches
     const int64_t near = ((int64_t)32 << 20) / std::max<int64_t>(1, d->total_k * d->Hk * d->D * 8);
@@ -626,49 +635,58 @@ int64_t key_rows(const gdn_attn_desc* d, bool packed) {
     return (d->n_seq - 1) * d->k_room + d->max_k;
 }
 
-bool grid_of(int64_t n, unsigned* g) {
-    if (n > INT32_MAX) return false;
-    *g = (unsigned)n;
-    return true;
-}
-
-template <typename T, int D>
-gdn_status run_fwd(AttnArgs a, hipStream_t s) {
-    unsigned grid;
-    const int64_t n = places(a.total_q * a.G, (int64_t)a.max_q * a.G, a.n_seq, kRows, a.cu_q, &a.tiles);
-    if (!grid_of(n * a.splits * a.Hk, &grid)) return GDN_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL((attn_fwd_f32_kernel<T, D>), dim3(grid), dim3(kThreads), 0, s, a);
-    return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
-}
-template <typename T, int D>
-gdn_status run_join(AttnArgs a, hipStream_t s) {
-    unsigned grid;
+// The launches of a call, all of them sized before the first.
+struct FwdGrids {
+    Grid main;
+    unsigned join;                       // splits > 1
+};
+bool fwd_grids(AttnArgs& a, int rows, bool f32_kernel, FwdGrids* g) {
+    const int64_t n = places(a.total_q * a.G, (int64_t)a.max_q * a.G, a.n_seq, rows, a.cu_q, &g->main.tiles);
+    if (!grid_of(n * a.splits * a.Hk, f32_kernel ? kThreads : 2 * rows, &g->main.groups)) return false;
+    g->join = 0;
+    if (a.splits == 1) return true;
     // A row a wave where they are few (eight single-token requests: 80 us against
     // 95 with four), four where places of shorter sequences stay empty in number.
-    const int64_t rows = (int64_t)a.max_q * a.Hq;
-    a.join_rows = rows * a.n_seq > 16384 ? 16 : 4;
-    if (!grid_of((rows + a.join_rows - 1) / a.join_rows * a.n_seq, &grid)) return GDN_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3(grid), dim3(kThreads), 0, s, a);
-    return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+    const int64_t all = (int64_t)a.max_q * a.Hq;
+    a.join_rows = all * a.n_seq > 16384 ? 16 : 4;
+    return grid_of((all + a.join_rows - 1) / a.join_rows * a.n_seq, kThreads, &g->join);
 }
-template <typename T, int D>
-gdn_status run_bwd(AttnArgs a, hipStream_t s) {
-    unsigned grid;
-    int64_t n = places(a.total_q * a.G, (int64_t)a.max_q * a.G, a.n_seq, kRows, a.cu_q, &a.tiles);
-    if (!grid_of(n * a.Hk, &grid)) return GDN_ERR_UNSUPPORTED;
-    if (grid) hipLaunchKernelGGL((attn_dq_f32_kernel<T, D>), dim3(grid), dim3(kThreads), 0, s, a);
-    n = places(a.total_k, a.max_k, a.n_seq, kRows, a.cu_k, &a.tiles);
-    if (!grid_of(n * a.Hk * a.k_splits, &grid)) return GDN_ERR_UNSUPPORTED;
-    if (grid) hipLaunchKernelGGL((attn_dkv_f32_kernel<T, D>), dim3(grid), dim3(kThreads), 0, s, a);
-    return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+struct BwdGrids {
+    Grid dq, dkv;
+    unsigned sum;                        // k_splits > 1
+};
+bool bwd_grids(const AttnArgs& a, int size, BwdGrids* g) {
+    int64_t n = places(a.total_q * a.G, (int64_t)a.max_q * a.G, a.n_seq, size, a.cu_q, &g->dq.tiles);
+    if (!grid_of(n * a.Hk, kThreads, &g->dq.groups)) return false;
+    n = places(a.total_k, a.max_k, a.n_seq, size, a.cu_k, &g->dkv.tiles);
+    if (!grid_of(n * a.Hk * a.k_splits, kThreads, &g->dkv.groups)) return false;
+    g->sum = 0;
+    const int64_t per = kThreads / (a.D / 4);
+    return a.k_splits == 1 || grid_of(((int64_t)a.max_k * a.Hk + per - 1) / per * a.n_seq, kThreads, &g->sum);
 }
 
 template <typename T, int D>
-gdn_status run_sum(const AttnArgs& a, hipStream_t s) {
-    unsigned grid;
-    const int64_t per = kThreads / (D / 4);
-    if (!grid_of(((int64_t)a.max_k * a.Hk + per - 1) / per * a.n_seq, &grid)) return GDN_ERR_UNSUPPORTED;
-    if (grid) hipLaunchKernelGGL((attn_sum_kernel<T, D>), dim3(grid), dim3(kThreads), 0, s, a);
+gdn_status run_fwd(AttnArgs a, Grid g, hipStream_t s) {
+    a.tiles = g.tiles;
+    hipLaunchKernelGGL((attn_fwd_f32_kernel<T, D>), dim3(g.groups), dim3(kThreads), 0, s, a);
+    return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+template <typename T, int D>
+gdn_status run_join(const AttnArgs& a, unsigned groups, hipStream_t s) {
+    hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3(groups), dim3(kThreads), 0, s, a);
+    return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+template <typename T, int D>
+gdn_status run_bwd(AttnArgs a, Grid dq, Grid dkv, hipStream_t s) {
+    a.tiles = dq.tiles;
+    if (dq.groups) hipLaunchKernelGGL((attn_dq_f32_kernel<T, D>), dim3(dq.groups), dim3(kThreads), 0, s, a);
+    a.tiles = dkv.tiles;
+    if (dkv.groups) hipLaunchKernelGGL((attn_dkv_f32_kernel<T, D>), dim3(dkv.groups), dim3(kThreads), 0, s, a);
+    return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+template <typename T, int D>
+gdn_status run_sum(const AttnArgs& a, unsigned groups, hipStream_t s) {
+    if (groups) hipLaunchKernelGGL((attn_sum_kernel<T, D>), dim3(groups), dim3(kThreads), 0, s, a);
     return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
@@ -682,7 +700,8 @@ extern "C" {
 
 size_t gdn_attn_workspace_size(const gdn_attn_desc* d) {
     if (check_attn(d) != GDN_OK || d->n_seq == 0 || d->total_q == 0 || d->max_q == 0) return 0;
-    const int64_t n = fwd_splits(d);
+    const gdn_attn_desc b = bounded(d);
+    const int64_t n = fwd_splits(&b);
     if (n < 2) return 0;
     return round256((size_t)n * d->total_q * d->Hq * d->D * 4) + round256((size_t)n * d->total_q * d->Hq * 4);
 }
@@ -696,7 +715,13 @@ gdn_status gdn_attn_fwd(const gdn_attn_desc* d, const void* q, const void* k, co
     if (!cu_k && (int64_t)d->n_seq * d->max_k != d->total_k) return GDN_ERR_INVALID_ARG;
     if (d->n_seq == 0 || d->total_q == 0 || d->max_q == 0) return GDN_OK;
     if (!q || !o || (d->total_k > 0 && (!k || !v))) return GDN_ERR_INVALID_ARG;
-    AttnArgs a = fill(d);
+    const gdn_attn_desc b = bounded(d);
+    AttnArgs a = fill(&b);
+    a.cu_q = cu_q, a.cu_k = cu_k, a.k_len = k_len;
+    a.splits = fwd_splits(&b);
+    a.chunk = fwd_chunk(&b);
+    FwdGrids g;
+    if (!fwd_grids(a, fwd_rows(&b), !fast(d), &g)) return GDN_ERR_UNSUPPORTED;
     const size_t e = d->io_dtype == GDN_F32 ? 4 : 2;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
         !aligned(cu_q, 4) || !aligned(cu_k, 4) || !aligned(k_len, 4))
@@ -707,8 +732,8 @@ gdn_status gdn_attn_fwd(const gdn_attn_desc* d, const void* q, const void* k, co
     if (need && !aligned(workspace, 256)) return GDN_ERR_ALIGNMENT;
     const int64_t wq = (int64_t)d->Hq * d->D, wk = (int64_t)d->Hk * d->D;
     const Range ins[] = {rng(q, span(d->total_q, a.ldq, wq, e)), rng(k, span(key_rows(d, cu_k), a.ldk, wk, e)),
-                         rng(v, span(key_rows(d, cu_k), a.ldv, wk, e)), rng(cu_q, (size_t)(d->n_seq + 1) * 4),
-                         rng(cu_k, (size_t)(d->n_seq + 1) * 4), rng(k_len, (size_t)d->n_seq * 4)};
+                         rng(v, span(key_rows(d, cu_k), a.ldv, wk, e)), rng(cu_q, ((size_t)d->n_seq + 1) * 4),
+                         rng(cu_k, ((size_t)d->n_seq + 1) * 4), rng(k_len, (size_t)d->n_seq * 4)};
     const Range outs[] = {rng(o, (size_t)d->total_q * wq * e), rng(lse, (size_t)d->total_q * d->Hq * 4),
                           rng(need ? workspace : nullptr, need)};
     for (int i = 0; i < 3; ++i) {
@@ -719,9 +744,7 @@ gdn_status gdn_attn_fwd(const gdn_attn_desc* d, const void* q, const void* k, co
     }
     int cus;
     if ((st = check_device(&cus)) != GDN_OK) return st;
-    a.q = q, a.k = k, a.v = v, a.out = o, a.lse = lse, a.cu_q = cu_q, a.cu_k = cu_k, a.k_len = k_len;
-    a.splits = fwd_splits(d);
-    a.chunk = fwd_chunk(d);
+    a.q = q, a.k = k, a.v = v, a.out = o, a.lse = lse;
     if (a.splits > 1) {
         a.part_o = static_cast<float*>(workspace);
         a.part_lse = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
@@ -730,14 +753,17 @@ gdn_status gdn_attn_fwd(const gdn_attn_desc* d, const void* q, const void* k, co
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const bool f32 = d->io_dtype == GDN_F32;
     // bf16 heads of 16 features are narrower than the bf16 tiles and take the fp32 kernels
-    st = f32 ? GDN_BY_D(run_fwd, float, a, s) : fast(d) ? attn_fwd_bf16(a, s) : run_fwd<uint16_t, 16>(a, s);
+    st = f32       ? GDN_BY_D(run_fwd, float, a, g.main, s)
+         : fast(d) ? attn_fwd_bf16(a, fwd_rows(&b), g.main, s)
+                   : run_fwd<uint16_t, 16>(a, g.main, s);
     if (st != GDN_OK || a.splits == 1) return st;
-    return f32 ? GDN_BY_D(run_join, float, a, s) : GDN_BY_D(run_join, uint16_t, a, s);
+    return f32 ? GDN_BY_D(run_join, float, a, g.join, s) : GDN_BY_D(run_join, uint16_t, a, g.join, s);
 }
 
 size_t gdn_attn_workspace_size_bwd(const gdn_attn_desc* d) {
     if (check_attn(d) != GDN_OK || d->n_seq == 0) return 0;
-    const size_t n = bwd_splits(d);
+    const gdn_attn_desc b = bounded(d);
+    const size_t n = bwd_splits(&b);
     return round256((size_t)d->total_q * d->Hq * 4) + (n > 1 ? 2 * round256(n * d->total_k * d->Hk * d->D * 4) : 0);
 }
 
@@ -751,7 +777,12 @@ gdn_status gdn_attn_bwd(const gdn_attn_desc* d, const void* q, const void* k, co
     if (d->n_seq == 0 || (d->total_q == 0 && d->total_k == 0)) return GDN_OK;
     if (d->total_q > 0 && (!q || !o || !lse || !dO || !dq)) return GDN_ERR_INVALID_ARG;
     if (d->total_k > 0 && (!k || !v || !dk || !dv)) return GDN_ERR_INVALID_ARG;
-    AttnArgs a = fill(d);
+    const gdn_attn_desc b = bounded(d);
+    AttnArgs a = fill(&b);
+    a.cu_q = cu_q, a.cu_k = cu_k;
+    a.k_splits = bwd_splits(&b);
+    BwdGrids g;
+    if (!bwd_grids(a, fast(d) ? kBwdTile : kRows, &g)) return GDN_ERR_UNSUPPORTED;
     const size_t e = d->io_dtype == GDN_F32 ? 4 : 2;
     for (const void* p : {q, k, v, o, dO, (const void*)dq, (const void*)dk, (const void*)dv})
         if (!aligned(p, 16)) return GDN_ERR_ALIGNMENT;
@@ -764,8 +795,8 @@ gdn_status gdn_attn_bwd(const gdn_attn_desc* d, const void* q, const void* k, co
     const size_t qb = (size_t)d->total_q * wq * e, kb = (size_t)d->total_k * wk * e;
     const Range ins[] = {rng(q, span(d->total_q, a.ldq, wq, e)), rng(k, span(key_rows(d, cu_k), a.ldk, wk, e)),
                          rng(v, span(key_rows(d, cu_k), a.ldv, wk, e)), rng(o, qb), rng(dO, qb),
-                         rng(lse, (size_t)d->total_q * d->Hq * 4), rng(cu_q, (size_t)(d->n_seq + 1) * 4),
-                         rng(cu_k, (size_t)(d->n_seq + 1) * 4)};
+                         rng(lse, (size_t)d->total_q * d->Hq * 4), rng(cu_q, ((size_t)d->n_seq + 1) * 4),
+                         rng(cu_k, ((size_t)d->n_seq + 1) * 4)};
     const Range outs[] = {rng(dq, qb), rng(dk, kb), rng(dv, kb), rng(need ? workspace : nullptr, need)};
     for (int i = 0; i < 4; ++i) {
         for (const Range& r : ins)
@@ -776,9 +807,8 @@ gdn_status gdn_attn_bwd(const gdn_attn_desc* d, const void* q, const void* k, co
     int cus;
     if ((st = check_device(&cus)) != GDN_OK) return st;
     a.q = q, a.k = k, a.v = v, a.o = o, a.lse = const_cast<float*>(lse), a.d_o = dO;
-    a.dq = dq, a.dk = dk, a.dv = dv, a.cu_q = cu_q, a.cu_k = cu_k;
+    a.dq = dq, a.dk = dk, a.dv = dv;
     a.delta = static_cast<float*>(workspace);
-    a.k_splits = bwd_splits(d);
     if (a.k_splits > 1) {
         unsigned char* w = static_cast<unsigned char*>(workspace) + round256((size_t)d->total_q * d->Hq * 4);
         a.part_k = reinterpret_cast<float*>(w);
@@ -786,9 +816,11 @@ gdn_status gdn_attn_bwd(const gdn_attn_desc* d, const void* q, const void* k, co
     }
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const bool f32 = d->io_dtype == GDN_F32;
-    st = f32 ? GDN_BY_D(run_bwd, float, a, s) : fast(d) ? attn_bwd_bf16(a, s) : run_bwd<uint16_t, 16>(a, s);
+    st = f32       ? GDN_BY_D(run_bwd, float, a, g.dq, g.dkv, s)
+         : fast(d) ? attn_bwd_bf16(a, g.dq, g.dkv, s)
+                   : run_bwd<uint16_t, 16>(a, g.dq, g.dkv, s);
     if (st != GDN_OK || a.k_splits == 1) return st;
-    return f32 ? GDN_BY_D(run_sum, float, a, s) : GDN_BY_D(run_sum, uint16_t, a, s);
+    return f32 ? GDN_BY_D(run_sum, float, a, g.sum, s) : GDN_BY_D(run_sum, uint16_t, a, g.sum, s);
 }
 
 }  // extern "C"

@@ -204,6 +204,17 @@ inline int64_t places(int64_t rows, int64_t most, int n_seq, int size, bool pack
     return n_seq > 64 || share < all ? share : all;
 }
 
+// One launch over tiles of rows or keys; a launch takes fewer than 2^32 work items.
+struct Grid {
+    unsigned groups;
+    int tiles;                           // of the longest sequence
+};
+inline bool grid_of(int64_t groups, int threads, unsigned* g) {
+    if (groups > (int64_t)(UINT32_MAX / (unsigned)threads)) return false;
+    *g = (unsigned)groups;
+    return true;
+}
+
 // Hidden places and values that are not finite.  A matrix product multiplies a
 // hidden place by an exact 0, which for an infinity or a NaN there gives NaN in
 // rows that must not see it.  Nothing in the loops guards against it: where a
@@ -225,8 +236,11 @@ __device__ __forceinline__ float exp2_f(float x) { return __builtin_amdgcn_exp2f
 __device__ __forceinline__ float log2_f(float x) { return __builtin_amdgcn_logf(x); }
 
 // Kernels in bf16 matrix instructions (gdn_attn_bf16.hip), D in {32, 64, 128}.
-gdn_status attn_fwd_bf16(const AttnArgs& a, hipStream_t s);
-gdn_status attn_bwd_bf16(const AttnArgs& a, hipStream_t s);
+// `rows` is attn_fwd_bf16_rows(): two threads a row; the backward kernels have
+// tiles of kBwdTile rows or keys.
+constexpr int kBwdTile = 128;
+gdn_status attn_fwd_bf16(const AttnArgs& a, int rows, Grid g, hipStream_t s);
+gdn_status attn_bwd_bf16(const AttnArgs& a, Grid dq, Grid dkv, hipStream_t s);
 // Row tile of the forward kernel that these arguments select.
 int attn_fwd_bf16_rows(int max_q, int G, int D);
 

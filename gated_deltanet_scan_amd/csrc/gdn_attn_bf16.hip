@@ -723,30 +723,21 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_kernel(const AttnArgs a) 
         }
 }
 
-bool grid_of(int64_t n, unsigned* g) {
-    if (n > INT32_MAX) return false;
-    *g = (unsigned)n;
-    return true;
-}
-
 template <int D, int NW>
-gdn_status launch_fwd(AttnArgs a, hipStream_t s) {
-    unsigned grid;
-    const int64_t n = places(a.total_q * a.G, (int64_t)a.max_q * a.G, a.n_seq, 32 * NW, a.cu_q, &a.tiles);
-    if (!grid_of(n * a.splits * a.Hk, &grid)) return GDN_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL((attn_fwd_kernel<D, NW>), dim3(grid), dim3(64 * NW), 0, s, a);
+gdn_status launch_fwd(AttnArgs a, Grid g, hipStream_t s) {
+    a.tiles = g.tiles;
+    hipLaunchKernelGGL((attn_fwd_kernel<D, NW>), dim3(g.groups), dim3(64 * NW), 0, s, a);
     return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
-template <int D, int NW>
-gdn_status launch_bwd(AttnArgs a, hipStream_t s) {
-    unsigned grid;
-    int64_t n = places(a.total_q * a.G, (int64_t)a.max_q * a.G, a.n_seq, 32 * NW, a.cu_q, &a.tiles);
-    if (!grid_of(n * a.Hk, &grid)) return GDN_ERR_UNSUPPORTED;
-    if (grid) hipLaunchKernelGGL((attn_dq_kernel<D, NW>), dim3(grid), dim3(64 * NW), 0, s, a);
-    n = places(a.total_k, a.max_k, a.n_seq, 32 * NW, a.cu_k, &a.tiles);
-    if (!grid_of(n * a.Hk * a.k_splits, &grid)) return GDN_ERR_UNSUPPORTED;
-    if (grid) hipLaunchKernelGGL((attn_dkv_kernel<D, NW, (D == 128 ? 32 : 64)>), dim3(grid), dim3(64 * NW), 0, s, a);
+template <int D>
+gdn_status launch_bwd(AttnArgs a, Grid dq, Grid dkv, hipStream_t s) {
+    constexpr int NW = kBwdTile / 32;
+    a.tiles = dq.tiles;
+    if (dq.groups) hipLaunchKernelGGL((attn_dq_kernel<D, NW>), dim3(dq.groups), dim3(64 * NW), 0, s, a);
+    a.tiles = dkv.tiles;
+    if (dkv.groups)
+        hipLaunchKernelGGL((attn_dkv_kernel<D, NW, (D == 128 ? 32 : 64)>), dim3(dkv.groups), dim3(64 * NW), 0, s, a);
     return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
@@ -759,16 +750,16 @@ gdn_status launch_bwd(AttnArgs a, hipStream_t s) {
 // other waves only help to stage (eight requests: 80 us against 101).
 int attn_fwd_bf16_rows(int max_q, int G, int D) { return D == 128 && (int64_t)max_q * G > 256 ? 256 : 128; }
 
-gdn_status attn_fwd_bf16(const AttnArgs& a, hipStream_t s) {
-    if (a.D == 32) return launch_fwd<32, 4>(a, s);
-    if (a.D == 64) return launch_fwd<64, 4>(a, s);
-    return attn_fwd_bf16_rows(a.max_q, a.G, a.D) == 256 ? launch_fwd<128, 8>(a, s) : launch_fwd<128, 4>(a, s);
+gdn_status attn_fwd_bf16(const AttnArgs& a, int rows, Grid g, hipStream_t s) {
+    if (a.D == 32) return launch_fwd<32, 4>(a, g, s);
+    if (a.D == 64) return launch_fwd<64, 4>(a, g, s);
+    return rows == 256 ? launch_fwd<128, 8>(a, g, s) : launch_fwd<128, 4>(a, g, s);
 }
 
-gdn_status attn_bwd_bf16(const AttnArgs& a, hipStream_t s) {
-    if (a.D == 32) return launch_bwd<32, 4>(a, s);
-    if (a.D == 64) return launch_bwd<64, 4>(a, s);
-    return launch_bwd<128, 4>(a, s);
+gdn_status attn_bwd_bf16(const AttnArgs& a, Grid dq, Grid dkv, hipStream_t s) {
+    if (a.D == 32) return launch_bwd<32>(a, dq, dkv, s);
+    if (a.D == 64) return launch_bwd<64>(a, dq, dkv, s);
+    return launch_bwd<128>(a, dq, dkv, s);
 }
 
 }  // namespace gdnattn

@@ -468,7 +468,9 @@ gdn_status gdn_rotary(const gdn_rotary_desc* d, const void* q, const void* k, co
  * (GDN_ERR_INVALID_ARG); D in {16, 32, 64, 128}, Hq D and the strides at most
  * 2^20 (where max_q or max_k is 1, any stride of that tensor: the last tokens of
  * long sequences, the first tokens of a cache's slots), tokens below 2^31, max_q
- * Hq and max_k at most 2^30 (GDN_ERR_UNSUPPORTED).  Tensors and token
+ * Hq and max_k at most 2^30, launches below 2^32 work items (256 or 512 for each
+ * tile of 64 to 256 rows or keys of one sequence and key head; all launches are
+ * checked before the first) (GDN_ERR_UNSUPPORTED).  Tensors and token
  * strides are multiples of 16 bytes, workspace 256 (its size depends on the
  * descriptor alone); outputs are disjoint from the inputs, from each other and
  * from the workspace. */

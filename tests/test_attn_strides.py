@@ -1,5 +1,6 @@
-"""Which views attention takes, on the host: the token stride that the torch
-wrapper passes across the ABI (0 there means packed), and the ABI's own bounds.
+"""Which views and sizes attention takes, on the host: the token stride that the
+torch wrapper passes across the ABI (0 there means packed), and the ABI's own
+bounds.
 """
 import ctypes
 import os
@@ -74,3 +75,24 @@ def both(lib, tq, tk, n, mq, mk, qs=0, ks=0, vs=0, room=0, Hq=4, Hk=2, D=64):
 def test_range_of_strides(lib, which, stride, tokens, most, expect):
     n = tokens // most
     assert both(lib, tokens, tokens, n, most, most, **{which: stride}) == (expect, expect)
+
+
+# ------------------------------------------------------------------ launches
+def test_launches_that_are_too_large_are_refused_first(lib):
+    """2^32 work items in any of a call's launches: refused before the first."""
+    n = 1 << 20
+    assert both(lib, 16 * n, 16 * n, n, 16, 16, Hq=16, Hk=16, D=32) == (UNSUPPORTED, UNSUPPORTED)   # every launch
+    assert both(lib, 16 * n, 0, n, 16, 0, Hq=16, Hk=16, D=32) == (UNSUPPORTED, UNSUPPORTED)         # o, dq
+    assert both(lib, 0, 16 * n, n, 0, 16, Hq=16, Hk=16, D=32) == (OK, UNSUPPORTED)                  # dk and dv alone
+    assert both(lib, 16 * n, 16 * n, n, 16, 16, Hq=15, Hk=15, D=32) == (ALIAS, ALIAS)               # just below
+
+
+@pytest.mark.parametrize("Hq,Hk,D", [(4, 4, 64), (8, 1, 128), (6, 2, 16)])
+@pytest.mark.parametrize("tq,tk", [(1, 20000), (700, 900), (3000, 40)])
+def test_bounds_above_the_tensors_are_the_tensors(lib, Hq, Hk, D, tq, tk):
+    """max_q and max_k only bound the lengths: whatever lies above the number of
+    tokens is the same call, down to its splits and their workspace."""
+    def sizes(mq, mk):
+        d = ctypes.byref(_lib.GdnAttnDesc(tq, tk, 0, 0, 0, 0, 1, Hq, Hk, D, mq, mk, 1, _lib.GDN_BF16, 0, 0.1))
+        return lib.gdn_attn_workspace_size(d), lib.gdn_attn_workspace_size_bwd(d)
+    assert sizes((1 << 30) // Hq, 1 << 30) == sizes(tq, tk)

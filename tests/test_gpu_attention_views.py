@@ -1,12 +1,15 @@
 """Softmax attention on views of one token per sequence that lie far apart: the
 first token of a batched cache's slots, the last token of long sequences.  The
 kernels read the same values as from packed copies, so the results are the same
-bit for bit; where one key is visible, o is that key's v up to rounding.
+bit for bit; where one key is visible, o is that key's v up to rounding.  And
+bounds of the lengths far above them.
 """
+import ctypes
+
 import pytest
 import torch
 
-from gated_deltanet_scan_amd import api, autograd
+from gated_deltanet_scan_amd import _lib, api, autograd
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +60,28 @@ def test_rollout_from_its_first_token():
         k_len = torch.full((2,), n, dtype=torch.int32, device="cuda")
         o2, lse2 = api.attention_fwd(q.contiguous(), kc[:, :66], vc[:, :66], causal=True, k_len=k_len)
         assert torch.equal(o, o2) and torch.equal(lse, lse2), n
+
+
+@pytest.mark.parametrize("dtype,Hq,Hk,D,lens_q,lens_k", [
+    (BF, 8, 1, 128, (1, 1), (5000, 12000)), (F32, 6, 2, 64, (70, 1, 0), (300, 400, 5)), (BF, 4, 2, 32, (900,), (1300,))])
+def test_bounds_far_above_the_lengths(dtype, Hq, Hk, D, lens_q, lens_k):
+    """max_q = 2^30 / Hq and max_k = 2^30 are bounds like any other."""
+    lib, n = _lib.load(), len(lens_q)
+    cu_q, cu_k = [torch.tensor([0] + list(lens), dtype=torch.int32).cumsum(0).int().cuda() for lens in (lens_q, lens_k)]
+    tq, tk = sum(lens_q), sum(lens_k)
+    q, k, v, do = rand((tq, Hq, D), dtype, 1), rand((tk, Hk, D), dtype, 2), rand((tk, Hk, D), dtype, 3), \
+        rand((tq, Hq, D), dtype, 4)
+    o, lse = api.attention_fwd(q, k, v, cu_q=cu_q, cu_k=cu_k, causal=True)
+    ref = [o, lse, *api.attention_bwd(q, k, v, o, lse, do, cu_q=cu_q, cu_k=cu_k, causal=True)]
+    got = [torch.full_like(t, float("nan")) for t in ref]
+    d = ctypes.byref(_lib.GdnAttnDesc(tq, tk, 0, 0, 0, 0, n, Hq, Hk, D, (1 << 30) // Hq, 1 << 30, 1,
+                                      _lib.GDN_BF16 if dtype == BF else _lib.GDN_F32, _lib.GDN_FLAG_ATTN_CAUSAL,
+                                      D ** -0.5))
+    size = max(lib.gdn_attn_workspace_size(d), lib.gdn_attn_workspace_size_bwd(d))
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    P = [t.data_ptr() for t in (q, k, v, do, cu_q, cu_k, ws, *got)]
+    assert lib.gdn_attn_fwd(d, *P[:3], P[4], P[5], None, P[7], P[8], P[6], size, stream) == 0
+    assert lib.gdn_attn_bwd(d, *P[:3], P[7], P[8], P[3], P[4], P[5], *P[9:12], P[6], size, stream) == 0
+    for a, b in zip(got, ref):
+        assert torch.equal(a, b)
