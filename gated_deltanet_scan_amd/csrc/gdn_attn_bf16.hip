@@ -578,10 +578,12 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_kernel(const AttnArgs a) 
     const int w0 = k0 + 32 * wave, key = w0 + r;
     const bool valid = key < z.lk;
     const int rows = z.lq * a.G;
-    // rows below w_first see none of the wave's keys, rows from w_all on see them all
+    // rows below w_first see none of the wave's keys, rows from w_all on see all 32;
+    // no row sees a place past the last key (its score of 0 less a low logarithm
+    // would be a probability of infinity, and send the wave to the tail below)
     const int w_first = w0 < z.lk ? first_query(a, z, w0) * a.G : rows;
-    const int w_all = w0 < z.lk ? first_query(a, z, min(w0 + 32, z.lk) - 1) * a.G : rows;
-    const int from = first_query(a, z, min(key, z.lk - 1)) * a.G;
+    const int w_all = w0 + 32 <= z.lk ? first_query(a, z, w0 + 31) * a.G : rows;
+    const int from = valid ? first_query(a, z, key) * a.G : rows;
     const u32x4 none = {0u, 0u, 0u, 0u};
     u32x4 kf[KS], vf[VL ? 1 : KS];
     f32x16 ak[DB], av[DB];
