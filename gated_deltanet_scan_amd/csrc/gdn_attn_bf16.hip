@@ -676,10 +676,28 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_kernel(const AttnArgs a) 
     const int lane2 = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u)), h2 = lane2 >> 5;
     const int key2 = w0 + (lane2 & 31);
     const bool valid2 = key2 < z.lk;
-    // see finite(); a hidden value that spoils dv spoils dS, and so dk, as well
-    if (a.causal && !finite(ak)) {
+    // see finite(); a hidden value that spoils dv spoils dS, and so dk, as well.
+    // Without a mask only the zeros past the last row are such places, for a key
+    // that is infinite (0 times it is a NaN); the wave's other keys keep their sums.
+    bool again = false;
+    if (a.causal) {
+        again = !finite(ak);
+    } else if (rows % RT) {
+        float t = 0.f;
 #pragma unroll
-        for (int e = 0; e < DB; ++e) ak[e] = av[e] = zero16();
+        for (int e = 0; e < KS; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                t = __builtin_fmaf(__uint_as_float(kf[e][i] << 16), 0.f, t);
+                t = __builtin_fmaf(__uint_as_float(kf[e][i] & 0xffff0000u), 0.f, t);
+            }
+        again = half_sum(t) != 0.f;                           // 0, or NaN
+    }
+    if (__any(again)) {
+        if (again) {
+#pragma unroll
+            for (int e = 0; e < DB; ++e) ak[e] = av[e] = zero16();
+        }
         const int from2 = first_query(a, z, min(key2, z.lk - 1)) * a.G;
         u32x4 vr[KS];
 #pragma unroll
@@ -689,7 +707,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_kernel(const AttnArgs a) 
             const int64_t gr = packed_row(a, z, p.hk, i);
             const uint16_t *qr = q_row(a, z, p.hk, i), *gi = static_cast<const uint16_t*>(a.d_o) + gr * D;
             const float s = dot_row(kf, qr, h2), dp = dot_row(vr, gi, h2), lr = a.lse[gr];
-            if (lr != -INFINITY && valid2 && i >= from2) {
+            if (again && lr != -INFINITY && valid2 && i >= from2) {
                 const float pr = exp2_f(__builtin_fmaf(s, c2, -lr * kLog2e));
                 add_row(av, pr, gi, h2);
                 add_row(ak, pr * (dp - a.delta[gr]), qr, h2);

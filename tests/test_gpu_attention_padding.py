@@ -33,3 +33,24 @@ def test_keys_past_the_end(D, L):
         grads.append((o, lse) + api.attention_bwd(*x, o, lse, do[:, :n].contiguous(), causal=True))
     for name, a, b in zip(("o", "lse", "dq", "dk", "dv"), *grads):
         assert torch.equal(a, b[:, :L]), name
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("lq", [21, 32, 64, 90])
+def test_rows_past_the_end(dtype, D, lq):
+    """A key of -infinity that every query scores -infinity has the probability
+    0, as one of -1e30 has: the same o, lse, dk and dv, its own among them."""
+    g = torch.Generator().manual_seed(D + lq)
+    q, k, v, do = [torch.randn((2, n, h, D), generator=g) for n, h in ((lq, 6), (75, 2), (75, 2), (lq, 6))]
+    q[..., 0] = q[..., 0].abs() + 0.5
+    out = []
+    for hidden in (-1e30, -float("inf")):
+        k[:, 30, :, 0] = hidden
+        x = [t.to(dtype).cuda() for t in (q, k, v, do)]
+        o, lse = api.attention_fwd(*x[:3])
+        out.append((o, lse) + api.attention_bwd(*x[:3], o, lse, x[3])[1:])
+    for name, a, b in zip(("o", "lse", "dk", "dv"), *out):
+        assert torch.equal(a, b), name
+        if name[0] == "d":
+            assert torch.all(b[:, 30] == 0), name
