@@ -99,7 +99,10 @@ class _Rotary(torch.autograd.Function):
 
 def rotary(q, k, pos, *, axes, theta: float = 10000.0, halves: bool = False, inverse: bool = False):
     """Differentiable rotary positions (layouts as for api.rotary); the gradient
-    is the rotation turned back."""
+    is the rotation turned back.  Positions take no gradient: a pos that asks for
+    one is refused while gradients are recorded."""
+    if getattr(pos, "requires_grad", False) and torch.is_grad_enabled():
+        raise ValueError("positions take no gradient: pass pos.detach()")
     return _Rotary.apply(q, k, pos, tuple(axes), theta, halves, inverse)
 
 
