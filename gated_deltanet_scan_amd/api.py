@@ -520,6 +520,8 @@ def _launch(stream, device):
     belongs to the stream.  The current stream of the current device, the usual
     case, needs no context (entering one costs as much as a small kernel)."""
     if stream is not None:
+        if stream.device != device:
+            raise ValueError("stream must be on %s (got %s)" % (device, stream.device))
         return torch.cuda.stream(stream), stream.cuda_stream
     index = device.index
     return (_HERE if index == _current_device() else torch.cuda.device(device)), _raw_stream(index)

@@ -1,10 +1,12 @@
 """Calls that the torch side of the operators around the scan refuses, on the
 host.
 """
+import types
+
 import pytest
 import torch
 
-from gated_deltanet_scan_amd import autograd
+from gated_deltanet_scan_amd import api, autograd
 
 
 def test_positions_take_no_gradient():
@@ -19,3 +21,10 @@ def test_positions_take_no_gradient():
             autograd.rotary(q, None, p, axes=(64,))
     with pytest.raises(ValueError, match="device tensor"):
         autograd.rotary(q, None, pos.detach(), axes=(64,))
+
+
+def test_stream_of_another_device():
+    """A launch there would read the tensors' addresses on the wrong device."""
+    other = types.SimpleNamespace(device=torch.device("cuda:1"), cuda_stream=0)
+    with pytest.raises(ValueError, match="stream must be on cuda:0"):
+        api._launch(other, torch.device("cuda:0"))
