@@ -570,8 +570,13 @@ int fwd_rows(const gdn_attn_desc* d) {
 
 // Keys of a split of the key axis; max_k or more: not split.  Split where the
 // row tiles alone would leave compute units idle: as many splits as fill the
-// 256 in one round (with two waves a SIMD; 880 queries against 19360 keys, 16
-// heads of 128: 156 us, with twice as many 171).  A decode step (a few rows a key
+// 256 in one round with two waves a SIMD (880 queries against 19360 keys, 16
+// heads of 128: 156 us, with twice as many 171).  That is what the D = 128
+// kernels hold; for narrower heads, whose registers would let three (D = 64) or
+// four waves in, the same count stands and was not measured.  Nor does the rule
+// look at the lengths: 540 tiles of a packed batch are not split, and its
+// longest sequence's walk (4096 keys, 131 us) is the kernel's whole time, where
+// its work spread evenly would take about 92.  A decode step (a few rows a key
 // head) is cut eight times finer, because the lengths of its caches differ and
 // short work spreads evenly; a split's fp32 partial result is then small
 // against its keys, of which it takes 512 at least (128 at the fp32 rate).

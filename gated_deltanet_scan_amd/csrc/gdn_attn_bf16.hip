@@ -175,9 +175,12 @@ struct Tile {
 // pipes of a SIMD work at once.  K of a tile is therefore in LDS half a tile
 // before V of it.
 //
-// Measured: frame-causal clip of 18480 tokens, 16 heads of 128: 1.40 ms, 1050
-// TFLOP/s, 76% of a large library product's rate; the matrix pipes are busy
-// half the time, two waves a SIMD leave the rest to dependences within a step.
+// Measured: frame-causal clip of 18480 tokens, 16 heads of 128: 2.88 million
+// cycles, 1.39 to 1.48 ms a call at the 2.07 to 1.95 GHz that cards hold with
+// calls in a row (the first calls after a pause run at 1.6 to 1.8 GHz), which is
+// 1060 to 1000 TFLOP/s; the matrix pipes are busy half the time, two waves a SIMD
+// leave the rest to dependences within a step.  Sequences of unequal lengths leave
+// waves idle as well: the longest walk, not the sum of them, sets the time.
 // 4096 x 4096, 16 heads, no mask: 908 TFLOP/s at D = 128 (256 workgroups, one
 // round), 655 at 64 and 473 at 32, where exponentials (16 a lane and step
 // whatever D is) bound it.
@@ -246,6 +249,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_fwd_kernel(const AttnArgs a) 
             l *= al;
 #pragma unroll
             for (int e = 0; e < DB; ++e) acc[e] *= al;
+            // the step still pending, rounded to bf16 once more: in fp32 it would take
+            // 8 registers more, and a row comes here a few times at most
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -268,6 +273,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_fwd_kernel(const AttnArgs a) 
             sum += cur[i];
         }
         l += sum;                                             // this lane's keys; joined at the end
+        // P in bf16, which the products take: off by half a step (2^-8 at most,
+        // 1.7e-3 in the mean square), as much as o's own rounding
         now[0] = pack8(cur, 0);
         now[1] = pack8(cur, 8);
         __builtin_amdgcn_s_setprio(0);
@@ -354,11 +361,16 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_fwd_kernel(const AttnArgs a) 
 // dq, and <d_o, o> for the dk/dv kernel.  Query rows as columns, as in the
 // forward kernel; the key tile is read both ways (S^T = K Q^T, dQ^T += K^T dS^T).
 //
-// <d_o, o> = sum_j p_j dp_j.  From the rounded o it is off by 2^-9 |d_o| |o|,
-// which matters where a row sees few keys and o is as large as v (a causal
+// dS is rounded to bf16 for its products, here and in the dk/dv kernel (there P
+// as well), half a step each.
+//
+// <d_o, o> = sum_j p_j dp_j.  From the rounded o it is off by 2^-8 |d_o| |o| at
+// most, which matters where a row sees few keys and o is as large as v (a causal
 // sequence of 300 tokens: dq off by 2.40e-3 with it and 2.26e-3 without, of
 // which 1.68e-3 are dq's own rounding).  Where the workgroup's rows see at most
-// kExactKeys keys the sum is formed in fp32 by a first walk over them.
+// kExactKeys keys the sum is formed in fp32 by a first walk over them.  That
+// makes 10 D flops of the 6 D a pair there: 8192 packed sequences of 1 to 299
+// tokens, 8/2 heads of 64, backward 3452 us with it and 3132 without.
 //
 // Measured: 4096 x 4096, 16 heads of 128: 227 us, 910 TFLOP/s of 6 D flops a
 // pair (783 at D = 64, 603 at 32); two waves a SIMD wait on the products of one

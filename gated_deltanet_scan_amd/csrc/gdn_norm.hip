@@ -425,7 +425,9 @@ __global__ __launch_bounds__(kThreads) void norm_wide_dw_kernel(const NormArgs a
 }
 
 // dw[c] = sum over the groups' partial rows, 64 columns a workgroup; its 16
-// waves take every sixteenth row and add up through LDS in order.  Bound by the
+// waves take every sixteenth row and add up through LDS in order.  All of it in
+// fp32: sums of a few dozen to a few hundred terms one after the other, 1.4e-7 off
+// in the Frobenius norm at 1777 rows where 64-bit sums are 0.8e-7.  Bound by the
 // latency of those rows: 1024 of 2 x 2048 (16 MiB, in the caches) in 10 us.
 constexpr int kColWaves = 16;
 template <typename W>

@@ -38,8 +38,12 @@ struct RotArgs {
 };
 
 // Turns per position of pair j, theta^(-2i/d) / (2 pi), and its axis: a power
-// by squaring, off by at most 14 half steps of 2^-53 (a table in the kernel's
-// arguments made them 1.3 KB and the launch 3 us longer).
+// by squaring.  Each squaring doubles what its base is off by, so step^i is off
+// by about 2 i half steps of 2^-53 (the rounded step's i, and i of the squarings
+// and products), 256 at most.  The angle is off by that share of itself and falls
+// faster with i: at theta = 10^4 and positions up to 2^26 by less than the half
+// step of 2^-26 turns that fp32 costs next.  (A table in the kernel's arguments
+// made them 1.3 KB and the launch 3 us longer.)
 __device__ __forceinline__ double turns_of(const RotArgs& a, int j, int& axis) {
     axis = 0;
 #pragma unroll
