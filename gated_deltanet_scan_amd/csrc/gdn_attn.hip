@@ -575,7 +575,7 @@ int fwd_rows(const gdn_attn_desc* d) {
 // kernels hold; for narrower heads, whose registers would let three (D = 64) or
 // four waves in, the same count stands and was not measured.  Nor does the rule
 // look at the lengths: 540 tiles of a packed batch are not split, and its
-// longest sequence's walk (4096 keys, 131 us) is the kernel's whole time, where
+// longest sequence's walk (4096 keys, 130 us) is the kernel's whole time, where
 // its work spread evenly would take about 92.  A decode step (a few rows a key
 // head) is cut eight times finer, because the lengths of its caches differ and
 // short work spreads evenly; a split's fp32 partial result is then small
