@@ -795,7 +795,9 @@ def attention_fwd(q, k, v, *, causal: bool = False, causal_block: Optional[int] 
     q: [B, L, Hq, D], k and v: [B, Lk, Hk, D] (or [B, F, N, H, D] frames, or
     packed [T, H, D] with cu_q), bf16 or fp32, Hq a multiple of Hk, D in {16,
     32, 64, 128}; heads packed, tokens evenly apart (a slice of a fused
-    projection, or the first tokens k[:, :n] of a cache's slots, will do).  causal=True: the queries are the last positions of
+    projection, the first tokens k[:, :n] of a cache's slots, or single tokens
+    q[:, -1:] of long sequences will do; broadcast views will not).
+    causal=True: the queries are the last positions of
     their sequence and see the keys up to the end of their own block of
     causal_block positions (default: a frame's N tokens for [B, F, N, H, D],
     else 1).  cu_q, cu_k (default cu_q): int32 [n_seq + 1] offsets of packed

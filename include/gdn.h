@@ -456,7 +456,8 @@ gdn_status gdn_rotary(const gdn_rotary_desc* d, const void* q, const void* k, co
  * values that no query of a sequence may see, past k_len included, are not used,
  * whatever they hold.  An infinity or a NaN reaches the rows that see it and no
  * others (a masked place is left out, not multiplied by 0), in the gradients too;
- * row tiles that hold such a value under a mask are computed many times slower.
+ * row tiles that hold such a value under a mask are computed many times slower,
+ * and so are dk and dv of an infinite key.
  *
  * gdn_attn_bwd takes the forward call's q, k, v, o and lse and dO = dL/do, and
  * writes dq, dk and dv (sums over the query heads that share a key head
