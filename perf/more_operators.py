@@ -31,11 +31,11 @@ def listed():
         # fp32 activations of a width that fills neither groups nor vectors
         dict(name="quant_odd_f32", op="quant", rows=1777, C=1001, dtype="f32"),
         # query, key and value projections of seven requests, a token each
-        dict(name="matmul_tokens", op="matmul", M=7, K=2048, N=6144, parts=3, dtype="bf16"),
+        dict(name="matmul_tokens", op="matmul", M=7, K=2048, N=6144, parts=3),
         # the output projection of a streamed frame
-        dict(name="matmul_frame", op="matmul", M=880, K=2048, N=2048, parts=1, dtype="bf16"),
+        dict(name="matmul_frame", op="matmul", M=880, K=2048, N=2048, parts=1),
         # query, key and value projections of a minute
-        dict(name="matmul_minute", op="matmul", M=121 * 880, K=2048, N=6144, parts=3, dtype="bf16"),
+        dict(name="matmul_minute", op="matmul", M=121 * 880, K=2048, N=6144, parts=3),
         # one token for each of eight requests into 4-bit caches, and the caches read back
         dict(name="cache_tokens_fp4", op="cache", lens_new="1,1,1,1,1,1,1,1", lens_k="40,511,1,1000,64,129,777,2",
              room=1024, H=8, D=128, fmt="fp4", dtype="bf16"),
@@ -73,11 +73,10 @@ def _draw_matmul(rng):
     K = rng.choice([16 * _log(rng, 1, 512), 128 * rng.randint(1, 64)])
     parts = rng.choice([1, 1, 2, 3])
     N = parts * rng.choice([_log(rng, 1, 8192) if parts == 1 else 16 * _log(rng, 1, 256), 128 * rng.randint(1, 32)])
-    dtype = rng.choice(["bf16", "bf16", "f32"])
     # no more than the listed minute: its products, and its output
-    most = min((121 * 880 * 2048 * 6144) // (K * N), (121 * 880 * 6144) // N // (1 if dtype == "bf16" else 2))
+    most = min((121 * 880 * 2048 * 6144) // (K * N), (121 * 880 * 6144) // N)
     M = _log(rng, 1, max(1, min(121 * 880, most)))
-    return dict(op="matmul", M=M, K=K, N=N, parts=parts, dtype=dtype)
+    return dict(op="matmul", M=M, K=K, N=N, parts=parts)
 
 
 def _draw_cache(rng):
@@ -231,7 +230,7 @@ def _matmul_plain(s):
     K, N = s["K"], s["N"]
     x = (s["x"].float() * s["xs"].repeat_interleave(GROUP, 1)[:, :K])
     w = s["w"].float() * s["ws"].repeat_interleave(GROUP, 0)[:N].repeat_interleave(GROUP, 1)[:, :K]
-    y = (x @ w.t()).to(DTYPES[s["dtype"]])
+    y = (x @ w.t()).to(torch.bfloat16)
     if s["parts"] > 1:
         y = y.reshape(s["M"], s["parts"], N // s["parts"]).transpose(0, 1).contiguous()
     return {"y": y}
@@ -344,7 +343,7 @@ def _norm_own(s):
 
 def _matmul_own(s):
     from gated_deltanet_scan_amd import api
-    return {"y": api.matmul_fp8(s["x"], s["xs"], s["w"], s["ws"], parts=s["parts"], out_dtype=DTYPES[s["dtype"]])}
+    return {"y": api.matmul_fp8(s["x"], s["xs"], s["w"], s["ws"], parts=s["parts"])}
 
 
 def _cache_own(s):
@@ -398,7 +397,7 @@ def work(case):
     if op == "matmul":
         M, K, N = case["M"], case["K"], case["N"]
         kb, nb = (K + GROUP - 1) // GROUP, (N + GROUP - 1) // GROUP
-        return {"bytes": M * K + N * K + 4 * kb * (M + nb) + M * N * e, "flops": 2 * M * N * K}
+        return {"bytes": M * K + N * K + 4 * kb * (M + nb) + M * N * 2, "flops": 2 * M * N * K}
     H, D = _heads(case), case["D"]
     token = H * (D // (2 if case["fmt"] == "fp4" else 1) + D // MX)       # bytes of a token's codes and scales
     lk = _ints(case["lens_k"])
