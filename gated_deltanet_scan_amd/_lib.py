@@ -56,6 +56,17 @@ class GdnAttnDesc(ctypes.Structure):
                 ("flags", ctypes.c_uint32), ("scale", ctypes.c_float)]
 
 
+class GdnCacheDesc(ctypes.Structure):
+    _fields_ = [("total_new", ctypes.c_int64), ("total_k", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("k_room", ctypes.c_int64), ("n_seq", ctypes.c_int32),
+                ("H", ctypes.c_int32), ("D", ctypes.c_int32), ("max_new", ctypes.c_int32), ("max_k", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("cache_dtype", ctypes.c_int32)]
+
+
+class GdnMatmulDesc(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("parts", ctypes.c_int32)]
+
+
 class GdnError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -136,6 +147,21 @@ def load():
     lib.gdn_attn_fwd.restype = ctypes.c_int
     lib.gdn_attn_bwd.argtypes = [ap, vp, vp, vp, vp, fp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.gdn_attn_bwd.restype = ctypes.c_int
+    for name in ("gdn_attn_fwd_fp8", "gdn_attn_fwd_fp4"):
+        fn = getattr(lib, name)
+        fn.argtypes = [ap, vp, vp, vp, vp, vp, vp, vp, vp, vp, fp, vp, sz, vp]
+        fn.restype = ctypes.c_int
+    cp = ctypes.POINTER(GdnCacheDesc)
+    lib.gdn_cache_write.argtypes = [cp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.gdn_cache_write.restype = ctypes.c_int
+    lib.gdn_cache_read.argtypes = [cp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.gdn_cache_read.restype = ctypes.c_int
+    lib.gdn_rms_norm_fwd_fp8.argtypes = [np_, vp, vp, vp, vp, vp, fp, vp]
+    lib.gdn_rms_norm_fwd_fp8.restype = ctypes.c_int
+    lib.gdn_quantize_fp8.argtypes = [np_, vp, vp, fp, vp]
+    lib.gdn_quantize_fp8.restype = ctypes.c_int
+    lib.gdn_matmul_fp8.argtypes = [ctypes.POINTER(GdnMatmulDesc), vp, fp, vp, fp, vp, vp]
+    lib.gdn_matmul_fp8.restype = ctypes.c_int
     lib.gdn_status_string.argtypes = [ctypes.c_int]
     lib.gdn_status_string.restype = ctypes.c_char_p
     lib.gdn_version.argtypes = []

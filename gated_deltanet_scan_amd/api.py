@@ -859,3 +859,369 @@ def attention_bwd(q, k, v, o, lse, dO, *, causal: bool = False, causal_block: Op
     if st != 0:
         raise GdnError(st, "gdn_attn_bwd")
     return dq, dk, dv
+
+
+# ------------------------------------------------------------------ 8-bit projections
+FP8_GROUP = 128   # columns of an activation's scale, rows and columns of a weight's
+
+
+def _fp8_out(x, y, y_scale):
+    """Checks of the outputs of rms_norm_fwd_fp8 and quantize_fp8: the scales' shape."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if x.dim() < 1:
+        raise ValueError("x must be [..., C]")
+    _check(x, "x", x.dtype, x.shape)
+    scales = x.shape[:-1] + (-(-x.shape[-1] // FP8_GROUP),)
+    if y is not None:
+        _check(y, "y", torch.float8_e4m3fn, x.shape)
+    if y_scale is not None:
+        _check(y_scale, "y_scale", torch.float32, scales)
+    return scales
+
+
+def rms_norm_fwd_fp8(x, weight=None, residual=None, *, eps: float = 1e-6, y=None, y_scale=None, total=None,
+                     stream=None):
+    """Root-mean-square norm over the last axis with an 8-bit output, for the
+    projections of matmul_fp8: y = t * (<t^2> + eps)^(-1/2) * weight, t = x + residual.
+
+    x: [..., C] bf16 or fp32; weight: [C] in x's dtype or fp32, or None; residual:
+    like x, or None.  Returns (y, y_scale, total): y float8_e4m3fn like x, y_scale
+    [..., ceil(C / 128)] fp32, one for each group of 128 columns (a value is its code
+    times its scale), and total = t in x's dtype (None without a residual), which may
+    be given as x or residual itself.
+    """
+    scales = _fp8_out(x, y, y_scale)
+    desc = _norm_desc(x, weight, None, eps)
+    if residual is not None:
+        _check(residual, "residual", x.dtype, x.shape)
+    if total is not None:
+        if residual is None:
+            raise ValueError("total needs a residual")
+        _check(total, "total", x.dtype, x.shape)
+    _same_device(x, weight=weight, residual=residual, y=y, y_scale=y_scale, total=total)
+    where, handle = _launch(stream, x.device)
+    with where:   # allocations belong to the launch stream
+        if y is None:
+            y = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+        if y_scale is None:
+            y_scale = torch.empty(scales, dtype=torch.float32, device=x.device)
+        if total is None and residual is not None:
+            total = torch.empty_like(x)
+        st = _lib.load().gdn_rms_norm_fwd_fp8(ctypes.byref(desc), _ptr(x), _ptr(residual), _ptr(weight), _ptr(total),
+                                              _ptr(y), _ptr(y_scale), handle)
+    if st != 0:
+        raise GdnError(st, "gdn_rms_norm_fwd_fp8")
+    return y, y_scale, total
+
+
+def quantize_fp8(x, *, y=None, y_scale=None, stream=None):
+    """x [..., C] (bf16 or fp32) in 8 bits with a scale for each group of 128
+    columns, as rms_norm_fwd_fp8 gives its output: (y, y_scale)."""
+    scales = _fp8_out(x, y, y_scale)
+    desc = _norm_desc(x, None, None, 1.0)
+    _same_device(x, y=y, y_scale=y_scale)
+    where, handle = _launch(stream, x.device)
+    with where:   # allocations belong to the launch stream
+        if y is None:
+            y = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+        if y_scale is None:
+            y_scale = torch.empty(scales, dtype=torch.float32, device=x.device)
+        st = _lib.load().gdn_quantize_fp8(ctypes.byref(desc), _ptr(x), _ptr(y), _ptr(y_scale), handle)
+    if st != 0:
+        raise GdnError(st, "gdn_quantize_fp8")
+    return y, y_scale
+
+
+def matmul_fp8(x, x_scale, w, w_scale, *, parts: int = 1, y=None, stream=None):
+    """Product of 8-bit floats with fp32 scales: y = x w^T.
+
+    x: [..., K] float8_e4m3fn with x_scale [..., ceil(K / 128)] fp32
+    (rms_norm_fwd_fp8, quantize_fp8); w: [N, K] float8_e4m3fn, output-major, with
+    w_scale [ceil(N / 128), ceil(K / 128)] fp32 (inputs.to_fp8_weight); K a multiple
+    of 16.  Returns y [..., N] bf16, or with parts > 1 [parts, ..., N / parts].
+    """
+    for name, t in (("x", x), ("w", w)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a torch.Tensor" % name)
+    if x.dim() < 1 or w.dim() != 2:
+        raise ValueError("x must be [..., K] and w [N, K]")
+    N, K = w.shape
+    lead = x.shape[:-1]
+    parts = int(parts)
+    if parts < 1 or N % parts:
+        raise ValueError("parts must divide N = %d (got %d)" % (N, parts))
+    _check(x, "x", torch.float8_e4m3fn, lead + (K,))
+    _check(w, "w", torch.float8_e4m3fn, (N, K))
+    kb = -(-K // FP8_GROUP)
+    _check(x_scale, "x_scale", torch.float32, lead + (kb,))
+    _check(w_scale, "w_scale", torch.float32, (-(-N // FP8_GROUP), kb))
+    shape = lead + (N,) if parts == 1 else (parts,) + lead + (N // parts,)
+    if y is not None:
+        _check(y, "y", torch.bfloat16, shape)
+    _same_device(x, x_scale=x_scale, w=w, w_scale=w_scale, y=y)
+    desc = _lib.GdnMatmulDesc(lead.numel(), N, K, parts)
+    where, handle = _launch(stream, x.device)
+    with where:   # allocations belong to the launch stream
+        if y is None:
+            y = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+        st = _lib.load().gdn_matmul_fp8(ctypes.byref(desc), _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(y),
+                                        handle)
+    if st != 0:
+        raise GdnError(st, "gdn_matmul_fp8")
+    return y
+
+
+# ------------------------------------------------------------------ block-scaled caches
+MX_BLOCK = 32     # features of a cache's scale
+
+
+def cache_empty(*lead: int, H: int, D: int, fp4: bool, device="cuda"):
+    """A cache of zeros for [*lead] tokens (slots and places, or packed tokens) of H
+    heads of D features: (k, k_scale, v, v_scale), MXFP4 (uint8 [*lead, H, D/2]) or
+    MXFP8 (float8_e4m3fn [*lead, H, D]) with E8M0 scales uint8 [*lead, H, D/32]."""
+    if D % MX_BLOCK:
+        raise ValueError("D must be a multiple of %d (got %d)" % (MX_BLOCK, D))
+    out = []
+    for _ in range(2):
+        codes = torch.zeros(lead + (H, D // 2 if fp4 else D), dtype=torch.uint8, device=device)
+        out += [codes if fp4 else codes.view(torch.float8_e4m3fn),
+                torch.zeros(lead + (H, D // MX_BLOCK), dtype=torch.uint8, device=device)]
+    return tuple(out)
+
+
+def _packed_tokens(t, name):
+    """Places from one slot of t [..., H, X] to the next, 0: packed."""
+    if t.is_contiguous() or t.numel() == 0:
+        return 0
+    ld, room = _token_strides(t, name)
+    row = t.shape[-2] * t.shape[-1]
+    if ld != row and t.shape[1:-2].numel() == 1 and ld % row == 0:
+        return ld // row                      # slots of one place
+    if ld != row:
+        raise ValueError("%s must have packed tokens" % name)
+    return room
+
+
+def _cache_args(k, k_scale, v, v_scale, fp4):
+    """Checks of a cache: (places' shape, H, D, places between slots or 0)."""
+    for name, t in (("k", k), ("k_scale", k_scale), ("v", v), ("v_scale", v_scale)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a torch.Tensor" % name)
+    if not 3 <= k.dim() <= 5:
+        raise ValueError("k must be [T, H, D], [B, L, H, D] or [B, F, N, H, D] (got %s)" % (tuple(k.shape),))
+    H, D = k.shape[-2], k.shape[-1] * (2 if fp4 else 1)
+    if D % MX_BLOCK:
+        raise ValueError("a cache's head size must be a multiple of %d (got %d)" % (MX_BLOCK, D))
+    codes, scales = k.shape, k.shape[:-1] + (D // MX_BLOCK,)
+    dtype = torch.uint8 if fp4 else torch.float8_e4m3fn
+    for name, t, dt, shape in (("k", k, dtype, codes), ("k_scale", k_scale, torch.uint8, scales), ("v", v, dtype, codes),
+                               ("v_scale", v_scale, torch.uint8, scales)):
+        if not t.is_cuda:
+            raise ValueError("%s must be a device tensor (got %s)" % (name, t.device))
+        if t.dtype != dt:
+            raise TypeError("%s must be %s (got %s)" % (name, dt, t.dtype))
+        if t.shape != shape:
+            raise ValueError("%s must have shape %s (got %s)" % (name, tuple(shape), tuple(t.shape)))
+    _same_device(k, k_scale=k_scale, v=v, v_scale=v_scale)
+    rooms = [_packed_tokens(t, n) for n, t in (("k", k), ("k_scale", k_scale), ("v", v), ("v_scale", v_scale))]
+    if any(r != rooms[0] for r in rooms):
+        raise ValueError("the slots of a cache's tensors must lie equally far apart")
+    return codes[:-2], H, D, rooms[0]
+
+
+def _is_fp4(k):
+    if not isinstance(k, torch.Tensor) or k.dtype not in (torch.uint8, torch.float8_e4m3fn):
+        raise TypeError("a cache's k must be uint8 (MXFP4) or float8_e4m3fn (MXFP8)")
+    return k.dtype == torch.uint8
+
+
+def cache_write(k, v, k_cache, k_scale, v_cache, v_scale, *, k_len=None, cu_new=None, cu_k=None, max_new=None,
+                max_k=None, stream=None) -> None:
+    """Quantises new keys and values into an MXFP4 or MXFP8 cache (cache_empty), in place.
+
+    k, v: [B, n, H, D] (or [B, F, N, H, D], or packed [T, H, D] with cu_new), bf16 or
+    fp32, heads packed and tokens evenly apart; the cache [B, L, H, ...] (or a slice
+    k_cache[:, :n] of longer slots, or packed with cu_k, default cu_new).  The new
+    tokens become the last of their sequence's k_len[s] positions (int32 [n_seq];
+    None: all L), as the queries of attention_fwd_fp4 and _fp8 with the same k_len
+    lie; tokens that fall outside the slot are dropped.
+    """
+    fp4 = _is_fp4(k_cache)
+    lead, H, D, room = _cache_args(k_cache, k_scale, v_cache, v_scale, fp4)
+    for name, t in (("k", k), ("v", v)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a torch.Tensor" % name)
+        if not t.is_cuda:
+            raise ValueError("%s must be a device tensor (got %s)" % (name, t.device))
+    if not 3 <= k.dim() <= 5 or v.shape != k.shape or k.shape[-2:] != (H, D):
+        raise ValueError("k and v must be [..., %d, %d], alike (got %s, %s)" % (H, D, tuple(k.shape), tuple(v.shape)))
+    if v.dtype != k.dtype:
+        raise TypeError("v must be %s (got %s)" % (k.dtype, v.dtype))
+    io = _io(k.dtype, "k and v")
+    (ldk, rk), (ldv, rv) = _token_strides(k, "k"), _token_strides(v, "v")
+    if rk or rv:
+        raise ValueError("k and v must have packed heads and evenly spaced tokens")
+    if (k.dim() == 3) != (len(lead) == 1):
+        raise ValueError("packed k [T, H, D] go with a packed cache")
+    if k.dim() == 3:
+        if cu_new is None:
+            raise ValueError("packed k [T, H, D] needs cu_new")
+        cu_k = cu_new if cu_k is None else cu_k
+        n_seq = cu_new.numel() - 1
+        if n_seq < 0:
+            raise ValueError("cu_new must hold n_seq + 1 offsets")
+        _check(cu_new, "cu_new", torch.int32, (n_seq + 1,))
+        _check(cu_k, "cu_k", torch.int32, (n_seq + 1,))
+        tn, tk = k.shape[0], lead[0]
+        max_new = tn if max_new is None else min(int(max_new), tn)
+        max_k = tk if max_k is None else min(int(max_k), tk)
+    else:
+        if cu_new is not None or cu_k is not None or max_new is not None or max_k is not None:
+            raise ValueError("cu_new, cu_k, max_new and max_k belong to packed k [T, H, D]")
+        n_seq = k.shape[0]
+        if lead[0] != n_seq:
+            raise ValueError("k and the cache must have the same batch size")
+        max_new, max_k = k.shape[1:-2].numel(), lead[1:].numel()
+        tn, tk = n_seq * max_new, n_seq * max_k
+    if k_len is not None:
+        _check(k_len, "k_len", torch.int32, (n_seq,))
+    _same_device(k, v=v, k_cache=k_cache, cu_new=cu_new, cu_k=cu_k, k_len=k_len)
+    desc = _lib.GdnCacheDesc(tn, tk, ldk, ldv, room, n_seq, H, D, max_new, max_k, io,
+                             _lib.GDN_FP4_E2M1 if fp4 else _lib.GDN_FP8_E4M3)
+    where, handle = _launch(stream, k.device)
+    with where:
+        st = _lib.load().gdn_cache_write(ctypes.byref(desc), _ptr(k), _ptr(v), _ptr(cu_new), _ptr(cu_k), _ptr(k_len),
+                                         _ptr(k_cache), _ptr(k_scale), _ptr(v_cache), _ptr(v_scale), handle)
+    if st != 0:
+        raise GdnError(st, "gdn_cache_write")
+
+
+def cache_read(k_cache, k_scale, v_cache, v_scale, *, dtype: torch.dtype = torch.bfloat16, k_len=None, cu_k=None,
+               max_k=None, k=None, v=None, stream=None):
+    """The values that a cache holds: (k, v) [..., H, D] in dtype (bf16 or fp32),
+    contiguous.  Only the first k_len[s] places of each slot (None: all) are written;
+    the others of k and v are left as they are.  Slots as for cache_write."""
+    fp4 = _is_fp4(k_cache)
+    lead, H, D, room = _cache_args(k_cache, k_scale, v_cache, v_scale, fp4)
+    dtype = k.dtype if k is not None else v.dtype if v is not None else dtype
+    io = _io(dtype, "k and v")
+    shape = lead + (H, D)
+    for name, t in (("k", k), ("v", v)):
+        if t is not None:
+            _check(t, name, dtype, shape)
+    if len(lead) == 1:
+        if cu_k is None:
+            raise ValueError("a packed cache needs cu_k")
+        n_seq, tk = cu_k.numel() - 1, lead[0]
+        if n_seq < 0:
+            raise ValueError("cu_k must hold n_seq + 1 offsets")
+        _check(cu_k, "cu_k", torch.int32, (n_seq + 1,))
+        max_k = tk if max_k is None else min(int(max_k), tk)
+    else:
+        if cu_k is not None or max_k is not None:
+            raise ValueError("cu_k and max_k belong to a packed cache")
+        n_seq, max_k = lead[0], lead[1:].numel()
+        tk = n_seq * max_k
+    if k_len is not None:
+        _check(k_len, "k_len", torch.int32, (n_seq,))
+    _same_device(k_cache, cu_k=cu_k, k_len=k_len, k=k, v=v)
+    desc = _lib.GdnCacheDesc(0, tk, 0, 0, room, n_seq, H, D, 0, max_k, io,
+                             _lib.GDN_FP4_E2M1 if fp4 else _lib.GDN_FP8_E4M3)
+    where, handle = _launch(stream, k_cache.device)
+    with where:   # allocations belong to the launch stream
+        k = torch.empty(shape, dtype=dtype, device=k_cache.device) if k is None else k
+        v = torch.empty(shape, dtype=dtype, device=k_cache.device) if v is None else v
+        st = _lib.load().gdn_cache_read(ctypes.byref(desc), _ptr(k_cache), _ptr(k_scale), _ptr(v_cache), _ptr(v_scale),
+                                        _ptr(cu_k), _ptr(k_len), _ptr(k), _ptr(v), handle)
+    if st != 0:
+        raise GdnError(st, "gdn_cache_read")
+    return k, v
+
+
+def _attention_mx(fp4, q, k, k_scale, v, v_scale, causal, causal_block, scale, cu_q, cu_k, max_q, max_k, k_len, o, lse,
+                  return_lse, workspace, stream):
+    lead, Hk, D, room = _cache_args(k, k_scale, v, v_scale, fp4)
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    if not q.is_cuda:
+        raise ValueError("q must be a device tensor (got %s)" % q.device)
+    if q.dtype != torch.bfloat16:
+        raise TypeError("q must be %s (got %s)" % (torch.bfloat16, q.dtype))
+    if not 3 <= q.dim() <= 5 or q.shape[-1] != D or (q.dim() == 3) != (len(lead) == 1):
+        raise ValueError("q must be [B, L, H, %d] or [B, F, N, H, %d], or packed [T, H, %d] over a packed cache (got %s)"
+                         % (D, D, D, tuple(q.shape)))
+    Hq = q.shape[-2]
+    ldq, rq = (0, 0) if q.is_contiguous() else _token_strides(q, "q")
+    if rq:
+        raise ValueError("q must have packed heads and evenly spaced tokens")
+    if q.dim() == 3:
+        if cu_q is None:
+            raise ValueError("packed q [T, H, D] needs cu_q")
+        cu_k = cu_q if cu_k is None else cu_k
+        n_seq = cu_q.numel() - 1
+        if n_seq < 0:
+            raise ValueError("cu_q must hold n_seq + 1 offsets")
+        _check(cu_q, "cu_q", torch.int32, (n_seq + 1,))
+        _check(cu_k, "cu_k", torch.int32, (n_seq + 1,))
+        tq, tk = q.shape[0], lead[0]
+        max_q = tq if max_q is None else min(int(max_q), tq)
+        max_k = tk if max_k is None else min(int(max_k), tk)
+    else:
+        if cu_q is not None or cu_k is not None or max_q is not None or max_k is not None:
+            raise ValueError("cu_q, cu_k, max_q and max_k belong to packed q [T, H, D]")
+        n_seq = q.shape[0]
+        if lead[0] != n_seq:
+            raise ValueError("q and the cache must have the same batch size")
+        max_q, max_k = q.shape[1:-2].numel(), lead[1:].numel()
+        tq, tk = n_seq * max_q, n_seq * max_k
+    if causal_block is None:
+        causal_block = q.shape[2] if q.dim() == 5 else 1
+    if k_len is not None:
+        _check(k_len, "k_len", torch.int32, (n_seq,))
+    if o is not None:
+        _check(o, "o", q.dtype, q.shape)
+    if lse is not None:
+        _check(lse, "lse", torch.float32, q.shape[:-1])
+    _check_workspace(workspace, q.device)
+    _same_device(q, k=k, cu_q=cu_q, cu_k=cu_k, k_len=k_len, o=o, lse=lse)
+    desc = _lib.GdnAttnDesc(tq, tk, ldq, 0, 0, room, n_seq, Hq, Hk, D, max_q, max_k, min(int(causal_block), 2 ** 31 - 1),
+                            _lib.GDN_FP4_E2M1 if fp4 else _lib.GDN_FP8_E4M3,
+                            _lib.GDN_FLAG_ATTN_CAUSAL if causal else 0, D ** -0.5 if scale is None else scale)
+    lib = _lib.load()
+    fn = lib.gdn_attn_fwd_fp4 if fp4 else lib.gdn_attn_fwd_fp8
+    where, handle = _launch(stream, q.device)
+    with where:   # allocations belong to the launch stream
+        if o is None:
+            o = _like(q)
+        if lse is None and return_lse:
+            lse = q.new_empty(q.shape[:-1], dtype=torch.float32)
+        workspace = _workspace(workspace, int(lib.gdn_attn_workspace_size(ctypes.byref(desc))), q.device)
+        st = fn(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(k_scale), _ptr(v), _ptr(v_scale), _ptr(cu_q), _ptr(cu_k),
+                _ptr(k_len), _ptr(o), _ptr(lse), _ptr(workspace), _ws_bytes(workspace), handle)
+    if st != 0:
+        raise GdnError(st, "gdn_attn_fwd_fp4" if fp4 else "gdn_attn_fwd_fp8")
+    return o, lse
+
+
+def attention_fwd_fp4(q, k, k_scale, v, v_scale, *, causal: bool = False, causal_block: Optional[int] = None,
+                      scale=None, cu_q=None, cu_k=None, max_q=None, max_k=None, k_len=None, o=None, lse=None,
+                      return_lse: bool = True, workspace=None, stream=None):
+    """attention_fwd over keys and values in MXFP4 (cache_write).
+
+    q: bf16 [B, L, Hq, D], [B, F, N, Hq, D] or packed [T, Hq, D]; k, v: uint8
+    [B, Lk, Hk, D/2] (two E2M1 codes a byte) with k_scale, v_scale uint8
+    [B, Lk, Hk, D/32], or packed; tokens packed, slices k[:, :n] of longer slots will
+    do.  D in {32, 64, 128}.  The rest as for attention_fwd; forward only.
+    """
+    return _attention_mx(True, q, k, k_scale, v, v_scale, causal, causal_block, scale, cu_q, cu_k, max_q, max_k, k_len,
+                         o, lse, return_lse, workspace, stream)
+
+
+def attention_fwd_fp8(q, k, k_scale, v, v_scale, *, causal: bool = False, causal_block: Optional[int] = None,
+                      scale=None, cu_q=None, cu_k=None, max_q=None, max_k=None, k_len=None, o=None, lse=None,
+                      return_lse: bool = True, workspace=None, stream=None):
+    """attention_fwd_fp4 over keys and values in MXFP8: k, v float8_e4m3fn
+    [B, Lk, Hk, D], scales as there."""
+    return _attention_mx(False, q, k, k_scale, v, v_scale, causal, causal_block, scale, cu_q, cu_k, max_q, max_k, k_len,
+                         o, lse, return_lse, workspace, stream)

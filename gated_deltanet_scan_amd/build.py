@@ -14,7 +14,11 @@ SRCS = [os.path.join(PKG, "csrc", "gdn_api.hip"),    # scan kernels and their C 
         os.path.join(PKG, "csrc", "gdn_norm.hip"),   # layer norm
         os.path.join(PKG, "csrc", "gdn_rotary.hip"), # rotary positions
         os.path.join(PKG, "csrc", "gdn_attn.hip"),   # softmax attention: entry points, fp32 kernels
-        os.path.join(PKG, "csrc", "gdn_attn_bf16.hip")]   # its bf16 kernels
+        os.path.join(PKG, "csrc", "gdn_attn_bf16.hip"),   # its bf16 kernels
+        os.path.join(PKG, "csrc", "gdn_attn_mx.hip"),     # its forward kernels over block-scaled caches
+        os.path.join(PKG, "csrc", "gdn_cache.hip"),       # block-scaled caches: writing and reading back
+        os.path.join(PKG, "csrc", "gdn_quant.hip"),       # 8-bit activations: rms norm, quantisation
+        os.path.join(PKG, "csrc", "gdn_matmul.hip")]      # products of 8-bit floats
 LIBS = ["-L/opt/rocm/lib", "-lhipblaslt", "-Wl,-rpath,/opt/rocm/lib"]
 SO = os.path.join(PKG, "libgdn.so")
 

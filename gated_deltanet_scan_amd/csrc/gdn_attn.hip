@@ -526,13 +526,16 @@ bool far(int64_t stride, int most, int64_t tokens) {
     return stride > kMaxStride && (most > 1 || stride > ((int64_t)1 << 40) / std::max<int64_t>(tokens, 1));
 }
 
+// Keys and values in block-scaled codes: queries and outputs are bf16 then.
+bool block_scaled(const gdn_attn_desc* d) { return d->io_dtype == GDN_FP8_E4M3 || d->io_dtype == GDN_FP4_E2M1; }
+
 gdn_status check_attn(const gdn_attn_desc* d) {
     if (!d) return GDN_ERR_INVALID_ARG;
     if (d->n_seq < 0 || d->Hq < 1 || d->Hk < 1 || d->D < 1 || d->total_q < 0 || d->total_k < 0 || d->max_q < 0 ||
         d->max_k < 0)
         return GDN_ERR_INVALID_ARG;
     if (d->Hq % d->Hk) return GDN_ERR_INVALID_ARG;
-    if (d->io_dtype != GDN_BF16 && d->io_dtype != GDN_F32) return GDN_ERR_INVALID_ARG;
+    if (d->io_dtype != GDN_BF16 && d->io_dtype != GDN_F32 && !block_scaled(d)) return GDN_ERR_INVALID_ARG;
     if (d->flags & ~(uint32_t)GDN_FLAG_ATTN_CAUSAL) return GDN_ERR_INVALID_ARG;
     if ((d->flags & GDN_FLAG_ATTN_CAUSAL) && d->causal_block < 1) return GDN_ERR_INVALID_ARG;
     // below, what a row's maximum may rise by without rescaling is no finite score
@@ -542,6 +545,9 @@ gdn_status check_attn(const gdn_attn_desc* d) {
     if ((d->q_stride && d->q_stride < rq) || (d->k_stride && d->k_stride < rk) || (d->v_stride && d->v_stride < rk))
         return GDN_ERR_INVALID_ARG;
     if (d->D != 16 && d->D != 32 && d->D != 64 && d->D != 128) return GDN_ERR_UNSUPPORTED;
+    // a scale covers 32 features; a cache's tokens are packed
+    if (block_scaled(d) && (d->D == 16 || (d->k_stride && d->k_stride != rk) || (d->v_stride && d->v_stride != rk)))
+        return GDN_ERR_UNSUPPORTED;
     // row numbers within a sequence are 32-bit, with room for a tile
     if (d->total_q > INT32_MAX || d->total_k > INT32_MAX || (int64_t)d->max_q * d->Hq > (1 << 30) ||
         d->max_k > (1 << 30) || d->k_room > INT32_MAX)
@@ -562,7 +568,7 @@ gdn_attn_desc bounded(const gdn_attn_desc* d) {
     return b;
 }
 
-bool fast(const gdn_attn_desc* d) { return d->io_dtype == GDN_BF16 && d->D >= 32; }
+bool fast(const gdn_attn_desc* d) { return d->io_dtype != GDN_F32 && d->D >= 32; }
 
 int fwd_rows(const gdn_attn_desc* d) {
     return fast(d) ? attn_fwd_bf16_rows(d->max_q, d->Hq / d->Hk, d->D) : kRows;
@@ -701,9 +707,7 @@ gdn_status run_sum(const AttnArgs& a, unsigned groups, hipStream_t s) {
 
 }  // namespace
 
-extern "C" {
-
-size_t gdn_attn_workspace_size(const gdn_attn_desc* d) {
+extern "C" size_t gdn_attn_workspace_size(const gdn_attn_desc* d) {
     if (check_attn(d) != GDN_OK || d->n_seq == 0 || d->total_q == 0 || d->max_q == 0) return 0;
     const gdn_attn_desc b = bounded(d);
     const int64_t n = fwd_splits(&b);
@@ -711,15 +715,18 @@ size_t gdn_attn_workspace_size(const gdn_attn_desc* d) {
     return round256((size_t)n * d->total_q * d->Hq * d->D * 4) + round256((size_t)n * d->total_q * d->Hq * 4);
 }
 
-gdn_status gdn_attn_fwd(const gdn_attn_desc* d, const void* q, const void* k, const void* v, const int32_t* cu_q,
-                        const int32_t* cu_k, const int32_t* k_len, void* o, float* lse, void* workspace,
-                        size_t workspace_bytes, void* stream) {
-    gdn_status st = check_attn(d);
-    if (st != GDN_OK) return st;
+namespace {
+
+// The forward call; k_scale and v_scale with block-scaled keys and values.
+gdn_status attn_fwd(const gdn_attn_desc* d, const void* q, const void* k, const uint8_t* k_scale, const void* v,
+                    const uint8_t* v_scale, const int32_t* cu_q, const int32_t* cu_k, const int32_t* k_len, void* o,
+                    float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    gdn_status st;
+    const bool mx = block_scaled(d);
     if (!cu_q && (int64_t)d->n_seq * d->max_q != d->total_q) return GDN_ERR_INVALID_ARG;
     if (!cu_k && (int64_t)d->n_seq * d->max_k != d->total_k) return GDN_ERR_INVALID_ARG;
     if (d->n_seq == 0 || d->total_q == 0 || d->max_q == 0) return GDN_OK;
-    if (!q || !o || (d->total_k > 0 && (!k || !v))) return GDN_ERR_INVALID_ARG;
+    if (!q || !o || (d->total_k > 0 && (!k || !v || (mx && (!k_scale || !v_scale))))) return GDN_ERR_INVALID_ARG;
     const gdn_attn_desc b = bounded(d);
     AttnArgs a = fill(&b);
     a.cu_q = cu_q, a.cu_k = cu_k, a.k_len = k_len;
@@ -731,14 +738,18 @@ gdn_status gdn_attn_fwd(const gdn_attn_desc* d, const void* q, const void* k, co
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
         !aligned(cu_q, 4) || !aligned(cu_k, 4) || !aligned(k_len, 4))
         return GDN_ERR_ALIGNMENT;
-    if (a.ldq * e % 16 || a.ldk * e % 16 || a.ldv * e % 16) return GDN_ERR_ALIGNMENT;
+    if (a.ldq * e % 16 || (!mx && (a.ldk * e % 16 || a.ldv * e % 16))) return GDN_ERR_ALIGNMENT;
     const size_t need = gdn_attn_workspace_size(d);
     if (need && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
     if (need && !aligned(workspace, 256)) return GDN_ERR_ALIGNMENT;
     const int64_t wq = (int64_t)d->Hq * d->D, wk = (int64_t)d->Hk * d->D;
-    const Range ins[] = {rng(q, span(d->total_q, a.ldq, wq, e)), rng(k, span(key_rows(d, cu_k), a.ldk, wk, e)),
-                         rng(v, span(key_rows(d, cu_k), a.ldv, wk, e)), rng(cu_q, ((size_t)d->n_seq + 1) * 4),
-                         rng(cu_k, ((size_t)d->n_seq + 1) * 4), rng(k_len, (size_t)d->n_seq * 4)};
+    // elements of k and v from the first to the last, in bytes, and their scales
+    const size_t nk = span(key_rows(d, cu_k), a.ldk, wk, 1), nv = span(key_rows(d, cu_k), a.ldv, wk, 1);
+    const size_t two = d->io_dtype == GDN_FP4_E2M1 ? 1 : mx ? 2 : 2 * e;
+    const Range ins[] = {rng(q, span(d->total_q, a.ldq, wq, e)), rng(k, nk * two / 2), rng(v, nv * two / 2),
+                         rng(k_scale, mx ? nk / 32 : 0), rng(v_scale, mx ? nv / 32 : 0),
+                         rng(cu_q, ((size_t)d->n_seq + 1) * 4), rng(cu_k, ((size_t)d->n_seq + 1) * 4),
+                         rng(k_len, (size_t)d->n_seq * 4)};
     const Range outs[] = {rng(o, (size_t)d->total_q * wq * e), rng(lse, (size_t)d->total_q * d->Hq * 4),
                           rng(need ? workspace : nullptr, need)};
     for (int i = 0; i < 3; ++i) {
@@ -749,7 +760,7 @@ gdn_status gdn_attn_fwd(const gdn_attn_desc* d, const void* q, const void* k, co
     }
     int cus;
     if ((st = check_device(&cus)) != GDN_OK) return st;
-    a.q = q, a.k = k, a.v = v, a.out = o, a.lse = lse;
+    a.q = q, a.k = k, a.v = v, a.out = o, a.lse = lse, a.k_scale = k_scale, a.v_scale = v_scale;
     if (a.splits > 1) {
         a.part_o = static_cast<float*>(workspace);
         a.part_lse = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
@@ -759,14 +770,48 @@ gdn_status gdn_attn_fwd(const gdn_attn_desc* d, const void* q, const void* k, co
     const bool f32 = d->io_dtype == GDN_F32;
     // bf16 heads of 16 features are narrower than the bf16 tiles and take the fp32 kernels
     st = f32       ? GDN_BY_D(run_fwd, float, a, g.main, s)
+         : mx      ? attn_fwd_mx(a, d->io_dtype == GDN_FP4_E2M1, fwd_rows(&b), g.main, s)
          : fast(d) ? attn_fwd_bf16(a, fwd_rows(&b), g.main, s)
                    : run_fwd<uint16_t, 16>(a, g.main, s);
     if (st != GDN_OK || a.splits == 1) return st;
     return f32 ? GDN_BY_D(run_join, float, a, g.join, s) : GDN_BY_D(run_join, uint16_t, a, g.join, s);
 }
 
+}  // namespace
+
+extern "C" {
+
+gdn_status gdn_attn_fwd(const gdn_attn_desc* d, const void* q, const void* k, const void* v, const int32_t* cu_q,
+                        const int32_t* cu_k, const int32_t* k_len, void* o, float* lse, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+    const gdn_status st = check_attn(d);
+    if (st != GDN_OK) return st;
+    if (block_scaled(d)) return GDN_ERR_INVALID_ARG;
+    return attn_fwd(d, q, k, nullptr, v, nullptr, cu_q, cu_k, k_len, o, lse, workspace, workspace_bytes, stream);
+}
+
+gdn_status gdn_attn_fwd_fp8(const gdn_attn_desc* d, const void* q, const void* k, const uint8_t* k_scale,
+                            const void* v, const uint8_t* v_scale, const int32_t* cu_q, const int32_t* cu_k,
+                            const int32_t* k_len, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+    if (d && d->io_dtype != GDN_FP8_E4M3) return GDN_ERR_INVALID_ARG;
+    const gdn_status st = check_attn(d);
+    if (st != GDN_OK) return st;
+    return attn_fwd(d, q, k, k_scale, v, v_scale, cu_q, cu_k, k_len, o, lse, workspace, workspace_bytes, stream);
+}
+
+gdn_status gdn_attn_fwd_fp4(const gdn_attn_desc* d, const void* q, const void* k, const uint8_t* k_scale,
+                            const void* v, const uint8_t* v_scale, const int32_t* cu_q, const int32_t* cu_k,
+                            const int32_t* k_len, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+    if (d && d->io_dtype != GDN_FP4_E2M1) return GDN_ERR_INVALID_ARG;
+    const gdn_status st = check_attn(d);
+    if (st != GDN_OK) return st;
+    return attn_fwd(d, q, k, k_scale, v, v_scale, cu_q, cu_k, k_len, o, lse, workspace, workspace_bytes, stream);
+}
+
 size_t gdn_attn_workspace_size_bwd(const gdn_attn_desc* d) {
-    if (check_attn(d) != GDN_OK || d->n_seq == 0) return 0;
+    if (check_attn(d) != GDN_OK || block_scaled(d) || d->n_seq == 0) return 0;
     const gdn_attn_desc b = bounded(d);
     const size_t n = bwd_splits(&b);
     return round256((size_t)d->total_q * d->Hq * 4) + (n > 1 ? 2 * round256(n * d->total_k * d->Hk * d->D * 4) : 0);
@@ -777,6 +822,7 @@ gdn_status gdn_attn_bwd(const gdn_attn_desc* d, const void* q, const void* k, co
                         void* dv, void* workspace, size_t workspace_bytes, void* stream) {
     gdn_status st = check_attn(d);
     if (st != GDN_OK) return st;
+    if (block_scaled(d)) return GDN_ERR_INVALID_ARG;
     if (!cu_q && (int64_t)d->n_seq * d->max_q != d->total_q) return GDN_ERR_INVALID_ARG;
     if (!cu_k && (int64_t)d->n_seq * d->max_k != d->total_k) return GDN_ERR_INVALID_ARG;
     if (d->n_seq == 0 || (d->total_q == 0 && d->total_k == 0)) return GDN_OK;

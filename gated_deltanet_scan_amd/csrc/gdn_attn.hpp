@@ -42,6 +42,7 @@ struct AttnArgs {
     int join_rows;                       // rows of a workgroup of the join
     int causal, block;
     float scale;
+    const uint8_t *k_scale, *v_scale;    // block-scaled keys and values
 };
 
 // Rows [start, start + len) of sequence s.  Whatever the device arrays hold,
@@ -243,6 +244,8 @@ __device__ __forceinline__ float log2_f(float x) { return __builtin_amdgcn_logf(
 constexpr int kBwdTile = 128;
 gdn_status attn_fwd_bf16(const AttnArgs& a, int rows, Grid g, hipStream_t s);
 gdn_status attn_bwd_bf16(const AttnArgs& a, Grid dq, Grid dkv, hipStream_t s);
+// The forward pass over block-scaled keys (gdn_attn_mx.hip), with the same row tiles.
+gdn_status attn_fwd_mx(const AttnArgs& a, bool fp4, int rows, Grid g, hipStream_t s);
 // Row tile of the forward kernel that these arguments select.
 int attn_fwd_bf16_rows(int max_q, int G, int D);
 

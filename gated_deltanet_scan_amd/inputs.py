@@ -255,6 +255,24 @@ def make_fp4(w: Workload):
     return tuple((c, s) for c, s, _ in enc), deq
 
 
+def to_fp8_weight(w):
+    """Encode a weight [N, K] (a torch tensor, any device) in E4M3 with a float32
+    scale for each 128 x 128 block, the layout of matmul_fp8: m the largest
+    magnitude of a block, 2^-100 at least, scale = m / 448 and the codes are
+    w (448 / m) rounded to nearest even.  Returns (codes torch.float8_e4m3fn
+    [N, K], scales [ceil(N/128), ceil(K/128)])."""
+    import torch
+    N, K = w.shape
+    nb, kb = -(-N // 128), -(-K // 128)
+    x = torch.zeros((nb * 128, kb * 128), dtype=torch.float32, device=w.device)
+    x[:N, :K] = w
+    x = x.reshape(nb, 128, kb, 128)
+    top = x.abs().amax(dim=(1, 3)).clamp_min(2.0 ** -100)
+    inv = torch.full_like(top, 448.0).div(top)             # one rounding (448.0 / top has two)
+    codes = (x * inv[:, None, :, None]).to(torch.float8_e4m3fn)
+    return codes.reshape(nb * 128, kb * 128)[:N, :K].contiguous(), top / 448.0
+
+
 def make_config(name: str, seed: int = 0, **overrides) -> Workload:
     """Draw one of the named workloads in CONFIGS (fields may be overridden)."""
     c = dict(CONFIGS[name])

@@ -500,6 +500,117 @@ gdn_status gdn_attn_bwd(const gdn_attn_desc* d, const void* q, const void* k, co
                         void* dq, void* dk, void* dv,
                         void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------- attention over block-scaled caches
+ * gdn_attn_fwd on keys and values held in 8 or 4 bits, for serving from long
+ * caches (a minute's keys and values, 16 heads of 128, take 872 MB a block in
+ * bf16, 450 in MXFP8 and 232 in MXFP4): the same operation on the dequantised
+ * values.  d->io_dtype is GDN_FP8_E4M3 or GDN_FP4_E2M1, each entry point accepting
+ * its own (GDN_ERR_INVALID_ARG otherwise, as gdn_attn_fwd and gdn_attn_bwd do of
+ * both); q and o are bfloat16.  k and v are codes [total_k][Hk][D] bytes, or
+ * [total_k][Hk][D/2] with two a byte, k_scale and v_scale E8M0 bytes
+ * [total_k][Hk][D/32], in the layouts of gdn_frame_scan_fwd_fp8 and _fp4; a scale
+ * byte of 255 makes its 32 values NaN, which as any other value reach the rows
+ * that see them and no others.  gdn_cache_write fills such a cache; cu_q, cu_k,
+ * k_len, k_room and the mask are as in gdn_attn_fwd, and k_len is what the write
+ * was given.  D in {32, 64, 128}, k_stride and v_stride 0 or Hk D (tokens are
+ * packed, slots may lie k_room apart) (GDN_ERR_UNSUPPORTED).  Codes are 16-byte
+ * aligned; scales need no alignment.  Workspace: gdn_attn_workspace_size of the
+ * same descriptor.  Codes widen to bf16 exactly, so the results differ from
+ * gdn_attn_fwd's on bf16 tensors of the dequantised values only by the order of
+ * sums. */
+gdn_status gdn_attn_fwd_fp8(const gdn_attn_desc* d, const void* q, const void* k, const uint8_t* k_scale,
+                            const void* v, const uint8_t* v_scale,
+                            const int32_t* cu_q, const int32_t* cu_k, const int32_t* k_len,
+                            void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+gdn_status gdn_attn_fwd_fp4(const gdn_attn_desc* d, const void* q, const void* k, const uint8_t* k_scale,
+                            const void* v, const uint8_t* v_scale,
+                            const int32_t* cu_q, const int32_t* cu_k, const int32_t* k_len,
+                            void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Writing such a cache, and reading it back.
+ *
+ * gdn_cache_write quantises new keys and values k, v [total_new][H][D] (io_dtype;
+ * k_stride and v_stride elements from one token to the next, 0 = packed) into the
+ * caches of gdn_attn_fwd_fp8 / _fp4 (cache_dtype).  Sequence s brings the tokens
+ * cu_new[s] .. cu_new[s+1]-1 (cu_new NULL: max_new each), which are the last of its
+ * k_len[s] positions: token i of n goes to place k_len[s] - n + i
+ * of the slot cu_k[s] .. cu_k[s+1]-1 (cu_k NULL: max_k places from s k_room on, 0
+ * = max_k), as the queries of an attention call lie.  k_len NULL: the slot's last
+ * places.  Tokens whose place lies outside the slot are dropped; places that get
+ * no token keep what they hold.  No two sequences may share a place.
+ *
+ * For 32 consecutive features of largest magnitude m the scale byte is e + 127,
+ * e = floor(log2 m) - 8 (E4M3) or - 2 (E2M1), at least -127 and 0 where m is 0; a
+ * value x is stored as x / 2^e rounded to nearest (ties to the even code, beyond
+ * +-448 or +-6 those; E2M1 holds no -0).  Where one of the 32 is infinite or NaN
+ * the scale byte is 255: all of them read as NaN.
+ *
+ * gdn_cache_read widens each slot's first k_len[s] places (all, where k_len is
+ * NULL) to k, v [total_k][H][D] in io_dtype, packed; the others are left as they
+ * are.  cu_new, total_new, max_new and the strides are unused there.  A bf16 or
+ * fp32 value is exact, but for bf16 ones below 2^-126.
+ *
+ * D in {32, 64, 128}, H D at most 2^20, tokens and k_room below 2^31, strides at
+ * most 2^31 (GDN_ERR_UNSUPPORTED).  k, v, their strides and codes are multiples of
+ * 16 bytes.  Outputs are disjoint from the inputs and from each other. */
+typedef struct gdn_cache_desc {
+    int64_t total_new, total_k;            /* new tokens; places of the caches   */
+    int64_t k_stride, v_stride;            /* elements between new tokens, 0: packed */
+    int64_t k_room;                        /* cu_k NULL: places from one slot to the next, 0: max_k */
+    int32_t n_seq, H, D;
+    int32_t max_new, max_k;                /* bounds of the new tokens and of the slots */
+    int32_t io_dtype, cache_dtype;         /* of k and v; GDN_FP8_E4M3 or GDN_FP4_E2M1 */
+} gdn_cache_desc;
+
+gdn_status gdn_cache_write(const gdn_cache_desc* d, const void* k, const void* v,
+                           const int32_t* cu_new, const int32_t* cu_k, const int32_t* k_len,
+                           void* k_codes, uint8_t* k_scale, void* v_codes, uint8_t* v_scale, void* stream);
+gdn_status gdn_cache_read(const gdn_cache_desc* d, const void* k_codes, const uint8_t* k_scale,
+                          const void* v_codes, const uint8_t* v_scale,
+                          const int32_t* cu_k, const int32_t* k_len, void* k, void* v, void* stream);
+
+/* ------------------------------------------------------------ 8-bit projections
+ * A block's projections on 8-bit floats (E4M3) with float32 scales, for serving:
+ * activations with a scale for each group of 128 columns of a row, weights with
+ * one for each 128 x 128 block.  A value is e4m3(code) times its scale.
+ *
+ * gdn_rms_norm_fwd_fp8: for every row of C values
+ *     t = x + residual,   y = t (<t^2> + eps)^(-1/2) weight
+ * x, residual, sum [rows][C] in d->io_dtype, weight [C] in d->w_dtype, each but x
+ * may be NULL (no residual; weight 1; sum not written).  sum takes t, rounded once;
+ * it may be x or residual (any other overlap is refused).  y comes in 8 bits: with
+ * m = max(max |y|, 2^-100) over a group, y_scale [rows][ceil(C/128)] = m / 448 and
+ * the codes y [rows][C] are y (448 / m) rounded to nearest.  gdn_quantize_fp8
+ * gives x itself so (its w_dtype and eps are unused).  A NaN reads as NaN, and so
+ * does the group of an infinity.  Sums are float32.  rows >= 0, 1 <= C <= 2^20;
+ * pointers need only their element's alignment.
+ *
+ * gdn_matmul_fp8:  y[m][n] = sum_k x[m][k] w[n][k] on the values
+ *     x [M][K] codes, x_scale [M][ceil(K/128)],
+ *     w [N][K] codes (output-major), w_scale [ceil(N/128)][ceil(K/128)],
+ * y bfloat16 [M][N], or with parts > 1 [parts][M][N / parts]: q, k and v of a
+ * w_qkv [3][H][D][C] as three tensors.  Products of 128 columns are formed by the
+ * 8-bit matrix instruction, which adds them eight at a time with at least 13 bits
+ * below the largest of the eight (Gaussian operands: 1.4e-5 of the result, a
+ * hundredth of its rounding to bfloat16); what they give is scaled and added in
+ * float32.  K a multiple of 16, N and K at most 2^20, M below 2^31
+ * (GDN_ERR_UNSUPPORTED).  x, w and y are 16-byte aligned, scales 4-byte.
+ *
+ * All are bitwise reproducible; outputs are disjoint from the inputs and from each
+ * other except as said. */
+gdn_status gdn_rms_norm_fwd_fp8(const gdn_norm_desc* d, const void* x, const void* residual, const void* weight,
+                                void* sum, void* y, float* y_scale, void* stream);
+gdn_status gdn_quantize_fp8(const gdn_norm_desc* d, const void* x, void* y, float* y_scale, void* stream);
+
+typedef struct gdn_matmul_desc {
+    int64_t M;                             /* tokens                             */
+    int32_t N, K;                          /* outputs, inputs                    */
+    int32_t parts;                         /* outputs stored as so many tensors  */
+} gdn_matmul_desc;
+
+gdn_status gdn_matmul_fp8(const gdn_matmul_desc* d, const void* x, const float* x_scale,
+                          const void* w, const float* w_scale, void* y, void* stream);
+
 /* Human-readable name of a status code (static storage). */
 const char* gdn_status_string(gdn_status s);
 

@@ -108,3 +108,30 @@ def attention_bwd(q, k, v, do, causal=False, block=1, scale=None):
         dk[:, c] += scale * (ds.T @ q[:, h])
         dv[:, c] += p.T @ do[:, h]
     return dq, dk, dv
+
+
+# ------------------------------------------------------------------ 8-bit projections
+def rms_norm(x, weight=None, residual=None, eps=1e-6):
+    """(y, t) of rows x [..., C]: t = x + residual, y = t / rms(t) weight."""
+    t = np.asarray(x, np.float64)
+    if residual is not None:
+        t = t + np.asarray(residual, np.float64)
+    y = t / np.sqrt((t * t).mean(-1, keepdims=True) + eps)
+    return (y if weight is None else y * np.asarray(weight, np.float64)), t
+
+
+def group_scales(y, group=128):
+    """Largest magnitude of each group of columns / 448."""
+    C = y.shape[-1]
+    m = np.stack([np.abs(y[..., c:c + group]).max(-1) for c in range(0, C, group)], -1)
+    return np.maximum(m, 2.0 ** -100) / 448
+
+
+def expand(scale, n, axis, group=128):
+    return np.repeat(scale, group, axis=axis).take(np.arange(n), axis=axis)
+
+
+def matmul(x, x_scale, w, w_scale):
+    """y [M, N] of codes' values x [M, K], w [N, K] and their scales."""
+    K, N = x.shape[1], w.shape[0]
+    return (x * expand(x_scale, K, 1)) @ (w * expand(expand(w_scale, K, 1), N, 0)).T
