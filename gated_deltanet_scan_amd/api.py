@@ -903,9 +903,9 @@ def rms_norm_fwd_fp8(x, weight=None, residual=None, *, eps: float = 1e-6, y=None
     where, handle = _launch(stream, x.device)
     with where:   # allocations belong to the launch stream
         if y is None:
-            y = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+            y = x.new_empty(x.shape, dtype=torch.float8_e4m3fn)
         if y_scale is None:
-            y_scale = torch.empty(scales, dtype=torch.float32, device=x.device)
+            y_scale = x.new_empty(scales, dtype=torch.float32)
         if total is None and residual is not None:
             total = torch.empty_like(x)
         st = _lib.load().gdn_rms_norm_fwd_fp8(ctypes.byref(desc), _ptr(x), _ptr(residual), _ptr(weight), _ptr(total),
@@ -924,9 +924,9 @@ def quantize_fp8(x, *, y=None, y_scale=None, stream=None):
     where, handle = _launch(stream, x.device)
     with where:   # allocations belong to the launch stream
         if y is None:
-            y = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+            y = x.new_empty(x.shape, dtype=torch.float8_e4m3fn)
         if y_scale is None:
-            y_scale = torch.empty(scales, dtype=torch.float32, device=x.device)
+            y_scale = x.new_empty(scales, dtype=torch.float32)
         st = _lib.load().gdn_quantize_fp8(ctypes.byref(desc), _ptr(x), _ptr(y), _ptr(y_scale), handle)
     if st != 0:
         raise GdnError(st, "gdn_quantize_fp8")
@@ -964,7 +964,7 @@ def matmul_fp8(x, x_scale, w, w_scale, *, parts: int = 1, y=None, stream=None):
     where, handle = _launch(stream, x.device)
     with where:   # allocations belong to the launch stream
         if y is None:
-            y = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+            y = x.new_empty(shape, dtype=torch.bfloat16)
         st = _lib.load().gdn_matmul_fp8(ctypes.byref(desc), _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(y),
                                         handle)
     if st != 0:
@@ -1014,9 +1014,15 @@ def _cache_args(k, k_scale, v, v_scale, fp4):
     if D % MX_BLOCK:
         raise ValueError("a cache's head size must be a multiple of %d (got %d)" % (MX_BLOCK, D))
     codes, scales = k.shape, k.shape[:-1] + (D // MX_BLOCK,)
-    dtype = torch.uint8 if fp4 else torch.float8_e4m3fn
-    for name, t, dt, shape in (("k", k, dtype, codes), ("k_scale", k_scale, torch.uint8, scales), ("v", v, dtype, codes),
-                               ("v_scale", v_scale, torch.uint8, scales)):
+    dtype, byte, index = torch.uint8 if fp4 else torch.float8_e4m3fn, torch.uint8, k.get_device()
+    # the usual case in few steps; what fails here is looked at one by one below
+    if (index >= 0 and index == v.get_device() == k_scale.get_device() == v_scale.get_device() and
+            k.dtype == v.dtype == dtype and k_scale.dtype == v_scale.dtype == byte and v.shape == codes and
+            k_scale.shape == scales and v_scale.shape == scales and k.is_contiguous() and v.is_contiguous() and
+            k_scale.is_contiguous() and v_scale.is_contiguous()):
+        return codes[:-2], H, D, 0
+    for name, t, dt, shape in (("k", k, dtype, codes), ("k_scale", k_scale, byte, scales), ("v", v, dtype, codes),
+                               ("v_scale", v_scale, byte, scales)):
         if not t.is_cuda:
             raise ValueError("%s must be a device tensor (got %s)" % (name, t.device))
         if t.dtype != dt:
@@ -1059,9 +1065,11 @@ def cache_write(k, v, k_cache, k_scale, v_cache, v_scale, *, k_len=None, cu_new=
     if v.dtype != k.dtype:
         raise TypeError("v must be %s (got %s)" % (k.dtype, v.dtype))
     io = _io(k.dtype, "k and v")
-    (ldk, rk), (ldv, rv) = _token_strides(k, "k"), _token_strides(v, "v")
-    if rk or rv:
-        raise ValueError("k and v must have packed heads and evenly spaced tokens")
+    ldk = ldv = 0
+    if not (k.is_contiguous() and v.is_contiguous()):
+        (ldk, rk), (ldv, rv) = _token_strides(k, "k"), _token_strides(v, "v")
+        if rk or rv:
+            raise ValueError("k and v must have packed heads and evenly spaced tokens")
     if (k.dim() == 3) != (len(lead) == 1):
         raise ValueError("packed k [T, H, D] go with a packed cache")
     if k.dim() == 3:
@@ -1130,8 +1138,8 @@ def cache_read(k_cache, k_scale, v_cache, v_scale, *, dtype: torch.dtype = torch
                              _lib.GDN_FP4_E2M1 if fp4 else _lib.GDN_FP8_E4M3)
     where, handle = _launch(stream, k_cache.device)
     with where:   # allocations belong to the launch stream
-        k = torch.empty(shape, dtype=dtype, device=k_cache.device) if k is None else k
-        v = torch.empty(shape, dtype=dtype, device=k_cache.device) if v is None else v
+        k = k_cache.new_empty(shape, dtype=dtype) if k is None else k
+        v = k_cache.new_empty(shape, dtype=dtype) if v is None else v
         st = _lib.load().gdn_cache_read(ctypes.byref(desc), _ptr(k_cache), _ptr(k_scale), _ptr(v_cache), _ptr(v_scale),
                                         _ptr(cu_k), _ptr(k_len), _ptr(k), _ptr(v), handle)
     if st != 0:

@@ -570,6 +570,9 @@ gdn_attn_desc bounded(const gdn_attn_desc* d) {
 
 bool fast(const gdn_attn_desc* d) { return d->io_dtype != GDN_F32 && d->D >= 32; }
 
+// Block-scaled keys under a few query rows take a kernel of their own.
+bool few(const gdn_attn_desc* d) { return block_scaled(d) && (int64_t)d->max_q * (d->Hq / d->Hk) <= kFewRows; }
+
 int fwd_rows(const gdn_attn_desc* d) {
     return fast(d) ? attn_fwd_bf16_rows(d->max_q, d->Hq / d->Hk, d->D) : kRows;
 }
@@ -587,6 +590,7 @@ int fwd_rows(const gdn_attn_desc* d) {
 // short work spreads evenly; a split's fp32 partial result is then small
 // against its keys, of which it takes 512 at least (128 at the fp32 rate).
 int fwd_chunk(const gdn_attn_desc* d) {
+    if (few(d)) return attn_few_chunk(d->n_seq, d->Hk, d->D, d->max_k);
     const int64_t rows = (int64_t)d->max_q * (d->Hq / d->Hk);
     int tiles;
     const int64_t units = places(d->total_q * (d->Hq / d->Hk), rows, d->n_seq, fwd_rows(d), true, &tiles) * d->Hk;
@@ -733,7 +737,8 @@ gdn_status attn_fwd(const gdn_attn_desc* d, const void* q, const void* k, const 
     a.splits = fwd_splits(&b);
     a.chunk = fwd_chunk(&b);
     FwdGrids g;
-    if (!fwd_grids(a, fwd_rows(&b), !fast(d), &g)) return GDN_ERR_UNSUPPORTED;
+    FewGrids gf;
+    if (few(&b) ? !attn_few_grids(a, &gf) : !fwd_grids(a, fwd_rows(&b), !fast(d), &g)) return GDN_ERR_UNSUPPORTED;
     const size_t e = d->io_dtype == GDN_F32 ? 4 : 2;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
         !aligned(cu_q, 4) || !aligned(cu_k, 4) || !aligned(k_len, 4))
@@ -767,6 +772,7 @@ gdn_status attn_fwd(const gdn_attn_desc* d, const void* q, const void* k, const 
                                               round256((size_t)a.splits * d->total_q * d->Hq * d->D * 4));
     }
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if (few(&b)) return attn_fwd_few(a, d->io_dtype == GDN_FP4_E2M1, gf, s);
     const bool f32 = d->io_dtype == GDN_F32;
     // bf16 heads of 16 features are narrower than the bf16 tiles and take the fp32 kernels
     st = f32       ? GDN_BY_D(run_fwd, float, a, g.main, s)

@@ -246,6 +246,15 @@ gdn_status attn_fwd_bf16(const AttnArgs& a, int rows, Grid g, hipStream_t s);
 gdn_status attn_bwd_bf16(const AttnArgs& a, Grid dq, Grid dkv, hipStream_t s);
 // The forward pass over block-scaled keys (gdn_attn_mx.hip), with the same row tiles.
 gdn_status attn_fwd_mx(const AttnArgs& a, bool fp4, int rows, Grid g, hipStream_t s);
+// The same for few query rows of a key head, at most kFewRows: launches, and the keys
+// of a split.
+constexpr int kFewRows = 16;
+struct FewGrids {
+    unsigned main, join;
+};
+int attn_few_chunk(int n_seq, int Hk, int D, int max_k);
+bool attn_few_grids(const AttnArgs& a, FewGrids* g);
+gdn_status attn_fwd_few(const AttnArgs& a, bool fp4, FewGrids g, hipStream_t s);
 // Row tile of the forward kernel that these arguments select.
 int attn_fwd_bf16_rows(int max_q, int G, int D);
 

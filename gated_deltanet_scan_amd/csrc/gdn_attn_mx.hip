@@ -1,16 +1,335 @@
 // Softmax attention over block-scaled keys and values (MXFP8, MXFP4): the
-// launches of gdn_attn_fwd_fp8 and gdn_attn_fwd_fp4.  The forward kernel is that
-// of bf16 keys (gdn_attn_tile.hpp); codes are widened to bf16 as they are staged.
+// launches of gdn_attn_fwd_fp8 and gdn_attn_fwd_fp4, and the kernel for few query
+// rows.  More rows take the forward kernel of bf16 keys (gdn_attn_tile.hpp), which
+// widens codes to bf16 as it stages them.
+//
+// Few rows (single tokens; at most 16 of a key head): a wave takes one key head and a
+// chunk of keys, in steps of 32.  v_mfma_f32_16x16x32_bf16: lane l = 16 g + r holds
+// eight contraction values of row r (operand A) or column r (operand B); the 16 x 16
+// result sits in lane l as rows 4 g .. 4 g + 3 of column r.
+//     S^T = K Q^T: a lane reads a quarter g of the features of key r as they are
+//     stored, one load; they are contracted in the order 8 e + (0..7) of each quarter.
+//     O^T += V^T P^T: the eight scores that a lane holds of query r, keys 4 g .. + 3
+//     and 16 + 4 g .. + 3, are its operand as they are; V goes through LDS, a tile of
+//     the wave's own (LDS serves a wave in order, so no barrier stands anywhere), and
+//     is read transposed.
 #include "gdn_attn_tile.hpp"
 
 namespace gdnattn {
 namespace {
 
+constexpr int kFewWaves = 4, kStep = 32;
+
+// A lane's share of one row: N / 4 dwords' worth of codes.
+template <int DW>
+struct Raw {
+    uint32_t w[DW];
+    __device__ __forceinline__ void load(rsrc_t rs, uint32_t at) {
+        if constexpr (DW == 1) {
+            w[0] = __builtin_amdgcn_raw_buffer_load_b32(rs, at, 0, 0);
+        } else if constexpr (DW == 2) {
+            const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(rs, at, 0, 0);
+            w[0] = x[0], w[1] = x[1];
+        } else {
+#pragma unroll
+            for (int i = 0; i < DW / 4; ++i) {
+                const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(rs, at + 16 * i, 0, 0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[4 * i + j] = x[j];
+            }
+        }
+    }
+};
+template <typename F, int DW>
+__device__ __forceinline__ u32x4 eight_of(const Raw<DW>& r, int e, float s) {
+    if constexpr (F::kPerByte == 2)
+        return F::widen(r.w[e], s);
+    else
+        return F::widen(u32x2{r.w[2 * e], r.w[2 * e + 1]}, s);
+}
+
+__device__ __forceinline__ f32x4 mma16(u32x4 x, u32x4 y, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), c, 0,
+                                                   0, 0);
+}
+// Over the four lanes that hold one column.
+__device__ __forceinline__ float quarters_max(float x) {
+    x = fmaxf(x, __shfl_xor(x, 16));
+    return fmaxf(x, __shfl_xor(x, 32));
+}
+__device__ __forceinline__ float quarters_sum(float x) {
+    x += __shfl_xor(x, 16);
+    return x + __shfl_xor(x, 32);
+}
+
+template <typename F, int D>
+__global__ __launch_bounds__(64 * kFewWaves, 3) void attn_few_kernel(const AttnArgs a) {
+    constexpr int Q = D / 4, E = D / 32, FT = D / 16, DW = Q / F::kPerByte / 4, TB = kStep * D * 2;
+    __shared__ __attribute__((aligned(256))) unsigned char lds[kFewWaves][TB];
+    const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // key heads run fastest: the waves of a workgroup read neighbouring rows of the same keys
+    const unsigned unit = blockIdx.x * kFewWaves + wave;
+    const int hk = (int)(unit % (unsigned)a.Hk), rest = (int)(unit / (unsigned)a.Hk);
+    const int split = rest % a.splits, sq = rest / a.splits;
+    if (sq >= a.n_seq) return;
+    const Seq z = sequence(a, sq);
+    const int rows = z.lq * a.G;
+    if (rows == 0 || (split > 0 && (int64_t)split * a.chunk >= z.lk)) return;
+    const bool valid = r < rows;
+    const int n = valid ? visible(a, z, r / a.G) : 0, n_first = visible(a, z, 0), n_last = visible(a, z, z.lq - 1);
+    const int lo = min(split * a.chunk, n_last), hi = min(lo + a.chunk, n_last);
+    const int64_t row = (z.q0 + r / a.G) * a.Hq + hk * a.G + r % a.G;
+    u32x4 q[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        q[e] = u32x4{0u, 0u, 0u, 0u};
+        if (valid)
+            q[e] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.q) + (z.q0 + r / a.G) * a.ldq +
+                                                   (int64_t)(hk * a.G + r % a.G) * D + g * Q + 8 * e);
+    }
+    f32x4 acc[FT];
+#pragma unroll
+    for (int t = 0; t < FT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const float c2 = a.scale * kLog2e, slack = kSlack / c2;
+    float m = -INFINITY, ms = 0.f, limit = -INFINITY, l = 0.f;    // as in the tile kernel
+
+    const KeysMx<F> kb(a.k, a.k_scale, 0, z.k0, hk, a.Hk, D), vb(a.v, a.v_scale, 0, z.k0, hk, a.Hk, D);
+    // the chunk's codes, and the lane's first place in them; past its end: zeros
+    const uint32_t bytes = lo < hi ? (uint32_t)(hi - lo - 1) * kb.ldc + D / F::kPerByte : 0;
+    const rsrc_t rk = make_rsrc(kb.codes + (int64_t)lo * kb.ldc, bytes), rv = make_rsrc(vb.codes + (int64_t)lo * vb.ldc, bytes);
+    const uint32_t place = r * kb.ldc + g * Q / F::kPerByte;
+    struct Keys {
+        Raw<DW> x[2];
+    };
+    // keys [n0, n0 + 32) as two tiles of 16.  Without a condition, since waits count
+    // loads: where one may not have been issued, the compiler waits for all.
+    auto load = [&](Keys& k, Keys& v, int n0) {
+        const uint32_t at = place + (uint32_t)(n0 - lo) * kb.ldc;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) k.x[t].load(rk, at + t * 16 * kb.ldc);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) v.x[t].load(rv, at + t * 16 * kb.ldc);
+    };
+    // The scales of a step in one load: those of a key's row in lane key, of its values in
+    // lane 32 + key.  (With a load for each tile of each the wave waited to issue them:
+    // 8 instead of 5 loads a step, 33 us against 26 for the whole call.)
+    const uint8_t* const sp = (lane < 32 ? kb.scales : vb.scales);
+    auto load_scales = [&](int n0) {
+        const uint8_t* const p = sp + (int64_t)min(n0 + (lane & 31), hi - 1) * kb.lds;
+        if constexpr (D == 128)
+            return *reinterpret_cast<const uint32_t __attribute__((aligned(1)))*>(p);
+        else if constexpr (D == 64)
+            return (uint32_t)p[0] | (uint32_t)p[1] << 8;
+        else
+            return (uint32_t)p[0];
+    };
+    // tile t's scale of the lane's features
+    auto scale_at = [&](uint32_t s, int from) {
+        const uint32_t row = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * (from + r), (int)s);
+        return gdnmx::scale_of(row >> (8 * (g * Q / gdnmx::kBlock)) & 255u);
+    };
+    unsigned char* tile = lds[wave];
+    // a lane's places in the tile: chunk g E + e of row r, and eight bytes of chunk 2 t +
+    // of key 4 g + r / 4 (the permutation is an exclusive or, so e and t are as well)
+    const uint32_t put = chunk_at<D>(r, g * E), get = chunk_at<D>(4 * g + (r >> 2), (r >> 1) & 1) + (r & 1) * 8;
+    constexpr int HALF = 16 * D * 2;                          // bytes of 16 keys
+    // keys [n0, n0 + 32); their registers then take those of two steps on
+    auto step = [&](Keys& k, Keys& v, uint32_t& scales, int n0) {
+        f32x4 s[2];
+        float sc[2], vs[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            s[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+            sc[t] = scale_at(scales, 16 * t);
+            vs[t] = scale_at(scales, 32 + 16 * t);
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) s[t] = mma16(eight_of<F>(k.x[t], e, sc[t]), q[e], s[t]);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                *reinterpret_cast<u32x4*>(tile + (put ^ (uint32_t)(16 * e)) + t * HALF) = eight_of<F>(v.x[t], e, vs[t]);
+        scales = load_scales(n0 + 2 * kStep);
+        load(k, v, n0 + 2 * kStep);
+        if (n0 + kStep > n_first) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (n0 + 16 * t + 4 * g + i >= n) s[t][i] = -INFINITY;
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) top = fmaxf(top, s[i >> 2][i & 3]);
+        if (__any(top > limit)) {
+            const float mn = fmaxf(m, quarters_max(top) * c2);
+            const float al = mn == -INFINITY ? 1.f : exp2_f(m - mn);
+            m = mn;
+            ms = mn == -INFINITY ? 0.f : mn;
+            limit = mn / c2 + slack;
+            l *= al;
+#pragma unroll
+            for (int t = 0; t < FT; ++t) acc[t] *= al;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            s[i >> 2][i & 3] = exp2_f(__builtin_fmaf(s[i >> 2][i & 3], c2, -ms));
+            l += s[i >> 2][i & 3];
+        }
+        // P in bf16: see the tile kernel
+        const u32x4 p = {pack_bf16x2(s[0][0], s[0][1]), pack_bf16x2(s[0][2], s[0][3]), pack_bf16x2(s[1][0], s[1][1]),
+                         pack_bf16x2(s[1][2], s[1][3])};
+#pragma unroll
+        for (int t = 0; t < FT; ++t) {
+            // features 16 t + r of keys 4 g .. + 3 and 16 + 4 g .. + 3
+            const u32x2 x = read_tr(tile + (get ^ (uint32_t)(32 * t)));
+            const u32x2 y = read_tr(tile + (get ^ (uint32_t)(32 * t)) + HALF);
+            acc[t] = mma16(u32x4{x[0], x[1], y[0], y[1]}, p, acc[t]);
+        }
+    };
+    if (lo < hi) {
+        Keys k0, v0, k1, v1;
+        uint32_t s0 = load_scales(lo);
+        load(k0, v0, lo);
+        uint32_t s1 = load_scales(lo + kStep);
+        load(k1, v1, lo + kStep);
+        for (int n0 = lo; n0 < hi; n0 += 2 * kStep) {             // chunks are whole pairs; past hi all is masked
+            step(k0, v0, s0, n0);
+            step(k1, v1, s1, n0 + kStep);
+        }
+    }
+    if (a.causal && !finite(acc)) {                           // see finite()
+        m = -INFINITY;
+        l = 0.f;
+#pragma unroll
+        for (int t = 0; t < FT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int j = lo; j < hi; ++j) {
+            float s = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) s = dot8(q[e], kb.eight(j, g * Q + 8 * e), s);
+            s = quarters_sum(s) * c2;
+            if (j < n) {
+                const float mn = fmaxf(m, s), mj = mn == -INFINITY ? 0.f : mn;
+                const float al = exp2_f(m - mj), pj = exp2_f(s - mj);
+                m = mn;
+                l = l * al + (g == 0 ? pj : 0.f);
+#pragma unroll
+                for (int t = 0; t < FT; ++t) {
+                    const u32x2 x = vb.four(j, 16 * t + 4 * g);
+                    acc[t] = acc[t] * al + pj * f32x4{__uint_as_float(x[0] << 16), __uint_as_float(x[0] & 0xffff0000u),
+                                                      __uint_as_float(x[1] << 16), __uint_as_float(x[1] & 0xffff0000u)};
+                }
+            }
+        }
+    }
+    l = quarters_sum(l);
+    if (!valid) return;
+    const float inv = l > 0.f ? 1.0f / l : l;
+    const float lg = l == 0.f ? -INFINITY : (m + log2_f(l)) * kLn2;
+    if (a.splits > 1) {
+        const int64_t pr = (int64_t)split * a.total_q * a.Hq + row;
+#pragma unroll
+        for (int t = 0; t < FT; ++t) *reinterpret_cast<f32x4*>(a.part_o + pr * D + 16 * t + 4 * g) = acc[t] * inv;
+        if (g == 0) a.part_lse[pr] = lg;
+    } else {
+#pragma unroll
+        for (int t = 0; t < FT; ++t)
+            *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + row * D + 16 * t + 4 * g) =
+                u32x2{pack_bf16x2(acc[t][0] * inv, acc[t][1] * inv), pack_bf16x2(acc[t][2] * inv, acc[t][3] * inv)};
+        if (g == 0 && a.lse) a.lse[row] = lg;
+    }
+}
+
+// o = sum over the splits of exp(lse_s - lse) o_s, a workgroup a row.  Its groups of
+// D / 4 lanes take the splits in turn, 128 at once, each with a maximum of its own,
+// so that nothing waits for a first look at all of them; the groups are joined in order
+// through LDS.  Bound by a launch and two trips to memory: 256 rows of 128, up to 128
+// splits, in 5 us.
+template <int D>
+__global__ __launch_bounds__(256) void attn_few_join_kernel(const AttnArgs a) {
+    constexpr int L = D / 4, NG = 256 / L, U = 128 / NG;
+    __shared__ f32x4 sums[NG][L];
+    __shared__ float tops[NG], weights[NG];
+    const int per = a.max_q * a.Hq;
+    const Seq z = sequence(a, (int)(blockIdx.x / (unsigned)per));
+    const int64_t rr = blockIdx.x % (unsigned)per;
+    if (rr >= (int64_t)z.lq * a.Hq) return;
+    const int64_t row = z.q0 * a.Hq + rr, all = a.total_q * a.Hq;
+    const int splits = max(1, (z.lk + a.chunk - 1) / a.chunk);
+    const int group = threadIdx.x / L, c = threadIdx.x % L;
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    float m = -INFINITY, l = 0.f;
+    for (int s0 = group; s0 < splits; s0 += U * NG) {
+        float ls[U];
+        f32x4 o[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t at = min(s0 + u * NG, splits - 1) * all + row;
+            ls[u] = a.part_lse[at] * kLog2e;
+            o[u] = *reinterpret_cast<const f32x4*>(a.part_o + at * D + 4 * c);
+        }
+        float top = m;
+#pragma unroll
+        for (int u = 0; u < U; ++u) top = fmaxf(top, ls[u]);
+        const float base = top == -INFINITY ? 0.f : top, al = exp2_f(m - base);
+        m = top;
+        acc *= al;
+        l *= al;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (s0 + u * NG < splits) {
+                const float w = exp2_f(ls[u] - base);             // 0 for a split that saw nothing
+                acc += w * o[u];
+                l += w;
+            }
+    }
+    sums[group][c] = acc;
+    if (c == 0) {
+        tops[group] = m;
+        weights[group] = l;
+    }
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int i = 1; i < NG; ++i) m = fmaxf(m, tops[i]);
+    const float base = m == -INFINITY ? 0.f : m;
+    acc = f32x4{0.f, 0.f, 0.f, 0.f};
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+        const float w = exp2_f(tops[i] - base);
+        acc += w * sums[i][c];
+        l += w * weights[i];
+    }
+    const float inv = l > 0.f ? 1.0f / l : l;
+    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + row * D + 4 * c) =
+        u32x2{pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv)};
+    if (c == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + log2_f(l)) * kLn2;
+}
+
+gdn_status done() { return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH; }
+
+template <typename F, int D>
+gdn_status launch_few(const AttnArgs& a, FewGrids g, hipStream_t s) {
+    hipLaunchKernelGGL((attn_few_kernel<F, D>), dim3(g.main), dim3(64 * kFewWaves), 0, s, a);
+    if (a.splits > 1) hipLaunchKernelGGL((attn_few_join_kernel<D>), dim3(g.join), dim3(256), 0, s, a);
+    return done();
+}
+template <typename F>
+gdn_status few_by_size(const AttnArgs& a, FewGrids g, hipStream_t s) {
+    return a.D == 32 ? launch_few<F, 32>(a, g, s) : a.D == 64 ? launch_few<F, 64>(a, g, s) : launch_few<F, 128>(a, g, s);
+}
+
 template <typename F, int D, int NW>
 gdn_status launch(AttnArgs a, Grid g, hipStream_t s) {
     a.tiles = g.tiles;
     hipLaunchKernelGGL((attn_fwd_kernel<KeysMx<F>, D, NW>), dim3(g.groups), dim3(64 * NW), 0, s, a);
-    return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+    return done();
 }
 template <typename F>
 gdn_status by_size(const AttnArgs& a, int rows, Grid g, hipStream_t s) {
@@ -23,6 +342,25 @@ gdn_status by_size(const AttnArgs& a, int rows, Grid g, hipStream_t s) {
 
 gdn_status attn_fwd_mx(const AttnArgs& a, bool fp4, int rows, Grid g, hipStream_t s) {
     return fp4 ? by_size<gdnmx::Fp4>(a, rows, g, s) : by_size<gdnmx::Fp8>(a, rows, g, s);
+}
+
+// Keys of a chunk: for about 8192 waves on the card's 256 compute units if every
+// sequence were as long as it may be (lengths differ, and short work spreads evenly);
+// a chunk's fp32 result is then small against its keys.
+int attn_few_chunk(int n_seq, int Hk, int D, int max_k) {
+    const int64_t keys = ((int64_t)max_k * n_seq * Hk + 8191) / 8192;
+    // a chunk and the steps behind it within 32-bit offsets
+    const int64_t most = ((int64_t)1 << 31) / ((int64_t)Hk * D) - 4 * kStep;
+    const int64_t chunk = std::min(std::max<int64_t>(keys, 128), most);
+    return (int)std::min<int64_t>((chunk + 2 * kStep - 1) / (2 * kStep) * (2 * kStep), std::max(max_k, 1));
+}
+bool attn_few_grids(const AttnArgs& a, FewGrids* g) {
+    const int64_t units = (int64_t)a.n_seq * a.splits * a.Hk;
+    if (!grid_of((units + kFewWaves - 1) / kFewWaves, 64 * kFewWaves, &g->main)) return false;
+    return units < INT32_MAX && grid_of((int64_t)a.n_seq * a.max_q * a.Hq, 256, &g->join);
+}
+gdn_status attn_fwd_few(const AttnArgs& a, bool fp4, FewGrids g, hipStream_t s) {
+    return fp4 ? few_by_size<gdnmx::Fp4>(a, g, s) : few_by_size<gdnmx::Fp8>(a, g, s);
 }
 
 }  // namespace gdnattn

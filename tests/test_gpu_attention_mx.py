@@ -124,6 +124,21 @@ def test_cache_filled_in_part(lq, G, Hk, D, fp4):
 
 
 @FORMATS
+@pytest.mark.parametrize("lk,Hq,Hk,D", [(40001, 4, 1, 32), (33000, 16, 1, 128), (17000, 2, 2, 64)])
+def test_many_splits(lk, Hq, Hk, D, fp4):
+    """One request against a long cache: hundreds of splits to a row."""
+    q = rand((1, 1, Hq, D), 1).to(BF).cuda()
+    kc, ks, kv = encode(rand((1, lk, Hk, D), 2), fp4)
+    vc, vs, vv = encode(rand((1, lk, Hk, D), 3), fp4)
+    for causal in (True, False):
+        o, lse = fwd(fp4)(q, kc, ks, vc, vs, causal=causal)
+        x = host(q[0])
+        val, bar = dense(x, kv[0], vv[0], np.zeros_like(x), causal, 1, D ** -0.5, BF)
+        check(host(o[0]), val["o"], bar["o"], "o")
+        check(host(lse[0]), val["lse"], bar["lse"], "lse")
+
+
+@FORMATS
 @pytest.mark.parametrize("lq,lk,Hq,Hk,block,D", [(200, 200, 4, 2, 1, 128), (150, 300, 2, 2, 44, 64), (70, 40, 8, 2, 1, 32),
                                                  (5, 2000, 4, 2, 1, 128), (300, 300, 4, 2, 100, 128),
                                                  (3, 900, 4, 2, 1, 64), (8, 8, 4, 2, 1, 32)])
