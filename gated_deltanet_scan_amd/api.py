@@ -1201,10 +1201,12 @@ def _attention_mx(fp4, q, k, k_scale, v, v_scale, causal, causal_block, scale, c
     where, handle = _launch(stream, q.device)
     with where:   # allocations belong to the launch stream
         if o is None:
-            o = _like(q)
+            o = q.new_empty(q.shape)
         if lse is None and return_lse:
             lse = q.new_empty(q.shape[:-1], dtype=torch.float32)
-        workspace = _workspace(workspace, int(lib.gdn_attn_workspace_size(ctypes.byref(desc))), q.device)
+        if workspace is None:
+            need = lib.gdn_attn_workspace_size(ctypes.byref(desc))
+            workspace = q.new_empty(need, dtype=torch.uint8) if need else None
         st = fn(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(k_scale), _ptr(v), _ptr(v_scale), _ptr(cu_q), _ptr(cu_k),
                 _ptr(k_len), _ptr(o), _ptr(lse), _ptr(workspace), _ws_bytes(workspace), handle)
     if st != 0:

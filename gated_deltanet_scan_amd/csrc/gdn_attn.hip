@@ -590,7 +590,7 @@ int fwd_rows(const gdn_attn_desc* d) {
 // short work spreads evenly; a split's fp32 partial result is then small
 // against its keys, of which it takes 512 at least (128 at the fp32 rate).
 int fwd_chunk(const gdn_attn_desc* d) {
-    if (few(d)) return attn_few_chunk(d->n_seq, d->Hk, d->D, d->max_k);
+    if (few(d)) return attn_few_chunk(d->max_q * (d->Hq / d->Hk), d->n_seq, d->Hk, d->D, d->max_k);
     const int64_t rows = (int64_t)d->max_q * (d->Hq / d->Hk);
     int tiles;
     const int64_t units = places(d->total_q * (d->Hq / d->Hk), rows, d->n_seq, fwd_rows(d), true, &tiles) * d->Hk;

@@ -248,11 +248,11 @@ gdn_status attn_bwd_bf16(const AttnArgs& a, Grid dq, Grid dkv, hipStream_t s);
 gdn_status attn_fwd_mx(const AttnArgs& a, bool fp4, int rows, Grid g, hipStream_t s);
 // The same for few query rows of a key head, at most kFewRows: launches, and the keys
 // of a split.
-constexpr int kFewRows = 16;
+constexpr int kFewRows = 32;
 struct FewGrids {
     unsigned main, join;
 };
-int attn_few_chunk(int n_seq, int Hk, int D, int max_k);
+int attn_few_chunk(int rows, int n_seq, int Hk, int D, int max_k);
 bool attn_few_grids(const AttnArgs& a, FewGrids* g);
 gdn_status attn_fwd_few(const AttnArgs& a, bool fp4, FewGrids g, hipStream_t s);
 // Row tile of the forward kernel that these arguments select.
