@@ -67,9 +67,11 @@ __device__ __forceinline__ float quarters_sum(float x) {
 // join, 62 through the tile kernel.  Bound by the instructions of a step, about 200 of
 // which 64 widen codes, in two or three waves a SIMD (with every load taken out the same
 // steps take 80% of the time); a load of four bytes a lane for each tile's scales costs
-// as much to issue as one of codes, so a step's scales come in one load.
+// as much to issue as one of codes, so a step's scales come in one load.  MXFP8 heads of
+// 128 are bound by memory, 8 x 11008 keys in 41.5 us (1.1 of the floor) with two waves a
+// SIMD; three spill (46.9).
 template <typename F, int D, int RT>
-__global__ __launch_bounds__(64 * kFewWaves, RT == 1 ? 3 : 2) void attn_few_kernel(const AttnArgs a) {
+__global__ __launch_bounds__(64 * kFewWaves, RT == 1 && D / F::kPerByte < 128 ? 3 : 2) void attn_few_kernel(const AttnArgs a) {
     constexpr int Q = D / 4, E = D / 32, FT = D / 16, DW = Q / F::kPerByte / 4, TB = kStep * D * 2;
     __shared__ __attribute__((aligned(256))) unsigned char lds[kFewWaves][TB];
     const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
