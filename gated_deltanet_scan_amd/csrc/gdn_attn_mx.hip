@@ -77,7 +77,12 @@ __global__ __launch_bounds__(64 * kFewWaves, RT == 1 && D / F::kPerByte < 128 ? 
     const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // key heads run fastest: the waves of a workgroup read neighbouring rows of the same keys
-    const unsigned unit = blockIdx.x * kFewWaves + wave;
+    // Workgroups go to the eight XCDs in turn.  Short sequences use their first chunks
+    // alone, which would meet the same XCDs every time: each eight are rotated (64 requests
+    // with room for 16 chunks, all but one of 300 keys: 41 us against 63).
+    const unsigned eight = blockIdx.x / 8;
+    const unsigned wg = 8 * eight + 8 <= gridDim.x ? 8 * eight + ((blockIdx.x + (eight * 0x9E3779B1u >> 29)) & 7) : blockIdx.x;
+    const unsigned unit = wg * kFewWaves + wave;
     const int hk = (int)(unit % (unsigned)a.Hk), rest = (int)(unit / (unsigned)a.Hk);
     const int split = rest % a.splits, sq = rest / a.splits;
     if (sq >= a.n_seq) return;
@@ -384,20 +389,24 @@ gdn_status attn_fwd_mx(const AttnArgs& a, bool fp4, int rows, Grid g, hipStream_
 }
 
 // Keys of a chunk: for about 8192 waves if every sequence were as long as it may be
-// (three fit a SIMD, 3072 the card; lengths differ, and short work spreads evenly).  Eight
-// single queries of 40 to 32768 keys, 8 key heads of 128, so 256 keys a chunk: 28.6 us in
-// both kernels, with 128 keys 34.7, with 512 39.8.  Where more than a row tile shares
-// them, 256 at least, since a chunk's fp32 results grow with the rows: 8 requests of 4
-// queries and 8192 keys, 8 heads on each of 4: 23.9 us against 30.1.
+// (three fit a SIMD, a little over 3000 the card; lengths differ, and short work spreads
+// evenly).  Eight single queries of 40 to 32768 keys, 8 key heads of 128, so 256 keys a
+// chunk: 28.6 us in both kernels, with 128 keys 34.7, with 512 39.8.  Past 2048 a quarter,
+// so that the longest of many requests is no long tail: one of 32768 keys beside 255 of
+// 40 71 us against 204 with 8192, 256 of 8192 keys 555 against 560.  Where more than a row
+// tile shares them, 256 at least, since a chunk's fp32 results grow with the rows: 8
+// requests of 4 queries and 8192 keys, 8 heads on each of 4: 23.9 us against 30.1.
 int attn_few_chunk(int rows, int n_seq, int Hk, int D, int max_k) {
-    const int64_t keys = ((int64_t)max_k * n_seq * Hk + 8191) / 8192;
+    const int64_t all = std::min((int64_t)max_k * n_seq, (int64_t)1 << 45) * Hk;      // Hk is below 2^16
+    const int64_t even = (all + 8191) / 8192, keys = std::max(std::min<int64_t>(even, 2048), even / 4);
     // a chunk and the steps behind it within 32-bit offsets
     const int64_t most = ((int64_t)1 << 31) / ((int64_t)Hk * D) - 4 * kStep;
     const int64_t chunk = std::min(std::max<int64_t>(keys, rows > 16 ? 256 : 128), most);
     return (int)std::min<int64_t>((chunk + 2 * kStep - 1) / (2 * kStep) * (2 * kStep), std::max(max_k, 1));
 }
 bool attn_few_grids(const AttnArgs& a, FewGrids* g) {
-    const int64_t units = (int64_t)a.n_seq * a.splits * a.Hk;
+    if ((int64_t)a.n_seq * a.Hk >= INT32_MAX) return false;
+    const int64_t units = (int64_t)a.n_seq * a.Hk * a.splits;
     if (!grid_of((units + kFewWaves - 1) / kFewWaves, 64 * kFewWaves, &g->main)) return false;
     return units < INT32_MAX && grid_of((int64_t)a.n_seq * a.max_q * a.Hq, 256, &g->join);
 }
