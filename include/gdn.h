@@ -593,7 +593,7 @@ gdn_status gdn_cache_read(const gdn_cache_desc* d, const void* k_codes, const ui
  * 8-bit matrix instruction, which adds them eight at a time with at least 13 bits
  * below the largest of the eight (Gaussian operands: 1.4e-5 of the result, a
  * hundredth of its rounding to bfloat16); what they give is scaled and added in
- * float32.  K a multiple of 16, N and K at most 2^20, M below 2^31
+ * float32.  K a multiple of 16, N and K at most 2^20, M below 2^31, M N about 2^44
  * (GDN_ERR_UNSUPPORTED).  x, w and y are 16-byte aligned, scales 4-byte.
  *
  * All are bitwise reproducible; outputs are disjoint from the inputs and from each

@@ -94,7 +94,7 @@ def matmul(lib, d, **over):
 @pytest.mark.parametrize("d,expect", [
     (None, INVALID), (mm(M=-1), INVALID), (mm(N=0), INVALID), (mm(K=0), INVALID), (mm(parts=0), INVALID),
     (mm(parts=5), INVALID), (mm(K=40), UNSUPPORTED), (mm(K=(1 << 20) + 16), UNSUPPORTED),
-    (mm(N=(1 << 20) + 1), UNSUPPORTED), (mm(M=1 << 31), UNSUPPORTED),
+    (mm(N=(1 << 20) + 1), UNSUPPORTED), (mm(M=1 << 31), UNSUPPORTED), (mm(M=(1 << 31) - 1, N=1 << 20, K=16), UNSUPPORTED),
 ])
 def test_matmul_descriptor(lib, d, expect):
     assert matmul(lib, d) == expect
@@ -164,6 +164,15 @@ def test_cache_pointers(lib):
 
 
 # ------------------------------------------------------------------ attention
+def test_workspace_of_loose_bounds(lib):
+    """Many packed sequences whose lengths have no bound but the tensor's: chunks are a quarter of an even share of
+    8192 at least, or as long as their offsets allow (2^31 bytes of codes, less four steps)."""
+    for n, tk, Hq, Hk in ((1, 10 ** 9, 32, 8), (3000, 10 ** 7, 32, 8), (8, 2 ** 30, 128, 4), (100000, 10 ** 8, 8, 8)):
+        d = _lib.GdnAttnDesc(n, tk, 0, 0, 0, 0, n, Hq, Hk, 128, 1, tk, 1, FP4, 1, 0.1)
+        splits = 1 + max(4 * 8192 // (n * Hk), tk // (2 ** 31 // (Hk * 128) - 192))
+        assert 0 <= lib.gdn_attn_workspace_size(ref(d)) <= splits * n * Hq * (128 + 1) * 4 + 512, (n, tk)
+
+
 def attn(tq=8, tk=8, qs=0, ks=0, vs=0, room=0, n=2, Hq=4, Hk=2, D=64, mq=4, mk=4, block=1, io=FP4, flags=0, scale=0.1):
     return _lib.GdnAttnDesc(tq, tk, qs, ks, vs, room, n, Hq, Hk, D, mq, mk, block, io, flags, scale)
 
