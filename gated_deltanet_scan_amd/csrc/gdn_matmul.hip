@@ -46,7 +46,9 @@ __device__ __forceinline__ int64_t uniform(int64_t x) {
 }
 
 // ---------------------------------------------------------------- tiles
-constexpr unsigned kTileRows = 8;             // rows of tiles that an XCD walks together
+// Rows of tiles that an XCD walks together: 1220 us for 106480 x 6144, K = 2048, as with
+// four; with two 1252, with sixteen 1249.
+constexpr unsigned kTileRows = 8;
 
 // Memory to LDS, 16 or 4 bytes a lane, one run of a wave's lanes at `to` (a
 // wave-uniform LDS address); places past the descriptor's end are written as zeros.
@@ -85,7 +87,7 @@ constexpr uint32_t kNowhere = 0x80000000u;    // past the end of every descripto
 // next block's first ones are read beside those products.  Sums stand two products
 // behind, so a wave waits for none of them.
 //
-// Bound by power: 106480 x 6144, K = 2048, takes 1.25 to 1.30 ms, 2050 to 2150
+// Bound by power: 106480 x 6144, K = 2048, takes 1.19 to 1.30 ms, 2050 to 2250
 // TFLOP/s.  Its 2.36 million cycles (1.28 of them of matrix instructions on every SIMD)
 // pass at 1.9 GHz, with operands of zeros at 2.4; a library product with one scale for
 // everything takes 1.00 ms on the same card.  Of the cycles 0.3 million are the ends of
