@@ -871,10 +871,12 @@ def _fp8_out(x, y, y_scale):
         raise TypeError("x must be a torch.Tensor")
     if x.dim() < 1:
         raise ValueError("x must be [..., C]")
-    _check(x, "x", x.dtype, x.shape)
-    scales = x.shape[:-1] + (-(-x.shape[-1] // FP8_GROUP),)
+    if not (x.is_cuda and x.is_contiguous()):
+        _check(x, "x", x.dtype, x.shape)
+    shape = x.shape
+    scales = shape[:-1] + (-(-shape[-1] // FP8_GROUP),)
     if y is not None:
-        _check(y, "y", torch.float8_e4m3fn, x.shape)
+        _check(y, "y", torch.float8_e4m3fn, shape)
     if y_scale is not None:
         _check(y_scale, "y_scale", torch.float32, scales)
     return scales
@@ -903,7 +905,7 @@ def rms_norm_fwd_fp8(x, weight=None, residual=None, *, eps: float = 1e-6, y=None
     where, handle = _launch(stream, x.device)
     with where:   # allocations belong to the launch stream
         if y is None:
-            y = x.new_empty(x.shape, dtype=torch.float8_e4m3fn)
+            y = torch.empty_like(x, dtype=torch.float8_e4m3fn)
         if y_scale is None:
             y_scale = x.new_empty(scales, dtype=torch.float32)
         if total is None and residual is not None:
@@ -924,7 +926,7 @@ def quantize_fp8(x, *, y=None, y_scale=None, stream=None):
     where, handle = _launch(stream, x.device)
     with where:   # allocations belong to the launch stream
         if y is None:
-            y = x.new_empty(x.shape, dtype=torch.float8_e4m3fn)
+            y = torch.empty_like(x, dtype=torch.float8_e4m3fn)
         if y_scale is None:
             y_scale = x.new_empty(scales, dtype=torch.float32)
         st = _lib.load().gdn_quantize_fp8(ctypes.byref(desc), _ptr(x), _ptr(y), _ptr(y_scale), handle)
