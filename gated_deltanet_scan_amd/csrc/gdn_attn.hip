@@ -588,7 +588,12 @@ int fwd_rows(const gdn_attn_desc* d) {
 // its work spread evenly would take about 92.  A decode step (a few rows a key
 // head) is cut eight times finer, because the lengths of its caches differ and
 // short work spreads evenly; a split's fp32 partial result is then small
-// against its keys, of which it takes 512 at least (128 at the fp32 rate).
+// against its keys, of which it takes 512 at least (128 at the fp32 rate).  Over
+// block-scaled keys 256 or 128 where no more than one workgroup a unit comes of
+// it, since a short walk is a chain of steps: 64 queries, 2000 keys, 4 heads of
+// 128 13.0 us against 14.7 with 256 and 19.4 with 512; with more workgroups it
+// costs (4 requests of 100 and 1500, 8 heads: 384 of 128 keys 25.9 us, 192 of 256
+// 21.7, 96 of 512 23.9).
 int fwd_chunk(const gdn_attn_desc* d) {
     if (few(d)) return attn_few_chunk(d->max_q * (d->Hq / d->Hk), d->n_seq, d->Hk, d->D, d->max_k);
     const int64_t rows = (int64_t)d->max_q * (d->Hq / d->Hk);
@@ -597,7 +602,10 @@ int fwd_chunk(const gdn_attn_desc* d) {
     int64_t n = (fwd_rows(d) == 256 ? 256 : 512) / std::max<int64_t>(units, 1);
     if (rows <= 32) n *= 8;
     if (n < 2) return std::max(d->max_k, 1);
-    const int64_t chunk = std::max<int64_t>(((d->max_k + n - 1) / n + 63) / 64 * 64, fast(d) ? 512 : 128);
+    int64_t least = fast(d) ? 512 : 128;
+    if (block_scaled(d))
+        while (least > 128 && (d->max_k + least / 2 - 1) / (least / 2) * units <= 256) least /= 2;
+    const int64_t chunk = std::max<int64_t>(((d->max_k + n - 1) / n + 63) / 64 * 64, least);
     return (int)std::min<int64_t>(chunk, std::max(d->max_k, 1));
 }
 int fwd_splits(const gdn_attn_desc* d) {
