@@ -509,7 +509,8 @@ def _same_device(x, **tensors):
 
 
 _HERE = contextlib.nullcontext()
-_current_device = torch.cuda.current_device
+# the tensors at hand have initialised the device layer, so its own check of that is left out
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 # the current stream's handle without a Stream object around it, where torch has it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -1065,8 +1066,10 @@ def cache_write(k, v, k_cache, k_scale, v_cache, v_scale, *, k_len=None, cu_new=
             raise TypeError("%s must be a torch.Tensor" % name)
         if not t.is_cuda:
             raise ValueError("%s must be a device tensor (got %s)" % (name, t.device))
-    if not 3 <= k.dim() <= 5 or v.shape != k.shape or k.shape[-2:] != (H, D):
-        raise ValueError("k and v must be [..., %d, %d], alike (got %s, %s)" % (H, D, tuple(k.shape), tuple(v.shape)))
+    shape = k.shape
+    dims = len(shape)
+    if not 3 <= dims <= 5 or v.shape != shape or shape[-2:] != (H, D):
+        raise ValueError("k and v must be [..., %d, %d], alike (got %s, %s)" % (H, D, tuple(shape), tuple(v.shape)))
     if v.dtype != k.dtype:
         raise TypeError("v must be %s (got %s)" % (k.dtype, v.dtype))
     io = _io(k.dtype, "k and v")
@@ -1075,9 +1078,9 @@ def cache_write(k, v, k_cache, k_scale, v_cache, v_scale, *, k_len=None, cu_new=
         (ldk, rk), (ldv, rv) = _token_strides(k, "k"), _token_strides(v, "v")
         if rk or rv:
             raise ValueError("k and v must have packed heads and evenly spaced tokens")
-    if (k.dim() == 3) != (len(lead) == 1):
+    if (dims == 3) != (len(lead) == 1):
         raise ValueError("packed k [T, H, D] go with a packed cache")
-    if k.dim() == 3:
+    if dims == 3:
         if cu_new is None:
             raise ValueError("packed k [T, H, D] needs cu_new")
         cu_k = cu_new if cu_k is None else cu_k
@@ -1086,16 +1089,16 @@ def cache_write(k, v, k_cache, k_scale, v_cache, v_scale, *, k_len=None, cu_new=
             raise ValueError("cu_new must hold n_seq + 1 offsets")
         _check(cu_new, "cu_new", torch.int32, (n_seq + 1,))
         _check(cu_k, "cu_k", torch.int32, (n_seq + 1,))
-        tn, tk = k.shape[0], lead[0]
+        tn, tk = shape[0], lead[0]
         max_new = tn if max_new is None else min(int(max_new), tn)
         max_k = tk if max_k is None else min(int(max_k), tk)
     else:
         if cu_new is not None or cu_k is not None or max_new is not None or max_k is not None:
             raise ValueError("cu_new, cu_k, max_new and max_k belong to packed k [T, H, D]")
-        n_seq = k.shape[0]
+        n_seq = shape[0]
         if lead[0] != n_seq:
             raise ValueError("k and the cache must have the same batch size")
-        max_new, max_k = k.shape[1:-2].numel(), lead[1:].numel()
+        max_new, max_k = shape[1:-2].numel(), lead[1:].numel()
         tn, tk = n_seq * max_new, n_seq * max_k
     if k_len is not None:
         _check(k_len, "k_len", torch.int32, (n_seq,))
@@ -1104,8 +1107,9 @@ def cache_write(k, v, k_cache, k_scale, v_cache, v_scale, *, k_len=None, cu_new=
                              _lib.GDN_FP4_E2M1 if fp4 else _lib.GDN_FP8_E4M3)
     where, handle = _launch(stream, k.device)
     with where:
-        st = _lib.load().gdn_cache_write(ctypes.byref(desc), _ptr(k), _ptr(v), _ptr(cu_new), _ptr(cu_k), _ptr(k_len),
-                                         _ptr(k_cache), _ptr(k_scale), _ptr(v_cache), _ptr(v_scale), handle)
+        st = _lib.load().gdn_cache_write(ctypes.byref(desc), k.data_ptr(), v.data_ptr(), _ptr(cu_new), _ptr(cu_k),
+                                         _ptr(k_len), k_cache.data_ptr(), k_scale.data_ptr(), v_cache.data_ptr(),
+                                         v_scale.data_ptr(), handle)
     if st != 0:
         raise GdnError(st, "gdn_cache_write")
 
@@ -1161,14 +1165,16 @@ def _attention_mx(fp4, q, k, k_scale, v, v_scale, causal, causal_block, scale, c
         raise ValueError("q must be a device tensor (got %s)" % q.device)
     if q.dtype != torch.bfloat16:
         raise TypeError("q must be %s (got %s)" % (torch.bfloat16, q.dtype))
-    if not 3 <= q.dim() <= 5 or q.shape[-1] != D or (q.dim() == 3) != (len(lead) == 1):
+    shape = q.shape
+    dims = len(shape)
+    if not 3 <= dims <= 5 or shape[-1] != D or (dims == 3) != (len(lead) == 1):
         raise ValueError("q must be [B, L, H, %d] or [B, F, N, H, %d], or packed [T, H, %d] over a packed cache (got %s)"
-                         % (D, D, D, tuple(q.shape)))
-    Hq = q.shape[-2]
+                         % (D, D, D, tuple(shape)))
+    Hq = shape[-2]
     ldq, rq = (0, 0) if q.is_contiguous() else _token_strides(q, "q")
     if rq:
         raise ValueError("q must have packed heads and evenly spaced tokens")
-    if q.dim() == 3:
+    if dims == 3:
         if cu_q is None:
             raise ValueError("packed q [T, H, D] needs cu_q")
         cu_k = cu_q if cu_k is None else cu_k
@@ -1177,43 +1183,46 @@ def _attention_mx(fp4, q, k, k_scale, v, v_scale, causal, causal_block, scale, c
             raise ValueError("cu_q must hold n_seq + 1 offsets")
         _check(cu_q, "cu_q", torch.int32, (n_seq + 1,))
         _check(cu_k, "cu_k", torch.int32, (n_seq + 1,))
-        tq, tk = q.shape[0], lead[0]
+        tq, tk = shape[0], lead[0]
         max_q = tq if max_q is None else min(int(max_q), tq)
         max_k = tk if max_k is None else min(int(max_k), tk)
     else:
         if cu_q is not None or cu_k is not None or max_q is not None or max_k is not None:
             raise ValueError("cu_q, cu_k, max_q and max_k belong to packed q [T, H, D]")
-        n_seq = q.shape[0]
+        n_seq = shape[0]
         if lead[0] != n_seq:
             raise ValueError("q and the cache must have the same batch size")
-        max_q, max_k = q.shape[1:-2].numel(), lead[1:].numel()
+        max_q, max_k = shape[1:-2].numel(), lead[1:].numel()
         tq, tk = n_seq * max_q, n_seq * max_k
     if causal_block is None:
-        causal_block = q.shape[2] if q.dim() == 5 else 1
+        causal_block = shape[2] if dims == 5 else 1
     if k_len is not None:
         _check(k_len, "k_len", torch.int32, (n_seq,))
     if o is not None:
-        _check(o, "o", q.dtype, q.shape)
+        _check(o, "o", q.dtype, shape)
     if lse is not None:
-        _check(lse, "lse", torch.float32, q.shape[:-1])
-    _check_workspace(workspace, q.device)
+        _check(lse, "lse", torch.float32, shape[:-1])
+    device = q.device
+    if workspace is not None:
+        _check_workspace(workspace, device)
     _same_device(q, k=k, cu_q=cu_q, cu_k=cu_k, k_len=k_len, o=o, lse=lse)
     desc = _lib.GdnAttnDesc(tq, tk, ldq, 0, 0, room, n_seq, Hq, Hk, D, max_q, max_k, min(int(causal_block), 2 ** 31 - 1),
                             _lib.GDN_FP4_E2M1 if fp4 else _lib.GDN_FP8_E4M3,
                             _lib.GDN_FLAG_ATTN_CAUSAL if causal else 0, D ** -0.5 if scale is None else scale)
     lib = _lib.load()
     fn = lib.gdn_attn_fwd_fp4 if fp4 else lib.gdn_attn_fwd_fp8
-    where, handle = _launch(stream, q.device)
+    where, handle = _launch(stream, device)
     with where:   # allocations belong to the launch stream
         if o is None:
-            o = q.new_empty(q.shape)
+            o = q.new_empty(shape)
         if lse is None and return_lse:
-            lse = q.new_empty(q.shape[:-1], dtype=torch.float32)
+            lse = q.new_empty(shape[:-1], dtype=torch.float32)
         if workspace is None:
             need = lib.gdn_attn_workspace_size(ctypes.byref(desc))
             workspace = q.new_empty(need, dtype=torch.uint8) if need else None
-        st = fn(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(k_scale), _ptr(v), _ptr(v_scale), _ptr(cu_q), _ptr(cu_k),
-                _ptr(k_len), _ptr(o), _ptr(lse), _ptr(workspace), _ws_bytes(workspace), handle)
+        st = fn(ctypes.byref(desc), q.data_ptr(), k.data_ptr(), k_scale.data_ptr(), v.data_ptr(), v_scale.data_ptr(),
+                _ptr(cu_q), _ptr(cu_k), _ptr(k_len), o.data_ptr(), _ptr(lse), _ptr(workspace), _ws_bytes(workspace),
+                handle)
     if st != 0:
         raise GdnError(st, "gdn_attn_fwd_fp4" if fp4 else "gdn_attn_fwd_fp8")
     return o, lse

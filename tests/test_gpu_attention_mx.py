@@ -124,6 +124,31 @@ def test_cache_filled_in_part(lq, G, Hk, D, fp4):
 
 
 @FORMATS
+@pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
+@pytest.mark.parametrize("lq,block,G,Hk,D", [(6, 3, 2, 3, 64), (7, 4, 4, 2, 128), (16, 16, 2, 1, 32), (9, 2, 1, 8, 128),
+                                             (60, 7, 2, 2, 64)])
+def test_blocks_over_a_part_of_the_cache(lq, block, G, Hk, D, causal, fp4):
+    """Drafts of several blocks, and full attention, over caches whose places behind their length are NaN: lengths
+    that end inside a step, at its end, short of the queries, and of several splits."""
+    lens_k = [lq, 64, 0, 1500, 3, 2049, 96]
+    room, B = 2100, 7
+    q = rand((B, lq, G * Hk, D), 1).to(BF).cuda()
+    kc, ks, kv = encode(rand((B, room, Hk, D), 2), fp4)
+    vc, vs, vv = encode(rand((B, room, Hk, D), 3), fp4)
+    for b, n in enumerate(lens_k):
+        ks[b, n:] = 255
+        vs[b, n:] = 255
+        vc.view(torch.uint8)[b, n:] = 255
+    n = torch.tensor(lens_k, dtype=torch.int32, device="cuda")
+    o, lse = fwd(fp4)(q, kc, ks, vc, vs, causal=causal, causal_block=block, k_len=n)
+    for b, lk in enumerate(lens_k):
+        x = host(q[b])
+        val, bar = dense(x, kv[b, :lk], vv[b, :lk], np.zeros_like(x), causal, block, D ** -0.5, BF)
+        check(host(o[b]), val["o"], bar["o"], "o[%d]" % b)
+        check(host(lse[b]), val["lse"], bar["lse"], "lse[%d]" % b)
+
+
+@FORMATS
 @pytest.mark.parametrize("lk,Hq,Hk,D", [(40001, 4, 1, 32), (33000, 16, 1, 128), (17000, 2, 2, 64)])
 def test_many_splits(lk, Hq, Hk, D, fp4):
     """One request against a long cache: hundreds of splits to a row."""
