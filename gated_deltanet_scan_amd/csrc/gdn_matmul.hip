@@ -298,6 +298,8 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void matmul_kernel(const MatmulArg
             }
         }
     }
+    // the loads behind the last tile (of nothing, zeros) still write this workgroup's LDS
+    wait_loads<0>();
 }
 
 // ---------------------------------------------------------------- few tokens

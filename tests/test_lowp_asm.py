@@ -85,3 +85,13 @@ def test_tiles_wait_where_they_say(products):
         assert text.count("v_mfma") == len(re.findall(r"v_mfma_f32_16x16x128_f8f6f4", text))
         seen += 1
     assert seen == 4
+
+
+def test_tiles_end_with_no_load_under_way(products):
+    """Loads to LDS run ahead past the last tile; a workgroup's LDS is another's once it ends."""
+    tiles = {n: b for n, b in products.items() if "few" not in n}
+    assert len(tiles) == 4
+    for name, body in tiles.items():
+        end = body[:body.rindex("s_endpgm")]
+        lines = [t for t in (x.strip() for x in end.splitlines()) if t and not t.startswith((";", ".LBB"))]
+        assert lines[-1] == "s_waitcnt vmcnt(0)", (name, lines[-3:])
