@@ -77,7 +77,9 @@ def test_product(shape, spread):
                                    (5, 6144, 2048), (31, 8192, 2048), (64, 2048, 8192), (300, 512, 8192),
                                    # every kernel with several tiles to a workgroup, rows of one block and of less
                                    (66000, 512, 128), (70001, 264, 48), (9000, 2048, 144), (33, 40000, 16),
-                                   (520, 16384, 128), (1000, 9000, 272)])
+                                   (520, 16384, 128), (1000, 9000, 272),
+                                   # many tokens and few columns: rows of workgroups of the kernels for few tokens
+                                   (1777, 48, 1040), (4001, 16, 400), (100, 1000, 272), (201, 500, 2048)])
 def test_large_products(M, N, K):
     """Against 64 bits on the card; the bound of the whole, and every element within 40 roundings of the typical
     value's: 8 bits of sum|p| 2^-13 7 / 8 are far below."""
