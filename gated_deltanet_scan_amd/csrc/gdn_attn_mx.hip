@@ -397,14 +397,17 @@ gdn_status attn_fwd_mx(const AttnArgs& a, bool fp4, int rows, Grid g, hipStream_
 // chunk: 28.6 us in both kernels, with 128 keys 34.7, with 512 39.8.  Past 2048 a quarter,
 // so that the longest of many requests is no long tail: one of 32768 keys beside 255 of
 // 40 71 us against 204 with 8192, 256 of 8192 keys 555 against 560.  Where more than a row
-// tile shares them, 256 at least, since a chunk's fp32 results grow with the rows: 8
-// requests of 4 queries and 8192 keys, 8 heads on each of 4: 23.9 us against 30.1.
+// tile shares them, 256 at least and up to 512 from 1024 waves on, since a chunk's fp32
+// results grow with the rows: 8 requests of 4 queries and 8192 keys, 8 heads on each of 4,
+// with 256 keys 24.5 us, with 128 30, with 512 28.6; 8 queries, 4 heads on each of 8, with
+// 512 32.8 and with 256 35.5; 64 requests of 700 keys 52 with 384, 59 with 256.
 int attn_few_chunk(int rows, int n_seq, int Hk, int D, int max_k) {
     const int64_t all = std::min((int64_t)max_k * n_seq, (int64_t)1 << 45) * Hk;      // Hk is below 2^16
     const int64_t even = (all + 8191) / 8192, keys = std::max(std::min<int64_t>(even, 2048), even / 4);
     // a chunk and the steps behind it within 32-bit offsets
     const int64_t most = ((int64_t)1 << 31) / ((int64_t)Hk * D) - 4 * kStep;
-    const int64_t chunk = std::min(std::max<int64_t>(keys, rows > 16 ? 256 : 128), most);
+    const int64_t least = rows > 16 ? std::min<int64_t>(std::max<int64_t>((all + 1023) / 1024, 256), 512) : 128;
+    const int64_t chunk = std::min(std::max(keys, least), most);
     return (int)std::min<int64_t>((chunk + 2 * kStep - 1) / (2 * kStep) * (2 * kStep), std::max(max_k, 1));
 }
 bool attn_few_grids(const AttnArgs& a, FewGrids* g) {
