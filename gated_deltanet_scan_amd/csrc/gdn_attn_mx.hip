@@ -394,19 +394,24 @@ gdn_status attn_fwd_mx(const AttnArgs& a, bool fp4, int rows, Grid g, hipStream_
 // Keys of a chunk: for about 8192 waves if every sequence were as long as it may be
 // (three fit a SIMD, a little over 3000 the card; lengths differ, and short work spreads
 // evenly).  Eight single queries of 40 to 32768 keys, 8 key heads of 128, so 256 keys a
-// chunk: 28.6 us in both kernels, with 128 keys 34.7, with 512 39.8.  Past 2048 a quarter,
-// so that the longest of many requests is no long tail: one of 32768 keys beside 255 of
-// 40 71 us against 204 with 8192, 256 of 8192 keys 555 against 560.  Where more than a row
-// tile shares them, 256 at least and up to 512 from 1024 waves on, since a chunk's fp32
-// results grow with the rows: 8 requests of 4 queries and 8192 keys, 8 heads on each of 4,
-// with 256 keys 24.5 us, with 128 30, with 512 28.6; 8 queries, 4 heads on each of 8, with
-// 512 32.8 and with 256 35.5; 64 requests of 700 keys 52 with 384, 59 with 256.
+// chunk: 28.3 us in both kernels, with 128 keys 34.7, with 512 38.9.
+//   - Past 2048 a quarter, so that the longest of many requests is no long tail: one of
+//     32768 keys beside 255 of 40 71 us against 204 with 8192, 256 of 8192 keys 555
+//     against 560.
+//   - 128 at least, and up to 256 where so many waves are left (32 of 2048 keys 23.3 us
+//     against 26.6 with 128; 4 of 1500 keys 11.3 with 128, 13.6 with 256) or where the
+//     join would take more than 128 splits, its one step (one of 20000 13.7 against 16.4).
+//   - More than 16 rows: 256 at least, and up to 512 where there are many, since a chunk's
+//     fp32 results grow with the rows: 8 requests of 8 queries and 40 to 32768 keys, 4
+//     heads on each of 8, 43.0 us against 53.2; 4 queries, 8 heads on each of 4, 31.9 with
+//     256 and 38.7 with 512.
 int attn_few_chunk(int rows, int n_seq, int Hk, int D, int max_k) {
     const int64_t all = std::min((int64_t)max_k * n_seq, (int64_t)1 << 45) * Hk;      // Hk is below 2^16
     const int64_t even = (all + 8191) / 8192, keys = std::max(std::min<int64_t>(even, 2048), even / 4);
     // a chunk and the steps behind it within 32-bit offsets
     const int64_t most = ((int64_t)1 << 31) / ((int64_t)Hk * D) - 4 * kStep;
-    const int64_t least = rows > 16 ? std::min<int64_t>(std::max<int64_t>((all + 1023) / 1024, 256), 512) : 128;
+    const int64_t least = rows > 16 ? std::min<int64_t>(std::max<int64_t>(all / 4096 * D / 128, 256), 512)
+                                    : std::min<int64_t>(std::max<int64_t>({(all + 2047) / 2048, (max_k + 127) / 128, 128}), 256);
     const int64_t chunk = std::min(std::max(keys, least), most);
     return (int)std::min<int64_t>((chunk + 2 * kStep - 1) / (2 * kStep) * (2 * kStep), std::max(max_k, 1));
 }
