@@ -1002,8 +1002,9 @@ def _packed_tokens(t, name):
         return 0
     ld, room = _token_strides(t, name)
     row = t.shape[-2] * t.shape[-1]
-    if ld != row and t.shape[1:-2].numel() == 1 and ld % row == 0:
-        return ld // row                      # slots of one place
+    # slots of one place, their step the token stride (packed [T, H, X] has no slots: its tokens must be packed)
+    if ld != row and t.dim() > 3 and t.shape[1:-2].numel() == 1 and ld % row == 0:
+        return ld // row
     if ld != row:
         raise ValueError("%s must have packed tokens" % name)
     return room

@@ -556,7 +556,8 @@ gdn_status gdn_attn_fwd_fp4(const gdn_attn_desc* d, const void* q, const void* k
 typedef struct gdn_cache_desc {
     int64_t total_new, total_k;            /* new tokens; places of the caches   */
     int64_t k_stride, v_stride;            /* elements between new tokens, 0: packed */
-    int64_t k_room;                        /* cu_k NULL: places from one slot to the next, 0: max_k */
+    int64_t k_room;                        /* cu_k NULL: places from one slot to the next, 0: max_k
+                                              (with cu_k unused; 0 or at least max_k all the same) */
     int32_t n_seq, H, D;
     int32_t max_new, max_k;                /* bounds of the new tokens and of the slots */
     int32_t io_dtype, cache_dtype;         /* of k and v; GDN_FP8_E4M3 or GDN_FP4_E2M1 */

@@ -227,3 +227,24 @@ def test_refusals():
         api.cache_write(k[0], k[0], *c, cu_new=torch.zeros(1, dtype=torch.int32, device="cuda"))
     with pytest.raises(ValueError, match="evenly"):
         api.cache_write(k.transpose(1, 2), k.transpose(1, 2), *api.cache_empty(2, 8, H=3, D=64, fp4=True))
+
+
+@FORMATS
+def test_layers_side_by_side_are_refused(fp4):
+    """One layer of a packed [T, layers, H, X] cache, with bounds that its tokens' distance passes: nothing is
+    written or read."""
+    T, layers, H, D = 12, 8, 2, 64
+    whole = filled((T, layers), H, D, fp4)
+    before = raw(whole)
+    one = [t[:, 3] for t in whole]
+    cu = torch.tensor([0, 4, 12], dtype=torch.int32, device="cuda")
+    new = make((T, H, D), BF, 1).cuda()
+    fwd = api.attention_fwd_fp4 if fp4 else api.attention_fwd_fp8
+    with pytest.raises(ValueError, match="packed tokens"):
+        api.cache_write(new, new, *one, cu_new=cu, max_new=8, max_k=8)
+    with pytest.raises(ValueError, match="packed tokens"):
+        api.cache_read(*one, cu_k=cu, max_k=8)
+    with pytest.raises(ValueError, match="packed tokens"):
+        fwd(new, *one, cu_q=cu, max_q=8, max_k=8)
+    for a, b in zip(raw(whole), before):
+        assert torch.equal(a, b)

@@ -268,6 +268,25 @@ def test_packed_tokens_of_a_cache():
     assert api._packed_tokens(s[:, :4], "k_scale") == 10
 
 
+@pytest.mark.parametrize("name,tensor", [
+    ("one of 32 layers", torch.zeros(16, 32, 2, 64, dtype=torch.uint8)[:, 3]),
+    ("k beside v", torch.zeros(16, 2, 2, 32, dtype=torch.uint8)[:, 0]),
+    ("every fourth token", torch.zeros(64, 2, 32, dtype=torch.uint8)[::4]),
+    ("scales of one byte a row", torch.zeros(16, 4, 1, 1, dtype=torch.uint8)[:, 1]),
+], ids=lambda x: x if isinstance(x, str) else "")
+def test_tokens_of_a_packed_cache_lie_side_by_side(name, tensor):
+    """[T, H, X] has no slots: tokens further apart than a row are no cache."""
+    with pytest.raises(ValueError, match="packed tokens"):
+        api._packed_tokens(tensor, "k")
+
+
+def test_slots_of_one_place():
+    """[B, 1, H, X] and [B, 1, 1, H, X] of longer slots, and packed tokens from the middle of a tensor, are caches."""
+    c = torch.zeros(3, 10, 2, 32, dtype=torch.uint8)
+    assert api._packed_tokens(c[:, 4:5], "k") == 10 and api._packed_tokens(c[:, 4:5, None], "k") == 10
+    assert api._packed_tokens(c[1], "k") == 0 and api._packed_tokens(c[1, 3:7], "k") == 0
+
+
 def test_weight_encoder():
     """The recipe: block maxima become +-448, values are within half a step."""
     r = np.random.default_rng(0)
