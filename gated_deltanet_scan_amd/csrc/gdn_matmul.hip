@@ -12,6 +12,7 @@
 // which needs one scale of x, and its store is four values wide.  One instruction
 // contracts exactly one scale's block; its result starts from zero and is added to
 // the fp32 sum with the block's scale.
+#include "gdn_matmul_rule.hpp"
 #include "gdn_ops.hpp"
 
 #include <algorithm>
@@ -19,6 +20,7 @@
 namespace {
 
 using namespace gdnops;
+using namespace gdnmatmul;
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
@@ -394,32 +396,6 @@ gdn_status run_few(MatmulArgs a, hipStream_t s) {
     return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
-// Which kernel, in tenths of a microsecond at K = 2048 (and in proportion at others).
-// Few tokens: what a workgroup takes, and more as a compute unit gets several.  100
-// tokens, N = 512: 4.5 us with 16 tokens to a workgroup, 5.9 with 32, 8.8 in tiles; 100 and
-// N = 1000: 6.8, 6.0, 9.1; 64 and N = 2048: 6.8, 6.0, 9.0; 64 and N = 6144: 15.8, 13.1,
-// 8.9; 200 and N = 1000: 10.8, 9.6, 9.2 (K = 8192: 36, 31, 25).
-// Tiles: the fewest rounds of the card times what a round takes: 128 x 64 two a unit
-// 14 us, one a unit 9.6; 128 x 128 13.2; 256 x 128 20; 256 x 256 32.  So 880 x 2048 takes
-// 10.0 us in the first where the others take 12.5, 16.7 and 26; 880 x 6144 18.8 in the
-// third (21.4, 22.5, -, 27.9); 7040 x 2048 32 in the last (42, 42, 35).
-enum Kind { kFew16, kFew32, k128x64, k128x128, k256x128, k256x256 };
-Kind choose(const MatmulArgs& a, int cus) {
-    if (a.M <= 16) return kFew16;
-    auto share = [&](int m) { return std::max(1.0, (double)((a.N + 15) / 16) * ((a.M + m - 1) / m) / cus); };
-    const double few16 = 23 + 23 * share(16), few32 = 18 + 41 * share(32);
-    if (std::min(few16, few32) < 85) return few16 < few32 ? kFew16 : kFew32;
-    auto tiles = [&](int n, int m) { return ((a.N + n - 1) / n) * ((a.M + m - 1) / m); };
-    auto rounds = [&](int64_t t, int at_once) { return (t + at_once - 1) / at_once; };
-    const int64_t t = tiles(128, 64);
-    const int64_t cost[] = {t <= cus ? 96 : 140 * rounds(t, 2 * cus), 132 * rounds(tiles(128, 128), cus),
-                            200 * rounds(tiles(256, 128), cus), 320 * rounds(tiles(256, 256), cus)};
-    int best = 0;
-    for (int i = 1; i < 4; ++i)
-        if (cost[i] < cost[best]) best = i;
-    return (Kind)(k128x64 + best);
-}
-
 }  // namespace
 
 extern "C" gdn_status gdn_matmul_fp8(const gdn_matmul_desc* d, const void* x, const float* x_scale, const void* w,
@@ -445,7 +421,7 @@ extern "C" gdn_status gdn_matmul_fp8(const gdn_matmul_desc* d, const void* x, co
     a.y = static_cast<uint16_t*>(y);
     a.M = d->M, a.N = d->N, a.K = d->K, a.kb = kb, a.part = d->N / d->parts;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    switch (choose(a, cus)) {
+    switch (choose(a.M, a.N, cus)) {
         case kFew16: return run_few<1>(a, s);
         case kFew32: return run_few<2>(a, s);
         case k128x64: return run_tiles<128, 64, 2, 2, 3>(a, 2 * cus, s);
