@@ -1056,9 +1056,11 @@ def cache_write(k, v, k_cache, k_scale, v_cache, v_scale, *, k_len=None, cu_new=
     k, v: [B, n, H, D] (or [B, F, N, H, D], or packed [T, H, D] with cu_new), bf16 or
     fp32, heads packed and tokens evenly apart; the cache [B, L, H, ...] (or a slice
     k_cache[:, :n] of longer slots, or packed with cu_k, default cu_new).  The new
-    tokens become the last of their sequence's k_len[s] positions (int32 [n_seq];
-    None: all L), as the queries of attention_fwd_fp4 and _fp8 with the same k_len
-    lie; tokens that fall outside the slot are dropped.
+    tokens become the last of their sequence's k_len[s] positions (int32 [n_seq], the
+    new tokens counted; None: all L).  The queries of attention_fwd_fp4 and _fp8 with
+    the same k_len lie at the same positions while k_len[s] <= L.  Tokens that fall
+    outside the slot are dropped without a word (lengths stay on the device), and
+    attention then takes a k_len[s] past L as L: check lengths where they are made.
     """
     fp4 = _is_fp4(k_cache)
     lead, H, D, room = _cache_args(k_cache, k_scale, v_cache, v_scale, fp4)

@@ -535,9 +535,16 @@ gdn_status gdn_attn_fwd_fp4(const gdn_attn_desc* d, const void* q, const void* k
  * cu_new[s] .. cu_new[s+1]-1 (cu_new NULL: max_new each), which are the last of its
  * k_len[s] positions: token i of n goes to place k_len[s] - n + i
  * of the slot cu_k[s] .. cu_k[s+1]-1 (cu_k NULL: max_k places from s k_room on, 0
- * = max_k), as the queries of an attention call lie.  k_len NULL: the slot's last
- * places.  Tokens whose place lies outside the slot are dropped; places that get
- * no token keep what they hold.  No two sequences may share a place.
+ * = max_k).  k_len NULL: the slot's last places.  Tokens whose place lies outside
+ * the slot are dropped; places that get no token keep what they hold.  No two
+ * sequences may share a place.
+ * The queries of an attention call with the same lengths lie at the same positions
+ * as long as k_len[s] is no more than the slot's size (or max_k, where that is
+ * less).  Past it attention has the keys that there are, and takes its queries as
+ * the last of those: it reads such a k_len[s] as the slot's size, while this call
+ * drops the tokens that find no room, so a causal mask then hides tokens that were
+ * kept from their own queries.  k_len counts the new tokens: 0 for a first token
+ * drops it.
  *
  * For 32 consecutive features of largest magnitude m the scale byte is e + 127,
  * e = floor(log2 m) - 8 (E4M3) or - 2 (E2M1), at least -127 and 0 where m is 0; a

@@ -267,3 +267,27 @@ def test_two_streams_and_repeats(lq, fp4):
         torch.cuda.synchronize()
         for a, b in zip(got, ref):
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@FORMATS
+@pytest.mark.parametrize("lq,block", [(4, 1), (4, 4), (40, 1)])
+def test_lengths_past_the_slot(lq, block, fp4):
+    """Tokens written and queried with the same lengths.  Within the slot a query lies where its token does; a length
+    past it is the slot's size to attention, while tokens that find no room are dropped."""
+    B, L, H, D = 4, 70, 2, 64
+    n = [lq, L - 1, L, L + 3]
+    old, new = rand((B, L, H, D), 1).to(BF), rand((B, lq, H, D), 2).to(BF)
+    q = rand((B, lq, 2 * H, D), 3).to(BF).cuda()
+    cache = api.cache_empty(B, L, H=H, D=D, fp4=fp4)
+    api.cache_write(old.cuda(), old.cuda(), *cache)
+    k_len = torch.tensor(n, dtype=torch.int32, device="cuda")
+    api.cache_write(new.cuda(), new.cuda(), *cache, k_len=k_len)
+    o, lse = fwd(fp4)(q, *cache, causal=True, causal_block=block, k_len=k_len)
+    for b, m in enumerate(n):
+        held = old[b].clone()
+        room = min(lq, L - (m - lq))
+        held[m - lq:m - lq + room] = new[b, :room]
+        x, lk = encode(held.float(), fp4)[2], min(m, L)
+        val, bar = dense(host(q[b]), x[:lk], x[:lk], np.zeros((lq, 2 * H, D)), True, block, D ** -0.5, BF)
+        check(host(o[b]), val["o"], bar["o"], "o[%d]" % b)
+        check(host(lse[b]), val["lse"], bar["lse"], "lse[%d]" % b)
