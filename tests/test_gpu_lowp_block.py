@@ -6,6 +6,8 @@ the 8-bit output projection.
 Tolerance.  The same chain in float64 over the same codes: every stage's own input is
 taken from the GPU, so a stage's error is its own rounding.
 """
+import os
+
 import numpy as np
 import pytest
 import torch
@@ -127,3 +129,35 @@ def test_tokens_captured_and_replayed(fp4):
             assert torch.equal(got, e), i
     for a, b in zip(cache, want):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_the_documented_block():
+    """README's low-precision block as it stands, three frames: what the cache holds, the attention over all of it,
+    and the output projection (an identity here)."""
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    code = [line[4:] for line in text[text.index("    cache = api.cache_empty"):].split("\nA frame of")[0].splitlines()]
+    once, each = "\n".join(code[:code.index("")]), "\n".join(code[code.index(""):])
+    B, N, W, F = 2, 880, 2048, 3
+    g = torch.Generator().manual_seed(5)
+    w = torch.randn((3 * W, W), generator=g) * W ** -0.5
+    (w_qkv, w_qkv_s), (w_out, w_out_s) = inputs.to_fp8_weight(w.cuda()), inputs.to_fp8_weight(torch.eye(W).cuda())
+    names = dict(api=api, B=B, N=N, room=F * N + 5, w_qkv=w_qkv, w_qkv_s=w_qkv_s, w_out=w_out, w_out_s=w_out_s,
+                 w_norm=torch.ones(W, device="cuda"), y=torch.randn((B, N, W), generator=g).to(BF).cuda(),
+                 x=torch.zeros((B, N, W), dtype=BF, device="cuda"))
+    exec(once, names)
+    for f in range(F):
+        names.update(f=f, n=torch.full((B,), (f + 1) * N, dtype=torch.int32, device="cuda"))
+        exec(each, names)
+        k, v = (t[:, :(f + 1) * N] for t in api.cache_read(*names["cache"], dtype=torch.float32, k_len=names["n"]))
+        want = inputs.to_mxfp4(names["k"].float().cpu().numpy())[2]
+        assert np.array_equal(k[:, f * N:].cpu().numpy(), want)
+        ref, _ = api.attention_fwd(names["q"], k.to(BF), v.to(BF), causal=True, causal_block=N)
+        o = names["o"]
+        assert (o.double() - ref.double()).norm() <= 2 * 2.5e-3 * ref.double().norm()      # each is 2.5e-3 from 64 bits
+        y = names["y"]
+        # the output projection is the identity: what is left is the 8-bit rounding of o (half a step of 2^-3, and a
+        # group's smallest values to 2^-10 of its largest)
+        assert y.shape == (B, N, W) and names["x"].shape == (B, N, W)
+        og = o.flatten(-2).float()
+        top = og.abs().unflatten(-1, (-1, 128)).amax(-1, keepdim=True).expand(-1, -1, -1, 128).flatten(-2)
+        assert torch.all((y.float() - og).abs() <= (2.0 ** -4 + 2.0 ** -8) * 1.01 * og.abs() + 2.0 ** -18 * 1.01 * top)
