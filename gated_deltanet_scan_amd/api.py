@@ -892,7 +892,9 @@ def rms_norm_fwd_fp8(x, weight=None, residual=None, *, eps: float = 1e-6, y=None
     like x, or None.  Returns (y, y_scale, total): y float8_e4m3fn like x, y_scale
     [..., ceil(C / 128)] fp32, one for each group of 128 columns (a value is its code
     times its scale), and total = t in x's dtype (None without a residual), which may
-    be given as x or residual itself.
+    be given as x or residual itself.  Any C will do here; matmul_fp8 takes multiples of
+    16.  Forward only, as all of this section: the outputs carry no gradient, whatever
+    the inputs ask for.
     """
     scales = _fp8_out(x, y, y_scale)
     desc = _norm_desc(x, weight, None, eps)
@@ -920,7 +922,7 @@ def rms_norm_fwd_fp8(x, weight=None, residual=None, *, eps: float = 1e-6, y=None
 
 def quantize_fp8(x, *, y=None, y_scale=None, stream=None):
     """x [..., C] (bf16 or fp32) in 8 bits with a scale for each group of 128
-    columns, as rms_norm_fwd_fp8 gives its output: (y, y_scale)."""
+    columns, as rms_norm_fwd_fp8 gives its output: (y, y_scale), without a gradient."""
     scales = _fp8_out(x, y, y_scale)
     desc = _norm_desc(x, None, None, 1.0)
     _same_device(x, y=y, y_scale=y_scale)
@@ -943,6 +945,7 @@ def matmul_fp8(x, x_scale, w, w_scale, *, parts: int = 1, y=None, stream=None):
     (rms_norm_fwd_fp8, quantize_fp8); w: [N, K] float8_e4m3fn, output-major, with
     w_scale [ceil(N / 128), ceil(K / 128)] fp32 (inputs.to_fp8_weight); K a multiple
     of 16.  Returns y [..., N] bf16, or with parts > 1 [parts, ..., N / parts].
+    Forward only: y carries no gradient.
     """
     for name, t in (("x", x), ("w", w)):
         if not isinstance(t, torch.Tensor):
@@ -1121,7 +1124,8 @@ def cache_read(k_cache, k_scale, v_cache, v_scale, *, dtype: torch.dtype = torch
                max_k=None, k=None, v=None, stream=None):
     """The values that a cache holds: (k, v) [..., H, D] in dtype (bf16 or fp32),
     contiguous.  Only the first k_len[s] places of each slot (None: all) are written;
-    the others of k and v are left as they are.  Slots as for cache_write."""
+    the others of k and v are left as they are (unset, where they are not given).
+    Slots as for cache_write."""
     fp4 = _is_fp4(k_cache)
     lead, H, D, room = _cache_args(k_cache, k_scale, v_cache, v_scale, fp4)
     dtype = k.dtype if k is not None else v.dtype if v is not None else dtype
@@ -1239,7 +1243,13 @@ def attention_fwd_fp4(q, k, k_scale, v, v_scale, *, causal: bool = False, causal
     q: bf16 [B, L, Hq, D], [B, F, N, Hq, D] or packed [T, Hq, D]; k, v: uint8
     [B, Lk, Hk, D/2] (two E2M1 codes a byte) with k_scale, v_scale uint8
     [B, Lk, Hk, D/32], or packed; tokens packed, slices k[:, :n] of longer slots will
-    do.  D in {32, 64, 128}.  The rest as for attention_fwd; forward only.
+    do.  D in {32, 64, 128}.  The rest as for attention_fwd; forward only, no gradient.
+
+    Kernel and splits of the keys are chosen by the bounds of the call alone, so give
+    packed calls max_q and max_k: max_q Hq / Hk <= 32 takes the kernel for few rows and
+    splits the keys finely, without max_q that is all tokens.  A long prompt and single
+    tokens on long caches are better two calls (eight single queries on caches of 40 to
+    32768 keys, 32 / 8 heads: 31 us alone, 541 in one call with a prompt of 512).
     """
     return _attention_mx(True, q, k, k_scale, v, v_scale, causal, causal_block, scale, cu_q, cu_k, max_q, max_k, k_len,
                          o, lse, return_lse, workspace, stream)

@@ -517,7 +517,9 @@ gdn_status gdn_attn_bwd(const gdn_attn_desc* d, const void* q, const void* k, co
  * aligned; scales need no alignment.  Workspace: gdn_attn_workspace_size of the
  * same descriptor.  Codes widen to bf16 exactly, so the results differ from
  * gdn_attn_fwd's on bf16 tensors of the dequantised values only by the order of
- * sums. */
+ * sums.  Up to 32 rows of a key head (max_q Hq / Hk) take a kernel of their own;
+ * that choice and the splits of the keys go by max_q and max_k, not by the lengths
+ * on the device. */
 gdn_status gdn_attn_fwd_fp8(const gdn_attn_desc* d, const void* q, const void* k, const uint8_t* k_scale,
                             const void* v, const uint8_t* v_scale,
                             const int32_t* cu_q, const int32_t* cu_k, const int32_t* k_len,
@@ -590,8 +592,9 @@ gdn_status gdn_cache_read(const gdn_cache_desc* d, const void* k_codes, const ui
  * m = max(max |y|, 2^-100) over a group, y_scale [rows][ceil(C/128)] = m / 448 and
  * the codes y [rows][C] are y (448 / m) rounded to nearest.  gdn_quantize_fp8
  * gives x itself so (its w_dtype and eps are unused).  A NaN reads as NaN, and so
- * does the group of an infinity.  Sums are float32.  rows >= 0, 1 <= C <= 2^20;
- * pointers need only their element's alignment.
+ * does the group of an infinity.  Sums are float32: a row whose squares add up past
+ * its largest number (a root of that sum past 1.8e19) gives zeros.  rows >= 0, 1 <=
+ * C <= 2^20; pointers need only their element's alignment.
  *
  * gdn_matmul_fp8:  y[m][n] = sum_k x[m][k] w[n][k] on the values
  *     x [M][K] codes, x_scale [M][ceil(K/128)],
@@ -601,7 +604,8 @@ gdn_status gdn_cache_read(const gdn_cache_desc* d, const void* k_codes, const ui
  * 8-bit matrix instruction, which adds them eight at a time with at least 13 bits
  * below the largest of the eight (Gaussian operands: 1.4e-5 of the result, a
  * hundredth of its rounding to bfloat16); what they give is scaled and added in
- * float32.  K a multiple of 16, N and K at most 2^20, M below 2^31, M N about 2^44
+ * float32, x_scale w_scale first, a product that has to be a normal float32 number
+ * (or 0) to count in full.  K a multiple of 16, N and K at most 2^20, M below 2^31, M N about 2^44
  * (GDN_ERR_UNSUPPORTED).  x, w and y are 16-byte aligned, scales 4-byte.
  *
  * All are bitwise reproducible; outputs are disjoint from the inputs and from each
