@@ -3,8 +3,10 @@
 // rows.  More rows take the forward kernel of bf16 keys (gdn_attn_tile.hpp), which
 // widens codes to bf16 as it stages them, once for a row tile of up to 256.  It is bound
 // by the matrix and vector instructions of two waves a SIMD, as with bf16 keys: 880
-// queries against 19360 keys in MXFP4, 16 heads of 128, 147 us and 9 for the join, whole
-// calls 156 (175 from bf16 caches, of 3.8 times the bytes).
+// queries against 19360 keys, 16 heads of 128, 154 to 162 us a call in MXFP4; traced, 160
+// to 163 and 9 for the join, in MXFP8 154 to 156 and 9, from bf16 caches (of 3.8 times the
+// bytes) 159 to 161 and 8.  A prompt of 18480 tokens on its own cache, frame-causal: 1.41
+// to 1.48 ms in all three.
 //
 // Few rows (single tokens, drafts; at most 32 of a key head): a wave takes one key head and a
 // chunk of keys, in steps of 32.  v_mfma_f32_16x16x32_bf16: lane l = 16 g + r holds
@@ -71,8 +73,9 @@ __device__ __forceinline__ float quarters_sum(float x) {
 // which 64 widen codes, in two or three waves a SIMD (with every load taken out the same
 // steps take 80% of the time); a load of four bytes a lane for each tile's scales costs
 // as much to issue as one of codes, so a step's scales come in one load.  MXFP8 heads of
-// 128 are bound by memory, 8 x 11008 keys in 41.5 us (1.1 of the floor) with two waves a
-// SIMD; three spill (46.9).
+// 128 are bound by memory: 8 x 11008 keys (186 MB) in 41.5 us a call with two waves a
+// SIMD (three spill, 46.9), traced 34 to 35 and 4.5 for the join.  8 x 8192 keys, four
+// queries each: 21 and 8 in MXFP4, 29 and 8 in MXFP8.
 template <typename F, int D, int RT>
 __global__ __launch_bounds__(64 * kFewWaves, RT == 1 && D / F::kPerByte < 128 ? 3 : 2) void attn_few_kernel(const AttnArgs a) {
     constexpr int Q = D / 4, E = D / 32, FT = D / 16, DW = Q / F::kPerByte / 4, TB = kStep * D * 2;

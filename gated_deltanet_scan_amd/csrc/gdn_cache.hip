@@ -10,9 +10,10 @@
 //
 // Bound by memory.  Four lanes hold a block, eight features each, so a block's
 // maximum is two exchanges within a quad, and a lane's codes are one store.  16 heads of
-// 128, bf16, both caches: 106480 tokens are written in 223 us (MXFP4) and 271 (MXFP8)
-// and read in 221 and 266, 4.9 to 5.0 TB/s; 880 tokens in 3.6 to 4.0; eight in 2.4 to
-// 2.6, a launch.
+// 128, bf16, both caches: 106480 tokens are written in 223 to 229 us (MXFP4) and 265 to 271
+// (MXFP8) and read in 221 to 226 and 265 to 266, 4.8 to 5.0 TB/s; 880 tokens in 3.6 to 4.3;
+// eight in 2.4 to 3.0, a launch.  From fp32 412 and 446 (4.8 and 4.9 TB/s), to fp32 563
+// and 610 (3.5 and 3.6).
 #include "gdn_attn.hpp"
 #include "gdn_mx.hpp"
 

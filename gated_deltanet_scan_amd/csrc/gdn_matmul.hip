@@ -89,11 +89,12 @@ constexpr uint32_t kNowhere = 0x80000000u;    // past the end of every descripto
 // next block's first ones are read beside those products.  Sums stand two products
 // behind, so a wave waits for none of them.
 //
-// Bound by power: 106480 x 6144, K = 2048, takes 1.19 to 1.30 ms, 2050 to 2250
-// TFLOP/s.  Its 2.36 million cycles (1.28 of them of matrix instructions on every SIMD)
-// pass at 1.9 GHz, with operands of zeros at 2.4; a library product with one scale for
-// everything takes 1.00 ms on the same card.  Of the cycles 0.3 million are the ends of
-// tiles.
+// Bound by power: 106480 x 6144, K = 2048, takes 1.19 to 1.56 ms from card to card and
+// launch to launch, 2250 to 1720 TFLOP/s (calls in a row 1.24 to 1.34, traced launches
+// 1.28 to 1.43).  Its 2.36 million cycles (1.28 of them of matrix instructions on every
+// SIMD) pass at 1.5 to 2.0 GHz, with operands of zeros at 2.4; a library product with one
+// scale for everything takes 1.00 ms on the faster cards.  Of the cycles 0.3 million are
+// the ends of tiles.
 template <int TN, int TM, int WN, int WM, int S>
 __global__ __launch_bounds__(64 * WN * WM, 2) void matmul_kernel(const MatmulArgs a) {
     constexpr int WAVES = WN * WM, FN = TN / WN, FM = TM / WM, NI = FN / 16, NT = FM / 16;
@@ -309,7 +310,8 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void matmul_kernel(const MatmulArg
 // block, operands straight from memory (each byte of w is read once for its tokens),
 // and add their sums in order through LDS.  Bound by memory where w is large (one token,
 // N = K = 8192: 13.5 us, 5.0 TB/s) and by a launch and two trips to memory where not (7
-// tokens, N = 6144, K = 2048: 5.4 us; two trips' worth of blocks at once, 6.5).
+// tokens, N = 6144, K = 2048: 5.4 to 6.0 us; two trips' worth of blocks at once, 6.5
+// beside 5.4).
 constexpr int kFewWaves = 8;
 template <int T>
 __global__ __launch_bounds__(64 * kFewWaves) void matmul_few_kernel(const MatmulArgs a) {

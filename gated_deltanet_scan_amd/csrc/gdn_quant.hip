@@ -93,8 +93,9 @@ __device__ __forceinline__ void quantise8(const float* f, uint8_t* row, float* s
 // Rows of up to 512 NV WPR columns, WPR waves to a row; lane t of a row holds
 // the columns 8 (t + 64 WPR i) and the seven after them.  A row stays in registers
 // between its norm and its codes, and the next row's loads run meanwhile.  106480 rows
-// of 2048 bf16 columns with residual and sum: 290 us, 5.3 TB/s, what a copy reaches; 880
-// rows: 4.3 us, a launch and two trips to memory.
+// of 2048 bf16 columns with residual and sum: 290 to 300 us, 5.3 to 5.1 TB/s, what a copy
+// reaches (fp32 540 to 543, 5.2 TB/s); 880 rows: 4.3 to 4.6 us, a launch and two trips to
+// memory.
 template <typename T, typename W, int NV, int WPR>
 __global__ __launch_bounds__(kThreads) void rms_quant_kernel(const QuantArgs a) {
     __shared__ float red[2][kWaves];
@@ -203,7 +204,8 @@ __global__ __launch_bounds__(kThreads) void rms_quant_wide_kernel(const QuantArg
 }
 
 // Quantisation alone: 16 lanes a group, groups in their order.  106480 rows of 2048
-// bf16 columns: 132 us, 5.0 TB/s; 880 rows: 2.9 us.
+// bf16 columns: 132 to 136 us, 5.0 to 4.8 TB/s (fp32 224 to 228, 4.9 to 4.8); 880 rows: 2.9
+// to 4.0 us.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void quantise_kernel(const QuantArgs a) {
     const int64_t all = a.rows * a.groups, step = (int64_t)gridDim.x * (kThreads / kLanes);
