@@ -422,7 +422,8 @@ bool attn_few_grids(const AttnArgs& a, FewGrids* g) {
     if ((int64_t)a.n_seq * a.Hk >= INT32_MAX) return false;
     const int64_t units = (int64_t)a.n_seq * a.Hk * a.splits;
     if (!grid_of((units + kFewWaves - 1) / kFewWaves, 64 * kFewWaves, &g->main)) return false;
-    return units < INT32_MAX && grid_of((int64_t)a.n_seq * a.max_q * a.Hq, 256, &g->join);
+    g->join = 0;
+    return units < INT32_MAX && (a.splits == 1 || grid_of((int64_t)a.n_seq * a.max_q * a.Hq, 256, &g->join));
 }
 gdn_status attn_fwd_few(const AttnArgs& a, bool fp4, FewGrids g, hipStream_t s) {
     return fp4 ? few_by_size<gdnmx::Fp4>(a, g, s) : few_by_size<gdnmx::Fp8>(a, g, s);

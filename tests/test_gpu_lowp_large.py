@@ -118,3 +118,21 @@ def test_no_keys(lq, fp4):
     assert o.shape == (0, lq, 4, 64)
     o, lse = fwd(fp4)(q[:, :0], *api.cache_empty(2, 3, H=2, D=64, fp4=fp4))
     assert o.shape == (2, 0, 4, 64)
+
+
+@FORMATS
+def test_more_rows_than_a_join_takes(fp4):
+    """70000 requests with room for 32 queries each, on 8 heads: more (row, head) places than one launch of the join
+    may have, which short keys do not need."""
+    n, H, D, most = 70000, 8, 32, 32
+    r = np.random.default_rng(9)
+    lens_q, lens_k = (r.random(n) < 0.01).astype(np.int64), r.choice([0, 0, 0, 0, 1, 3], n)
+    lens_q[[5, n - 1]], lens_k[[5, n - 1]] = most, 60
+    cu_q, cu_k = starts(lens_q), starts(lens_k)
+    q = rand((int(cu_q[-1]), H, D), 1).to(BF).cuda()
+    kc, ks, kv = encode(rand((int(cu_k[-1]), H, D), 2), fp4)
+    vc, vs, vv = encode(rand((int(cu_k[-1]), H, D), 3), fp4)
+    o, lse = fwd(fp4)(q, kc, ks, vc, vs, causal=True, cu_q=torch.from_numpy(cu_q).cuda(),
+                      cu_k=torch.from_numpy(cu_k).cuda(), max_q=most, max_k=60)
+    some = np.flatnonzero(lens_q)
+    compare(q, kv, vv, cu_q[some], cu_k[some], lens_q[some], lens_k[some], True, 1, D ** -0.5, o, lse)
